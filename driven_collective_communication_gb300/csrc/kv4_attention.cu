@@ -1,0 +1,80 @@
+// kv4_attention.cu -- host side of the attention over the 4-bit cache.
+#include "comm.h"
+#include "kv4_attention.cuh"
+
+namespace dcc {
+template <typename T>
+static const void* attention_kernel_of(int dim, int group) {
+  if (dim == 128) return group == 64 ? (const void*)&k_kv4_attention<T, 128, 64> : (const void*)&k_kv4_attention<T, 128, 32>;
+  return group == 64 ? (const void*)&k_kv4_attention<T, 64, 64> : (const void*)&k_kv4_attention<T, 64, 32>;
+}
+const void* kv4_attention_kernel(bool fp16, int dim, int group) {
+  return fp16 ? attention_kernel_of<__half>(dim, group) : attention_kernel_of<__nv_bfloat16>(dim, group);
+}
+}  // namespace dcc
+
+extern "C" {
+
+int dcc_kv4_attention_workspace(const dcc_kv4_t* kv, int q_heads, size_t* bytes) {
+  if (!kv || !bytes || q_heads < 1 || kv->kv_heads < 1 || q_heads % kv->kv_heads) return DCC_ERR_INVALID_ARG;
+  *bytes = 16;
+  return DCC_OK;
+}
+
+int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* const* out, float* const* lse, int q_heads,
+                      size_t tokens, size_t q_stride, const int32_t* start, int max_new, float scale, int window,
+                      void* workspace, size_t workspace_bytes, dcc_stream_t s) {
+  dcc::Kv4Dev d{};
+  int rc = dcc_host::kv4_view(kv, false, &d);
+  if (rc != DCC_OK) return rc;
+  if (!q || !out || !start || !workspace || layer < 0 || layer >= kv->layers || q_heads < 1 || max_new < 1 ||
+      window < 0 || !(scale - scale == 0.0f))
+    return DCC_ERR_INVALID_ARG;
+  if (q_heads % kv->kv_heads || q_heads / kv->kv_heads > 128) return DCC_ERR_INVALID_ARG;
+  size_t need = 0;
+  rc = dcc_kv4_attention_workspace(kv, q_heads, &need);
+  if (rc != DCC_OK) return rc;
+  if (workspace_bytes < need) return DCC_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(start) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 15u) || q_stride % 8)
+    return DCC_ERR_MISALIGNED;
+  const size_t width = (size_t)q_heads * kv->head_dim;
+  if (tokens > (size_t)1 << 26 || q_stride > (size_t)1 << 32 || (tokens > 1 && q_stride < width))
+    return DCC_ERR_INVALID_ARG;
+  if (tokens == 0) return DCC_OK;
+  const size_t qb = ((tokens - 1) * q_stride + width) * 2, ob = tokens * width * 2, lb = tokens * q_heads * 4;
+  const size_t pool = (size_t)kv->layers * kv->pages * kv->kv_heads * dcc::kv4_block_bytes(kv->head_dim, kv->group);
+  dcc::AttnArgs a{};
+  for (int r = 0; r < kv->n_ranks; ++r) {
+    if (!q[r] || !out[r] || (lse && !lse[r])) return DCC_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(q[r]) | reinterpret_cast<uintptr_t>(out[r])) & 15u) return DCC_ERR_MISALIGNED;
+    if (lse && (reinterpret_cast<uintptr_t>(lse[r]) & 3u)) return DCC_ERR_MISALIGNED;
+    for (int p = 0; p < kv->n_ranks; ++p) {
+      if (dcc_host::overlaps(out[r], ob, q[p], qb) || dcc_host::overlaps(out[r], ob, kv->pool[p], pool) ||
+          (p < r && dcc_host::overlaps(out[r], ob, out[p], ob)))
+        return DCC_ERR_INVALID_ARG;
+      if (lse && (dcc_host::overlaps(lse[r], lb, q[p], qb) || dcc_host::overlaps(lse[r], lb, kv->pool[p], pool) ||
+                  dcc_host::overlaps(lse[r], lb, out[p], ob) || (p < r && dcc_host::overlaps(lse[r], lb, lse[p], lb))))
+        return DCC_ERR_INVALID_ARG;
+    }
+    a.q[r] = q[r];
+    a.out[r] = out[r];
+    a.lse[r] = lse ? lse[r] : nullptr;
+  }
+  a.start = start;
+  a.q_stride = q_stride;
+  a.tokens = (int)tokens;
+  a.layer = layer;
+  a.q_heads = q_heads;
+  a.max_new = max_new;
+  a.window = window;
+  a.scale = scale;
+  const long long items = (long long)tokens * q_heads * kv->n_ranks;
+  const long long grid = (items + dcc::kAttnThreads / 32 - 1) / (dcc::kAttnThreads / 32);
+  if (grid > 0x7fffffffll) return DCC_ERR_INVALID_ARG;
+  if ((rc = dcc_host::kv4_ready(&d)) != DCC_OK) return rc;
+  void* args[] = {&d, &a};
+  return dcc_host::launch(dcc::kv4_attention_kernel(kv->dtype == DCC_FP16, kv->head_dim, kv->group), (int)grid,
+                          dcc::kAttnThreads, false, args, static_cast<cudaStream_t>(s), 0, true);
+}
+
+}  // extern "C"

@@ -1,0 +1,109 @@
+// ops_status.cu -- what the calls without a communicator share on the host:
+// the status word their kernels record failures in, and the checks of a cache
+// descriptor.
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "kv4.cuh"
+
+namespace {
+// one word per device; its address comes from cudaGetSymbolAddress
+static __device__ unsigned long long g_local_status;
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+unsigned long long* g_addr[kMaxDevices];
+}  // namespace
+
+namespace dcc_host {
+
+unsigned long long* local_status() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!g_addr[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_local_status) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    g_addr[dev] = static_cast<unsigned long long*>(p);
+  }
+  return g_addr[dev];
+}
+
+int kv4_view(const dcc_kv4_t* kv, bool need_refs, dcc::Kv4Dev* out) {
+  if (!kv || !kv->pool || !kv->table || !kv->len || (need_refs && !kv->refs)) return DCC_ERR_INVALID_ARG;
+  if (kv->n_ranks < 1 || kv->n_ranks > DCC_MAX_RANKS || kv->layers < 1 || kv->pages < 1 || kv->seqs < 1 ||
+      kv->max_pages < 1 || kv->kv_heads < 1)
+    return DCC_ERR_INVALID_ARG;
+  // positions and page numbers are 32-bit; pool offsets are not
+  if (kv->max_pages > (1 << 24) || kv->pages > (1 << 28) || kv->seqs > (1 << 20) || kv->kv_heads > (1 << 12) ||
+      kv->layers > (1 << 12))
+    return DCC_ERR_INVALID_ARG;
+  if (kv->dtype != DCC_FP16 && kv->dtype != DCC_BF16) return DCC_ERR_UNSUPPORTED;
+  if ((kv->head_dim != 64 && kv->head_dim != 128) || (kv->group != 32 && kv->group != 64)) return DCC_ERR_UNSUPPORTED;
+  if (((reinterpret_cast<uintptr_t>(kv->table) | reinterpret_cast<uintptr_t>(kv->len) |
+        reinterpret_cast<uintptr_t>(kv->refs)) & 3u))
+    return DCC_ERR_MISALIGNED;
+  const size_t bytes = (size_t)kv->layers * kv->pages * kv->kv_heads * dcc::kv4_block_bytes(kv->head_dim, kv->group);
+  for (int r = 0; r < kv->n_ranks; ++r) {
+    const char* p = static_cast<const char*>(kv->pool[r]);
+    if (!p) return DCC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return DCC_ERR_MISALIGNED;
+    for (int q = 0; q < r; ++q) {
+      const char* o = static_cast<const char*>(kv->pool[q]);
+      if (p < o + bytes && o < p + bytes) return DCC_ERR_INVALID_ARG;  // two ranks' pools overlap
+    }
+    out->pool[r] = const_cast<char*>(p);
+  }
+  out->table = kv->table;
+  out->len = kv->len;
+  out->refs = kv->refs;
+  out->n = kv->n_ranks;
+  out->layers = kv->layers;
+  out->pages = kv->pages;
+  out->seqs = kv->seqs;
+  out->max_pages = kv->max_pages;
+  out->heads = kv->kv_heads;
+  out->status = nullptr;  // kv4_ready
+  return DCC_OK;
+}
+
+int kv4_ready(dcc::Kv4Dev* d) {
+  d->status = local_status();
+  return d->status ? DCC_OK : DCC_ERR_CUDA;
+}
+
+}  // namespace dcc_host
+
+extern "C" {
+
+int dcc_kv4_block_bytes(int head_dim, int group, size_t* bytes) {
+  if (!bytes) return DCC_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128) || (group != 32 && group != 64)) return DCC_ERR_UNSUPPORTED;
+  *bytes = (size_t)dcc::kv4_block_bytes(head_dim, group);
+  return DCC_OK;
+}
+
+int dcc_local_check(dcc_stream_t s) {
+  unsigned long long* p = dcc_host::local_status();
+  if (!p) return DCC_ERR_CUDA;
+  unsigned long long st = 0;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(s)) != cudaSuccess ||
+      cudaMemcpy(&st, p, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) {
+    cudaGetLastError();
+    return DCC_ERR_CUDA;
+  }
+  if (st == 0) return DCC_OK;
+  if (cudaMemset(p, 0, sizeof st) != cudaSuccess) {
+    cudaGetLastError();
+    return DCC_ERR_CUDA;
+  }
+  return (st & 0xffull) == dcc::kStatusTimeout ? DCC_ERR_TIMEOUT : DCC_ERR_BOUNDS;
+}
+
+}  // extern "C"

@@ -55,6 +55,8 @@ OP_CODES = {"sum": DCC_OP_SUM, "max": DCC_OP_MAX, "min": DCC_OP_MIN}
 ALGO_CODES = {"auto": DCC_ALGO_AUTO, "one_shot": DCC_ALGO_ONE_SHOT, "two_shot": DCC_ALGO_TWO_SHOT,
               "two_shot_scratch": DCC_ALGO_TWO_SHOT_SCRATCH, "two_shot_bulk": DCC_ALGO_TWO_SHOT_BULK,
               "one_shot_ll": DCC_ALGO_ONE_SHOT_LL}
+DCC_KV4_PAGE = 64
+ACT_CODES = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 KIND_CODES = {"input": DCC_BUF_INPUT, "output": DCC_BUF_OUTPUT, "scratch": DCC_BUF_SCRATCH}
 
 # ------------------------------------------------------------------ signatures
@@ -63,6 +65,18 @@ _sz = ctypes.c_size_t
 _i = ctypes.c_int
 _u64 = ctypes.c_uint64
 _PP = ctypes.POINTER(ctypes.c_void_p)
+
+_f32 = ctypes.c_float
+
+
+class dcc_kv4_t(ctypes.Structure):
+    """Descriptor of a 4-bit cache (see dcc.h)."""
+    _fields_ = [("pool", _PP), ("table", _vp), ("len", _vp), ("refs", _vp)] + [
+        (name, _i) for name in ("n_ranks", "layers", "pages", "seqs", "max_pages", "kv_heads", "head_dim", "group",
+                                "dtype")]
+
+
+_KV = ctypes.POINTER(dcc_kv4_t)
 
 _SIGS = {
     "dcc_comm_create": [_i, ctypes.POINTER(_vp)],
@@ -106,6 +120,19 @@ _SIGS = {
     "dcc_linear_allreduce_residual": [_vp, _PP, _PP, _PP, _PP, _sz, _sz, _i, _vp],
     "dcc_linear_allreduce_tokens": [_vp, _PP, _PP, _PP, _sz, _sz, _sz, _i, _vp],
     "dcc_linear_allreduce_tokens_residual": [_vp, _PP, _PP, _PP, _PP, _sz, _sz, _sz, _i, _vp],
+    "dcc_kv4_block_bytes": [_i, _i, ctypes.POINTER(_sz)],
+    "dcc_kv4_append": [_KV, _i, _PP, _PP, _sz, _sz, _vp, _vp],
+    "dcc_kv4_read": [_KV, _i, _PP, _PP, _sz, _sz, _vp, _vp],
+    "dcc_kv4_attention": [_KV, _i, _PP, _PP, _PP, _i, _sz, _sz, _vp, _i, _f32, _i, _vp, _sz, _vp],
+    "dcc_kv4_attention_workspace": [_KV, _i, ctypes.POINTER(_sz)],
+    "dcc_kv4_pages_workspace": [_KV, ctypes.POINTER(_sz)],
+    "dcc_kv4_reserve": [_KV, _vp, _vp, _vp, _sz, _vp],
+    "dcc_kv4_free": [_KV, _vp, _sz, _vp, _vp, _sz, _vp],
+    "dcc_kv4_fork": [_KV, _vp, _vp, _sz, _vp, _vp, _sz, _vp],
+    "dcc_kv4_copy": [_KV, _vp, _vp, _sz, _vp],
+    "dcc_kv4_compact": [_KV, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "dcc_linear": [_i, _PP, _PP, _PP, _PP, _PP, _sz, _sz, _sz, _i, _i, _vp],
+    "dcc_local_check": [_vp],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -424,6 +451,170 @@ def dcc_fifo_push(comm, fst, snd=None, stream=None):
     return _check(_lib.dcc_fifo_push(comm, f, s, n, _stream(stream)), "dcc_fifo_push")
 
 
+class Ranks:
+    """One tensor per rank, all of one shape, type and row stride, with their
+    device pointers marshalled once (a serving loop passes the same buffers
+    every step).  Rows may be strided (a slice of a fused projection); the rest
+    of each row is dense."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        t = self.tensors[0]
+        for o in self.tensors:
+            if (o.shape, o.dtype, o.stride()) != (t.shape, t.dtype, t.stride()):
+                raise ValueError("the ranks' tensors differ in shape, type or strides")
+            if not o.is_cuda:
+                raise ValueError("the ranks' tensors are on a CUDA device")
+        self.shape, self.dtype = tuple(t.shape), t.dtype
+        dense = 1
+        for size, step in list(zip(t.shape, t.stride()))[:0:-1]:
+            if size > 1 and step != dense:
+                raise ValueError("a row of the tensors is not dense")
+            dense *= size
+        # elements between rows; a single row has none to skip
+        self.stride = t.stride(0) if t.dim() > 1 and t.shape[0] > 1 else dense
+        self.dense = self.stride == dense
+        self.ptrs = _ptrs(self.tensors)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _ranks(x):
+    return x if x is None or isinstance(x, Ranks) else Ranks(x)
+
+
+def _index(t, n, what):
+    """Device pointer of a contiguous int32 tensor of at least n elements."""
+    if t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda or t.numel() < n:
+        raise ValueError("%s: a contiguous int32 CUDA tensor of at least %d elements" % (what, n))
+    return t.data_ptr()
+
+
+def dcc_kv4_block_bytes(head_dim, group):
+    out = _sz()
+    _check(_lib.dcc_kv4_block_bytes(head_dim, group, ctypes.byref(out)), "dcc_kv4_block_bytes")
+    return out.value
+
+
+def dcc_local_check(stream=None):
+    """Returns the status code (does not raise) of the calls without a
+    communicator on the current device since the last check."""
+    return _lib.dcc_local_check(_stream(stream))
+
+
+def _same(x, shape, dtype, n, what):
+    if len(x) != n or x.shape != tuple(shape) or x.dtype != dtype:
+        raise ValueError("%s: %d tensors of shape %s, %s" % (what, n, tuple(shape), dtype))
+    return x
+
+
+def dcc_linear(weight, x, y, bias=None, residual=None, act="none", stream=None):
+    """y[r] = act(x[r] weight[r]^T + bias[r]) + residual[r] on every rank (lists
+    of tensors or Ranks): weight rows x k, x tokens x k, bias rows, residual and
+    y tokens x rows; residual may be y."""
+    weight, x, y, bias, residual = _ranks(weight), _ranks(x), _ranks(y), _ranks(bias), _ranks(residual)
+    n, (rows, k), tokens = len(weight), weight.shape, x.shape[0]
+    _same(x, (tokens, k), weight.dtype, n, "x")
+    _same(y, (tokens, rows), weight.dtype, n, "y")
+    if bias is not None:
+        _same(bias, (rows,), weight.dtype, n, "bias")
+    if residual is not None:
+        _same(residual, (tokens, rows), weight.dtype, n, "residual")
+    if not (weight.dense and x.dense and y.dense and (residual is None or residual.dense)):
+        raise ValueError("dcc_linear takes dense rows")
+    return _check(_lib.dcc_linear(n, weight.ptrs, x.ptrs, bias.ptrs if bias else None,
+                                  residual.ptrs if residual else None, y.ptrs, tokens, rows, k,
+                                  _code(ACT_CODES, act, "activation"), _dtype(weight.dtype), _stream(stream)),
+                  "dcc_linear")
+
+
+def _rows_args(kv, k, v, start):
+    k, v = _ranks(k), _ranks(v)
+    shape = (k.shape[0], kv.kv_heads, kv.head_dim)
+    _same(k, shape, kv.torch_dtype, kv.n, "k")
+    _same(v, shape, kv.torch_dtype, kv.n, "v")
+    if k.stride != v.stride:
+        raise ValueError("k and v have the same row stride")
+    return k.ptrs, v.ptrs, shape[0], k.stride, _index(start, kv.seqs + 1, "start")
+
+
+def dcc_kv4_append(kv, layer, k, v, start, stream=None):
+    """Quantise the batch's new keys and values into the cache (Kv4Cache)."""
+    return _check(_lib.dcc_kv4_append(kv.ref, layer, *_rows_args(kv, k, v, start), _stream(stream)), "dcc_kv4_append")
+
+
+def dcc_kv4_read(kv, layer, k, v, start, stream=None):
+    """Read the batch's last rows back as values."""
+    return _check(_lib.dcc_kv4_read(kv.ref, layer, *_rows_args(kv, k, v, start), _stream(stream)), "dcc_kv4_read")
+
+
+def dcc_kv4_attention_workspace(kv, q_heads):
+    out = _sz()
+    _check(_lib.dcc_kv4_attention_workspace(kv.ref, q_heads, ctypes.byref(out)), "dcc_kv4_attention_workspace")
+    return out.value
+
+
+def dcc_kv4_attention(kv, layer, q, out, start, max_new, workspace, lse=None, scale=None, window=0, stream=None):
+    """Causal attention of the batch's rows over the cache (see dcc.h).  scale
+    None: 1 / sqrt(head_dim)."""
+    q, out, lse = _ranks(q), _ranks(out), _ranks(lse)
+    tokens, heads = q.shape[0], q.shape[1]
+    _same(q, (tokens, heads, kv.head_dim), kv.torch_dtype, kv.n, "q")
+    _same(out, q.shape, kv.torch_dtype, kv.n, "out")
+    if lse is not None:
+        _same(lse, (tokens, heads), torch.float32, kv.n, "lse")
+    if not out.dense or (lse is not None and not lse.dense):
+        raise ValueError("out and lse have dense rows")
+    return _check(_lib.dcc_kv4_attention(kv.ref, layer, q.ptrs, out.ptrs, lse.ptrs if lse else None, heads, tokens,
+                                         q.stride, _index(start, kv.seqs + 1, "start"), max_new,
+                                         kv.head_dim ** -0.5 if scale is None else scale, window,
+                                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                         _stream(stream)), "dcc_kv4_attention")
+
+
+def dcc_kv4_pages_workspace(kv):
+    out = _sz()
+    _check(_lib.dcc_kv4_pages_workspace(kv.ref, ctypes.byref(out)), "dcc_kv4_pages_workspace")
+    return out.value
+
+
+def _ws(workspace):
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _info(info):
+    return None if info is None else _index(info, 4, "info")
+
+
+def dcc_kv4_reserve(kv, add, workspace, info=None, stream=None):
+    return _check(_lib.dcc_kv4_reserve(kv.ref, _index(add, kv.seqs, "add"), _info(info), *_ws(workspace),
+                                       _stream(stream)), "dcc_kv4_reserve")
+
+
+def dcc_kv4_free(kv, seqs, workspace, info=None, stream=None):
+    return _check(_lib.dcc_kv4_free(kv.ref, _index(seqs, 0, "seqs"), seqs.numel(), _info(info), *_ws(workspace),
+                                    _stream(stream)), "dcc_kv4_free")
+
+
+def dcc_kv4_fork(kv, src, dst, workspace, info=None, stream=None):
+    n = dst.numel()
+    return _check(_lib.dcc_kv4_fork(kv.ref, _index(src, n, "src"), _index(dst, n, "dst"), n, _info(info),
+                                    *_ws(workspace), _stream(stream)), "dcc_kv4_fork")
+
+
+def dcc_kv4_copy(kv, src, dst, stream=None):
+    n = dst.numel()
+    return _check(_lib.dcc_kv4_copy(kv.ref, _index(src, n, "src"), _index(dst, n, "dst"), n, _stream(stream)),
+                  "dcc_kv4_copy")
+
+
+def dcc_kv4_compact(kv, new_table, new_refs, remap, workspace, info=None, stream=None):
+    return _check(_lib.dcc_kv4_compact(kv.ref, _index(new_table, kv.seqs * kv.max_pages, "new_table"),
+                                       _index(new_refs, kv.pages, "new_refs"), _index(remap, kv.pages, "remap"),
+                                       _info(info), *_ws(workspace), _stream(stream)), "dcc_kv4_compact")
+
+
 def prepare_allreduce(comm, send, recv, count, dtype, algo="auto", stream=None):
     """Marshal the arguments of one dcc_allreduce once and return a callable that
     repeats exactly that call (for launch loops where Python overhead matters)."""
@@ -519,3 +710,73 @@ class Comm:
             self.close()
         except Exception:
             pass
+
+
+class Kv4Cache:
+    """A 4-bit paged key/value cache of N virtual ranks, over tensors the caller
+    owns: pools[r] uint8 (layers, pages, kv_heads, block bytes), table int32
+    (seqs, max_pages), lengths int32 (seqs,), refs int32 (pages,) for the page
+    calls.  Kv4Cache.create allocates an empty one."""
+
+    def __init__(self, pools, table, lengths, refs=None, kv_heads=1, head_dim=128, group=64, dtype="bf16"):
+        block = dcc_kv4_block_bytes(head_dim, group)
+        self.pools, self.table, self.lengths, self.refs = list(pools), table, lengths, refs
+        self.n, self.kv_heads, self.head_dim, self.group = len(self.pools), kv_heads, head_dim, group
+        code = _dtype(dtype)
+        self.torch_dtype = {v: k for k, v in TORCH_CODES.items()}[code]
+        shape = tuple(self.pools[0].shape)
+        if len(shape) != 4 or shape[2:] != (kv_heads, block):
+            raise ValueError("pools: (layers, pages, %d, %d) bytes" % (kv_heads, block))
+        for p in self.pools:
+            if tuple(p.shape) != shape or p.element_size() != 1 or not p.is_contiguous() or not p.is_cuda:
+                raise ValueError("pools: contiguous byte tensors of one shape on the GPU")
+        self.layers, self.pages = shape[0], shape[1]
+        if table.dim() != 2:
+            raise ValueError("table: (seqs, max_pages)")
+        self.seqs, self.max_pages = table.shape
+        self._ptrs = _ptrs(self.pools)
+        self.desc = dcc_kv4_t(self._ptrs, _index(table, 1, "table"), _index(lengths, self.seqs, "lengths"),
+                              None if refs is None else _index(refs, self.pages, "refs"), self.n, self.layers,
+                              self.pages, self.seqs, self.max_pages, kv_heads, head_dim, group, code)
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def create(cls, n_ranks, layers, pages, seqs, max_pages, kv_heads=1, head_dim=128, group=64, dtype="bf16",
+               device="cuda"):
+        """An empty cache with buffers of its own."""
+        block = dcc_kv4_block_bytes(head_dim, group)
+        pools = [torch.zeros(layers, pages, kv_heads, block, dtype=torch.uint8, device=device) for _ in range(n_ranks)]
+        return cls(pools, torch.full((seqs, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(seqs, dtype=torch.int32, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device), kv_heads, head_dim, group, dtype)
+
+    def attention_workspace(self, q_heads):
+        """A workspace for attention() (zeroed once; one per concurrent call)."""
+        return torch.zeros(dcc_kv4_attention_workspace(self, q_heads), dtype=torch.uint8, device=self.table.device)
+
+    def pages_workspace(self):
+        return torch.empty(dcc_kv4_pages_workspace(self), dtype=torch.uint8, device=self.table.device)
+
+    def append(self, k, v, start, layer=0, stream=None):
+        dcc_kv4_append(self, layer, k, v, start, stream)
+
+    def read(self, k, v, start, layer=0, stream=None):
+        dcc_kv4_read(self, layer, k, v, start, stream)
+
+    def attention(self, q, out, start, max_new, workspace, lse=None, scale=None, window=0, layer=0, stream=None):
+        dcc_kv4_attention(self, layer, q, out, start, max_new, workspace, lse, scale, window, stream)
+
+    def reserve(self, add, workspace, info=None, stream=None):
+        dcc_kv4_reserve(self, add, workspace, info, stream)
+
+    def free(self, seqs, workspace, info=None, stream=None):
+        dcc_kv4_free(self, seqs, workspace, info, stream)
+
+    def fork(self, src, dst, workspace, info=None, stream=None):
+        dcc_kv4_fork(self, src, dst, workspace, info, stream)
+
+    def copy_pages(self, src, dst, stream=None):
+        dcc_kv4_copy(self, src, dst, stream)
+
+    def compact(self, new_table, new_refs, remap, workspace, info=None, stream=None):
+        dcc_kv4_compact(self, new_table, new_refs, remap, workspace, info, stream)

@@ -537,6 +537,145 @@ const char* dcc_version(void);
  * architectures). */
 int dcc_kernel_binary_version(int* version);
 
+/* ------------------------------------------------------------------------ */
+/* Around the row-parallel layer of a tensor-parallel decoder: the 4-bit    */
+/* key/value cache, the attention that reads it, its pages, and the          */
+/* column-parallel linear layer.  These calls need no communicator and no    */
+/* registration: rank r's buffers are only ever touched for rank r (its      */
+/* heads, its rows), one launch for all ranks.  They run on the device that  */
+/* is current on the calling thread, asynchronously on the stream, allocate  */
+/* nothing and keep nothing between calls.  HOST arrays hold one device      */
+/* pointer per rank.  A failure seen on the device (a page number outside    */
+/* the pool, a wait that gave up) is recorded and skipped; dcc_local_check   */
+/* reports it.                                                               */
+/* ------------------------------------------------------------------------ */
+
+#define DCC_KV4_PAGE 64 /* tokens per page of a 4-bit cache */
+
+/* A 4-bit key/value cache.  Rank r's pool holds layers * pages * kv_heads
+ * blocks of dcc_kv4_block_bytes, [layer][page][kv head]; one table serves all
+ * layers and ranks: position x of sequence s lies in row x mod 64 of page
+ * table[s * max_pages + x / 64].  A sequence owns ceil(len / 64) pages, the
+ * rest of its row is -1.  Channels are quantised in groups: lo = the group's
+ * minimum, step = R((max - lo) / 15), code = (x - lo) / step rounded to the
+ * nearest even in 0..15, value = lo + step * code, with step and lo in the
+ * cache's type; a group that holds a NaN or an infinity, or whose range
+ * overflows fp32, reads back as NaN.  fp16 / bf16, head_dim 64 or 128,
+ * group 32 or 64 (UNSUPPORTED otherwise).  Pools are 16-byte aligned. */
+typedef struct {
+  void* const* pool; /* HOST array of n_ranks device pointers */
+  int32_t* table;    /* device, seqs * max_pages */
+  int32_t* len;      /* device, seqs: tokens each sequence holds */
+  int32_t* refs;     /* device, pages: sequences that own each page (0 = free); only the page calls need it */
+  int n_ranks, layers, pages, seqs, max_pages, kv_heads, head_dim, group;
+  dcc_dtype_t dtype;
+} dcc_kv4_t;
+
+/* Bytes of one block (one kv head of one page). */
+int dcc_kv4_block_bytes(int head_dim, int group, size_t* bytes);
+
+/* Quantise new keys and values into the pages.  The batch is ragged: rows
+ * start[s] .. start[s+1]-1 (device, seqs + 1 entries, ascending, start[seqs] <=
+ * tokens) are the last rows of sequence s, whose len already counts them: row
+ * i goes to position len[s] - start[s+1] + i.  k[r] / v[r]: tokens rows of
+ * kv_heads * head_dim elements, `stride` elements apart (a multiple of 8, so
+ * that rows of a fused projection may be passed in place).  Rows of no
+ * sequence, or at a position below zero, are skipped. */
+int dcc_kv4_append(const dcc_kv4_t* kv, int layer, void* const* k, void* const* v, size_t tokens, size_t stride,
+                   const int32_t* start, dcc_stream_t s);
+
+/* Read the last rows of each sequence back as values (same batch as
+ * dcc_kv4_append; rows that it would skip are left as they are). */
+int dcc_kv4_read(const dcc_kv4_t* kv, int layer, void* const* k, void* const* v, size_t tokens, size_t stride,
+                 const int32_t* start, dcc_stream_t s);
+
+/* Causal attention over the cache, grouped heads: query head h reads kv head
+ * h / (q_heads / kv_heads).  Rows as in dcc_kv4_append: row i of sequence s
+ * stands at position x = len[s] - start[s+1] + i and sees the positions
+ * max(0, x - window + 1) .. x (window 0: all up to x):
+ *   out = sum_j p_j V_j,  p = softmax_j(scale * q . K_j),  lse = ln sum_j exp(scale * q . K_j).
+ * A row that sees nothing (an idle slot) gives zeros and lse -infinity.
+ * q[r] / out[r]: tokens rows of q_heads * head_dim elements, q rows q_stride
+ * elements apart (a multiple of 8), out rows dense; lse NULL, or lse[r]:
+ * tokens * q_heads floats.  max_new: an upper bound of start[s+1] - start[s]
+ * (rows past it are left as they are).  q_heads a multiple of kv_heads, at
+ * most 128 query heads per kv head.  Scores, softmax and sums in fp32; the
+ * probabilities enter the second product rounded to 16 bits.
+ * workspace: dcc_kv4_attention_workspace bytes, 16-byte aligned, filled with
+ * zeros once before its first use (calls leave its counters at zero); calls
+ * that may run at the same time need one each. */
+int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* const* out, float* const* lse, int q_heads,
+                      size_t tokens, size_t q_stride, const int32_t* start, int max_new, float scale, int window,
+                      void* workspace, size_t workspace_bytes, dcc_stream_t s);
+int dcc_kv4_attention_workspace(const dcc_kv4_t* kv, int q_heads, size_t* bytes);
+
+/* Page calls: all state is on the device, the lowest free pages are given out
+ * first, requests are served in order, so the outcome is the same every time.  Lists of sequences have at
+ * most seqs entries, lists of pages at most pages.
+ * workspace: dcc_kv4_pages_workspace bytes, 16-byte aligned, any content.
+ * info (device, 4 int32, may be NULL) receives what each call says.  Sequence
+ * and page numbers out of range are skipped and recorded (dcc_local_check). */
+int dcc_kv4_pages_workspace(const dcc_kv4_t* kv, size_t* bytes);
+
+/* Let sequence s hold add[s] more tokens (device, seqs; add[s] <= 0: none):
+ * len[s] grows and new pages join its row.  A sequence whose pages are no
+ * longer there, or whose row is too short, keeps its length, and so does
+ * every later one that needs a page once the pool has run out.  info: free
+ * pages left, sequences not served, pages given. */
+int dcc_kv4_reserve(const dcc_kv4_t* kv, const int32_t* add, int32_t* info, void* workspace, size_t workspace_bytes,
+                    dcc_stream_t s);
+
+/* Give up the pages of `count` sequences (device list): a page returns to the
+ * pool with its last owner; len 0, row -1.  info: free pages left, entries
+ * skipped (out of range or named twice), 0. */
+int dcc_kv4_free(const dcc_kv4_t* kv, const int32_t* seqs, size_t count, int32_t* info, void* workspace,
+                 size_t workspace_bytes, dcc_stream_t s);
+
+/* Beam step: sequence dst[i] gives up its pages, then becomes a copy of
+ * src[i] (device lists, i < count): full pages are shared, a partial last
+ * page is copied (all layers, all ranks) to the lowest free page, so that the
+ * two can grow apart.  A fork fails, leaving dst[i] empty, when no page is
+ * left, when dst[i] was named before or when src[i] is itself some dst.
+ * info: free pages left, forks failed, pages copied. */
+int dcc_kv4_fork(const dcc_kv4_t* kv, const int32_t* src, const int32_t* dst, size_t count, int32_t* info,
+                 void* workspace, size_t workspace_bytes, dcc_stream_t s);
+
+/* Copy page src[i] to page dst[i] (device lists, i < count) in all layers and
+ * ranks.  No dst may be named twice or be some src. */
+int dcc_kv4_copy(const dcc_kv4_t* kv, const int32_t* src, const int32_t* dst, size_t count, dcc_stream_t s);
+
+/* Squeeze the pool: with m pages in use, those numbered m and up move, in
+ * ascending order, to the free pages below m, in ascending order.  remap[p]
+ * (device, pages) is page p's new number, -1 for a free page; new_table and
+ * new_refs are the table and counts that follow (they may be kv->table and
+ * kv->refs themselves).  Pages that moved keep their old content until they
+ * are given out again, so work still running on the old table stays valid.
+ * info: free pages, pages moved. */
+int dcc_kv4_compact(const dcc_kv4_t* kv, int32_t* new_table, int32_t* new_refs, int32_t* remap, int32_t* info,
+                    void* workspace, size_t workspace_bytes, dcc_stream_t s);
+
+typedef enum { DCC_ACT_NONE = 0, DCC_ACT_RELU = 1, DCC_ACT_GELU = 2, DCC_ACT_GELU_TANH = 3, DCC_ACT_SILU = 4 } dcc_act_t;
+
+/* Column-parallel linear layer (what precedes dcc_linear_allreduce in a
+ * tensor-parallel block): rank r computes its own rows for every token,
+ *   y[r][t*rows + i] = R( act( sum_k weight[r][i*k + .] * x[r][t*k + .] + bias[r][i] ) + residual[r][t*rows + i] )
+ * weight[r] rows x k, x[r] tokens x k (the ranks may pass the same x), y[r]
+ * tokens x rows, all dense; bias NULL or rows elements per rank; residual
+ * NULL or tokens x rows per rank (residual[r] == y[r] works in place).  Sums,
+ * activation and residual in fp32, one rounding.  GELU is the erf form,
+ * GELU_TANH the tanh form, SILU z / (1 + exp(-z)).  fp16 / bf16, rows and k
+ * multiples of 8 (UNSUPPORTED otherwise), 16-byte aligned; outputs disjoint
+ * from each other and from every other buffer. */
+int dcc_linear(int n_ranks, void* const* weight, void* const* x, void* const* bias, void* const* residual,
+               void* const* y, size_t tokens, size_t rows, size_t k, dcc_act_t act, dcc_dtype_t t, dcc_stream_t s);
+
+/* Synchronise the stream and report what the calls of this section recorded
+ * on the current device since the last check: DCC_OK, DCC_ERR_BOUNDS (a
+ * sequence or page number out of range; the access was skipped) or
+ * DCC_ERR_TIMEOUT (a wait inside a kernel gave up; its outputs are not
+ * complete).  Clears the record. */
+int dcc_local_check(dcc_stream_t s);
+
 #ifdef __cplusplus
 }
 #endif
