@@ -28,7 +28,7 @@
 namespace dcc {  // kernels of the calls without a communicator, for visit_kernels
 const void* linear_kernel(bool fp16);
 const void* kv4_row_kernel(bool fp16, bool read, int dim, int group);
-const void* kv4_attention_kernel(bool fp16, int dim, int group);
+const void* kv4_attention_kernel(bool fp16, int dim, int group, int which);
 const void* kv4_pages_kernel(int i);
 }  // namespace dcc
 
@@ -364,7 +364,7 @@ bool visit_kernels(F&& visit) {
     for (int dim = 64; dim <= 128; dim += 64)
       for (int group = 32; group <= 64; group += 32)
         if (!v(dcc::kv4_row_kernel(fp16, false, dim, group)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group)) ||
-            !v(dcc::kv4_attention_kernel(fp16, dim, group)))
+            !v(dcc::kv4_attention_kernel(fp16, dim, group, 1)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 2)))
           return false;
   }
   for (int i = 0; i < 3; ++i)

@@ -1,23 +1,37 @@
 // kv4_attention.cu -- host side of the attention over the 4-bit cache.
 #include "comm.h"
-#include "kv4_attention.cuh"
+#include "kv4_decode.cuh"
 
 namespace dcc {
-template <typename T>
-static const void* attention_kernel_of(int dim, int group) {
-  if (dim == 128) return group == 64 ? (const void*)&k_kv4_attention<T, 128, 64> : (const void*)&k_kv4_attention<T, 128, 32>;
-  return group == 64 ? (const void*)&k_kv4_attention<T, 64, 64> : (const void*)&k_kv4_attention<T, 64, 32>;
+namespace {
+struct Kernel {
+  const void* fn;
+  int threads;
+  size_t smem;
+};
+template <typename T, int D, int G, int RT>
+Kernel decode_of() {
+  using S = DecShape<D, G, RT>;
+  return {(const void*)&k_kv4_decode<T, D, G, RT>, S::warps * 32, S::smem};
 }
-const void* kv4_attention_kernel(bool fp16, int dim, int group) {
-  return fp16 ? attention_kernel_of<__half>(dim, group) : attention_kernel_of<__nv_bfloat16>(dim, group);
+template <typename T, int RT>
+Kernel decode_for(int dim, int group) {
+  if (dim == 128) return group == 64 ? decode_of<T, 128, 64, RT>() : decode_of<T, 128, 32, RT>();
+  return group == 64 ? decode_of<T, 64, 64, RT>() : decode_of<T, 64, 32, RT>();
 }
+Kernel decode(bool fp16, int dim, int group, int tiles) {
+  if (tiles > 1) return fp16 ? decode_for<__half, 2>(dim, group) : decode_for<__nv_bfloat16, 2>(dim, group);
+  return fp16 ? decode_for<__half, 1>(dim, group) : decode_for<__nv_bfloat16, 1>(dim, group);
+}
+}  // namespace
+const void* kv4_attention_kernel(bool fp16, int dim, int group, int which) { return decode(fp16, dim, group, which).fn; }
 }  // namespace dcc
 
 extern "C" {
 
 int dcc_kv4_attention_workspace(const dcc_kv4_t* kv, int q_heads, size_t* bytes) {
   if (!kv || !bytes || q_heads < 1 || kv->kv_heads < 1 || q_heads % kv->kv_heads) return DCC_ERR_INVALID_ARG;
-  *bytes = 16;
+  *bytes = dcc::dec_ws_bytes();
   return DCC_OK;
 }
 
@@ -68,13 +82,21 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
   a.max_new = max_new;
   a.window = window;
   a.scale = scale;
-  const long long items = (long long)tokens * q_heads * kv->n_ranks;
-  const long long grid = (items + dcc::kAttnThreads / 32 - 1) / (dcc::kAttnThreads / 32);
-  if (grid > 0x7fffffffll) return DCC_ERR_INVALID_ARG;
+  a.share = q_heads / kv->kv_heads;
+  a.ws = static_cast<char*>(workspace);
+  a.timeout_ns = 2000000000ull;
   if ((rc = dcc_host::kv4_ready(&d)) != DCC_OK) return rc;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return DCC_ERR_CUDA;
+  }
+  const dcc::Kernel k = dcc::decode(kv->dtype == DCC_FP16, kv->head_dim, kv->group, max_new * a.share > 8 ? 2 : 1);
+  if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
   void* args[] = {&d, &a};
-  return dcc_host::launch(dcc::kv4_attention_kernel(kv->dtype == DCC_FP16, kv->head_dim, kv->group), (int)grid,
-                          dcc::kAttnThreads, false, args, static_cast<cudaStream_t>(s), 0, true);
+  return dcc_host::launch(k.fn, sms < dcc::kDecMaxCtas ? sms : dcc::kDecMaxCtas, k.threads, false, args,
+                          static_cast<cudaStream_t>(s), k.smem, true);
 }
 
 }  // extern "C"
