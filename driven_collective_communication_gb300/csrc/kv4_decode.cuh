@@ -6,26 +6,38 @@
 // m) V_j.  K_j = lo + step * code per group of G channels, so
 //   q.K_j = sum_groups step_jg (q_g . code_jg) + lo_jg (sum q_g),
 //   O_d   = sum_j (p_j step_jg) code_jd + sum_j p_j lo_jg.
-// The products with the codes run on the tensor cores; the codes are exact in
-// 16 bits, so the scores lose nothing, and of the second product only p * step
-// is rounded (bf16; in two bf16 terms, 16 bits, when the result is fp16: in
-// fp16 itself p * step would leave the type's range).  Everything that
-// carries lo is fp32.
+// The products with the codes run on the tensor cores in fp16 with fp32 sums;
+// everything that carries lo is fp32.  The codes are exact.  So is Q: a row is
+// scaled by a power of two that brings its largest channel to 2^14, which
+// keeps all bits of a bf16 or fp16 channel down to 2^-28 of it.  p * step is
+// the one operand that is rounded (11 bits; 22 in pages where a mask begins or
+// ends); its scale follows the running maximum of s_j and of the steps (R
+// below: l, O and all sums are in units of 2^R), so it neither overflows nor
+// falls into the subnormals unless it is 2^-28 of the largest seen.  Codes
+// enter O as n - 8, about the middle of their range, so that what is rounded
+// is no larger than V itself.
 //
-// Bound by reading the cache (0.56 bytes a channel at G = 64), if the
-// instructions that unpack it stay below the memory's time.  Codes become
-// floats by one AND-OR: nibble n in the mantissa of 128 (bf16) or 64 (fp16)
-// is 128 + n (64 + n); that constant is taken off the scores through sum q_g,
-// and off O through a product with a row of ones, which sums the same rounded
-// p * step -- no subtraction per code, no conversion.  The fragments take the
-// codes where they lie (kv4.cuh).  mma.sync with its operands in registers
-// suits this: the tensor work is 8 rows wide, and tcgen05 would want the
-// unpacked operands written to shared or tensor memory first, which costs
-// more than the products.
+// Bound by reading the cache (0.56 bytes a channel at G = 64) if the
+// instructions that unpack it stay below the memory's time, above all the
+// integer pipe's (half rate).  A nibble in bits 4..7 of a 16-bit lane, with
+// the exponent of 64 put around it, is the fp16 number 64 + n: one AND-OR
+// makes two codes an operand register, after a shift for three nibbles of
+// four (the left one runs on the multiply pipe).  The 64 comes off the scores
+// as the accumulators' initial value (-64 sum q), and off O, with the 8,
+// through a product with a row of ones, which sums the same rounded p * step:
+// nothing is subtracted or converted per code.  (Bare nibbles are fp16
+// subnormals and need no exponent, one instruction fewer in seven, but the
+// tensor core aligns its sums by nominal exponents: measured, the sums lost
+// some 9 bits.)  The fragments take the codes where they lie (kv4.cuh).
+// mma.sync with its operands in registers suits this: the tensor work is 8
+// rows wide, and tcgen05 would want the unpacked operands written to shared
+// or tensor memory first, which costs more than the products.
 //
-//   S[row][key]: A = Q (16 rows), B = codes of 8 keys; its accumulator holds,
-//   in each lane, row g and keys of the quad pair -- exactly the B fragment of
-//   O^T[channel][row]: A = V codes (16 channels x 16 keys), B = P^T.
+//   S^T[key][row]: A = codes of 16 keys, B = Q^T (8 rows); the accumulator
+//   holds keys g, g + 8 and rows 2 t, 2 t + 1 of lane 4 g + t;
+//   O^T[channel][row]: A = V codes (16 channels x 16 keys), B = P^T: p * step
+//   of the accumulator, packed and transposed 8 x 8 by movmatrix.  Its rows lie
+//   in the same lanes, so rescaling needs no exchange.
 //
 // Work split.  The pages of all (sequence, rank, kv head, row tile) segments
 // form one line of units; CTA and warp ranges cut it evenly, so every SM reads
@@ -36,6 +48,8 @@
 // ring), then over the CTAs by whichever comes last, in CTA order, so results
 // do not depend on timing.
 #pragma once
+#include <type_traits>
+
 #include "bulk.cuh"
 #include "kv4.cuh"
 
@@ -70,7 +84,10 @@ __host__ __device__ constexpr size_t dec_ws_bytes() {
 template <int D, int G, int RT>
 struct DecShape {
   static constexpr int block = kv4_block_bytes(D, G);
-  static constexpr int warps = RT > 1 ? 8 : (12 * 2 * block <= 222 * 1024 ? 12 : 10);
+#ifndef DEC_W
+#define DEC_W 12
+#endif
+  static constexpr int warps = RT > 1 || 12 * 2 * block > 222 * 1024 ? 8 : DEC_W;
   static constexpr int fit = 222 * 1024 / (warps * block);
   static constexpr int stages = fit > 4 ? 4 : fit;
   static constexpr size_t smem = (size_t)warps * stages * block + 128;
@@ -82,34 +99,35 @@ __device__ __forceinline__ float exp2_approx(float x) {  // 2^x; -inf gives 0
   return y;
 }
 // D += A B, 16 x 8 x 16, fp32 accumulators
-template <bool FP16>
 __device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-  if (FP16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-template <uint32_t MASK, uint32_t MAGIC>
-__device__ __forceinline__ uint32_t and_or(uint32_t w) {
+__device__ __forceinline__ void mma_16816_from(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1, const float* c) {  // D = C + A B
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }  // -126 <= k <= 127
+// nibbles P and P + 4 of w as two fp16 numbers 64 + n
+template <int P>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  const uint32_t x = P == 0 ? w * 16u : w >> (4 * (P - (P > 0)));
   uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "n"(MAGIC));  // (w & MASK) | MAGIC
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(0x00f000f0u), "r"(0x54005400u));  // (x & mask) | 64.0
   return r;
 }
-// nibbles P and P + 4 of w as two floats 64 + n (fp16) or 128 + n (bf16)
-template <bool FP16, int P>
-__device__ __forceinline__ uint32_t unpack_pair(uint32_t w) {
-  if (FP16) return and_or<0x00f000f0u, 0x54005400u>(P == 0 ? w << 4 : w >> (4 * (P - 1)));
-  return and_or<0x000f000fu, 0x43004300u>(w >> (4 * P));
+// the 8 x 8 matrix of 16-bit elements of which lane 4 r + c holds (r, 2 c) and (r, 2 c + 1), transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
 }
-template <bool FP16>
-__host__ __device__ constexpr float unpack_bias() { return FP16 ? 64.0f : 128.0f; }
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) { return Half16<__half>::narrow2(a, b); }
 
 // One sequence's part of the line of units.
 struct DecSeq {
@@ -137,28 +155,52 @@ __device__ __forceinline__ DecSeq dec_seq(const Kv4Dev& kv, const AttnArgs& a, i
   return q;
 }
 
+struct DecCursor {
+  int s, seg;  // sequence, segment of it: (rank, head), tile
+  DecSeq q;
+};
+
 // Join `n` partials (by `at`) of one segment and store the result: to `part`
-// (a partial again) or to the outputs.  All threads of the CTA.
+// (a partial again) or to the outputs.  All threads of the CTA.  Eight
+// partials' loads are in flight at a time: they come from other SMs.
 template <typename T, int D, int ROWS, typename At>
 __device__ __forceinline__ void dec_join(const AttnArgs& a, int n, At at, float* part, int rank, int head, int row0,
                                          int rows, int begin) {
+  constexpr int kBatch = 8;
   for (int e = threadIdx.x; e < ROWS * (D / 4); e += blockDim.x) {
     const int row = e / (D / 4), d4 = e % (D / 4);
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, at(i)[row]);
-    const float mu = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
+    float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* p = at(i);
-      const float w = exp2_approx(p[row] - mu);
-      const float4 v = *reinterpret_cast<const float4*>(p + 2 * ROWS + row * (D + 4) + d4 * 4);
-      l = fmaf(w, p[ROWS + row], l);
-      o.x = fmaf(w, v.x, o.x);
-      o.y = fmaf(w, v.y, o.y);
-      o.z = fmaf(w, v.z, o.z);
-      o.w = fmaf(w, v.w, o.w);
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float pm[kBatch], pl[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float* p = at(min(i0 + i, n - 1));
+        pm[i] = i0 + i < n ? p[row] : -INFINITY;
+        pl[i] = i0 + i < n ? p[ROWS + row] : 0.0f;
+        v[i] = i0 + i < n ? *reinterpret_cast<const float4*>(p + 2 * ROWS + row * (D + 4) + d4 * 4)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float mn = m;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, pm[i]);
+      const float mu = mn == -INFINITY ? 0.0f : mn, fix = exp2_approx(m - mu);
+      l *= fix;
+      o.x *= fix;
+      o.y *= fix;
+      o.z *= fix;
+      o.w *= fix;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float w = exp2_approx(pm[i] - mu);
+        l = fmaf(w, pl[i], l);
+        o.x = fmaf(w, v[i].x, o.x);
+        o.y = fmaf(w, v[i].y, o.y);
+        o.z = fmaf(w, v[i].z, o.z);
+        o.w = fmaf(w, v[i].w, o.w);
+      }
+      m = mn;
     }
     if (part) {
       if (d4 == 0) {
@@ -183,20 +225,23 @@ __device__ __forceinline__ void dec_join(const AttnArgs& a, int n, At at, float*
 template <typename T, int D, int G, int RT>
 __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decode(Kv4Dev kv, AttnArgs a) {
   using Shape = DecShape<D, G, RT>;
-  constexpr bool FP16 = sizeof(T) == 2 && !__is_same(T, __nv_bfloat16);
   constexpr int W = Shape::warps, S = Shape::stages, BLK = Shape::block, THREADS = W * 32;
   constexpr int NG = D / G, ROWS = 8 * RT, JW = D / 32, MT = D / 16, SLOT = dec_slot(ROWS, D);
-  constexpr float kCenter = 8.0f;  // codes enter O as n - 8: what p * step is rounded against
+  constexpr float kCenter = 8.0f;
+  constexpr int kMinExp = -60;  // steps below 2^-60 count as that: 2^(14 + 60) a key still sums in fp32
+  constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
   extern __shared__ __align__(128) char dec_smem[];
   __shared__ __align__(8) uint64_t bars[W][S];
   __shared__ long long s_sum[W];
-  __shared__ int s_seq[W];         // where each warp's range begins: sequence,
-  __shared__ long long s_base[W];  // its first unit
+  __shared__ DecCursor s_cur[W][2];  // each warp's two cursors; where its range begins at first
+  __shared__ int s_page[W];          // and the page of the segment there
   // what each warp leaves: a segment that began before its range and ended in
   // it (head), one still open at its end (tail); by first and last unit
   __shared__ long long s_seg[2 * W][2];
-  __shared__ int s_who[2 * W][3];  // sequence, (rank, head), tile
-  __shared__ int s_last;
+  __shared__ int s_who[2 * W][5];  // rank, head, first row; rows and first token of the sequence
+  __shared__ int s_list[2][W + 1];
+  __shared__ int s_open[2];        // CTAs that hold parts of the two segments open at the CTA's ends
+  __shared__ int s_last[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   char* ring = dec_smem + (size_t)warp * S * BLK;
   if (lane < S) mbar_init(&bars[warp][lane], 1);
@@ -204,33 +249,10 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
   fence_mbar_init();
   pdl_prologue();
 
-  // ---- the line of units, and this warp's range of it
+  // ---- the line of units, and this warp's range of it.  Up to one sequence a
+  // thread, the sequences are looked at once.
   const int nh = kv.n * kv.heads;
-  long long sum = 0;
-  for (int s = threadIdx.x; s < kv.seqs; s += THREADS) {
-    const DecSeq q = dec_seq(kv, a, s, ROWS);
-    sum += (long long)q.pages * q.tiles;
-  }
-  for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  long long units = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) units += s_sum[w];
-  units *= nh;
-  // no more CTAs than units, so that no range between two others is empty
-  const int C = units < (long long)gridDim.x ? (int)units : (int)gridDim.x, cta = (int)blockIdx.x;
-  if (cta >= C) return;
-  const long long c0 = units * cta / C, c1 = units * (cta + 1) / C;
-  auto warp_begin = [&](int w) { return c0 + (c1 - c0) * w / W; };
-  long long before = 0;
-  for (int s0 = 0; s0 < kv.seqs; s0 += THREADS) {
-    const int s = s0 + (int)threadIdx.x;
-    long long mine = 0;
-    if (s < kv.seqs) {
-      const DecSeq q = dec_seq(kv, a, s, ROWS);
-      mine = (long long)q.pages * q.tiles;
-    }
+  auto scan = [&](long long mine, long long* total) {  // exclusive, over the CTA
     long long x = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -240,72 +262,124 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
     __syncthreads();
     if (lane == 31) s_sum[warp] = x;
     __syncthreads();
-    long long first = before + x - mine;
+    long long first = x - mine;
+    *total = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       if (w < warp) first += s_sum[w];
-      before += s_sum[w];
+      *total += s_sum[w];
     }
-    if (mine)
-#pragma unroll
+    return first;
+  };
+  DecSeq sq0 = {};
+  long long units = 0, first0 = 0;
+  for (int s0 = 0; s0 < kv.seqs; s0 += THREADS) {
+    const int s = s0 + (int)threadIdx.x;
+    DecSeq q = {};
+    if (s < kv.seqs) q = dec_seq(kv, a, s, ROWS);
+    long long total;
+    const long long first = scan((long long)q.pages * q.tiles, &total);
+    if (s0 == 0) {
+      sq0 = q;
+      first0 = first;
+    }
+    units += total;
+  }
+  units *= nh;
+  // no more CTAs than units, so that no range between two others is empty
+  const int C = units < (long long)gridDim.x ? (int)units : (int)gridDim.x, cta = (int)blockIdx.x;
+  if (cta >= C) return;
+  const long long c0 = units * cta / C, c1 = units * (cta + 1) / C;
+  auto warp_begin = [&](int w) { return c0 + (c1 - c0) * w / W; };
+  long long before = 0;
+  for (int s0 = 0; s0 < kv.seqs && before * nh <= c1; s0 += THREADS) {
+    const int s = s0 + (int)threadIdx.x;
+    DecSeq q = sq0;
+    long long first = first0;
+    if (s0 > 0 || kv.seqs > THREADS) {
+      q = DecSeq{};
+      if (s < kv.seqs) q = dec_seq(kv, a, s, ROWS);
+      long long total;
+      first = before + scan((long long)q.pages * q.tiles, &total);
+      before += total;
+    }
+    const long long mine = (long long)q.pages * q.tiles, base = first * nh;
+    if (mine && base < c1 && base + mine * nh > c0)
       for (int w = 0; w < W; ++w) {
         const long long u = warp_begin(w);
-        if (first * nh <= u && u < (first + mine) * nh) {
-          s_seq[w] = s;
-          s_base[w] = first * nh;
+        if (base <= u && u < base + mine * nh) {
+          const int seg = (int)((u - base) / q.pages);
+          s_cur[w][0] = s_cur[w][1] = DecCursor{s, seg, q};
+          s_page[w] = (int)(u - base - (long long)seg * q.pages);
         }
       }
-    if (before * nh > c1) break;
   }
   __syncthreads();
   const long long u0 = warp_begin(warp), u1 = warp_begin(warp + 1);
   const int count = (int)(u1 - u0);
 
-  // ---- a walk along the units: the loads' cursor runs ahead of the sums'
-  struct Cursor {
-    int s, seg, j;  // sequence, segment of it ((rank, head), tile), page of the segment
-    DecSeq q;
-  };
-  auto seek = [&](Cursor& c) {
-    c.s = s_seq[warp];
-    c.q = dec_seq(kv, a, c.s, ROWS);
-    const long long off = u0 - s_base[warp];
-    c.seg = (int)(off / c.q.pages);
-    c.j = (int)(off - (long long)c.seg * c.q.pages);
-  };
-  auto step = [&](Cursor& c) {
-    if (++c.j < c.q.pages) return;
-    c.j = 0;
-    if (++c.seg < nh * c.q.tiles) return;
-    c.seg = 0;
-    do {
-      ++c.s;
-      if (c.s < kv.seqs) c.q = dec_seq(kv, a, c.s, ROWS);
-    } while (c.s < kv.seqs && c.q.pages == 0);
-  };
-  Cursor ld = {}, cu = {};
-  uint32_t missing = 0;  // stages that hold no page
-  int ids = -1, ids_seq = -1, ids_at = -1;
-  auto issue = [&](int st) {
-    const int slot = ld.q.page0 + ld.j;
-    int page = -1;
-    if (!ld.q.empty) {
-      if (ids_seq != ld.s || ids_at != (slot & ~31)) {  // 32 page numbers at a time
-        ids_seq = ld.s;
-        ids_at = slot & ~31;
-        const int x = ids_at + lane;
-        ids = x >= ld.q.page0 && x < ld.q.page0 + ld.q.pages ? kv4_page(kv, ld.s, x) : -1;
-      }
-      page = __shfl_sync(0xffffffffu, ids, slot & 31);
+  // ---- a walk along the units: the loads' cursor runs ahead of the sums'.
+  // What changes with the segment only lies in shared memory.
+  auto put = [&](DecCursor& c, int s, int seg, const DecSeq& q) {
+    __syncwarp();
+    if (lane == 0) {
+      c.s = s;
+      c.seg = seg;
+      c.q = q;
     }
+    __syncwarp();
+  };
+  auto next_segment = [&](DecCursor& c) {
+    int s = c.s, seg = c.seg + 1;
+    DecSeq q = c.q;
+    if (seg >= nh * q.tiles) {
+      seg = 0;
+      do {
+        ++s;
+        if (s < kv.seqs) q = dec_seq(kv, a, s, ROWS);
+      } while (s < kv.seqs && q.pages == 0);
+    }
+    put(c, s, seg, q);
+  };
+  DecCursor& ldc = s_cur[warp][0];
+  DecCursor& cuc = s_cur[warp][1];
+  int ld_slot = 0, ld_end = 0;     // pages of the sequence's row left to load
+  const char* ld_base = nullptr;   // the segment's block of page 0; null: nothing is there to load
+  int ids = -1, ids_at = -1;       // 32 page numbers of that row, from this one on
+  const size_t page_stride = (size_t)kv.heads * BLK;
+  auto ld_open = [&]() {
+    const DecSeq q = ldc.q;
+    const int rh = ldc.seg / q.tiles, rank = rh / kv.heads;
+    ld_slot = q.page0;
+    ld_end = q.page0 + q.pages;
+    ld_base = q.empty ? nullptr : kv4_block(kv, rank, a.layer, 0, rh - rank * kv.heads, BLK);
+  };
+  uint32_t missing = 0;  // stages that hold no page
+  auto issue = [&](int st) {
+    if (ld_slot == ld_end) {
+      const int s = ldc.s;
+      next_segment(ldc);
+      if (ldc.s != s) ids_at = -1;
+      ld_open();
+    }
+    int page = -1;
+    if (ld_base) {
+      if (ids_at < 0 || ld_slot - ids_at >= 32) {
+        ids_at = ld_slot;
+        ids = ids_at + lane < ld_end ? kv4_page(kv, ldc.s, ids_at + lane) : -1;
+      }
+      if (ld_slot < ids_at) {  // the next segment of the same sequence starts over
+        ids_at = ld_slot;
+        ids = ids_at + lane < ld_end ? kv4_page(kv, ldc.s, ids_at + lane) : -1;
+      }
+      page = __shfl_sync(0xffffffffu, ids, ld_slot - ids_at);
+    }
+    ++ld_slot;
     if (page < 0) missing |= 1u << st;
     else missing &= ~(1u << st);
     if (lane == 0) {
-      const int rh = ld.seg / ld.q.tiles;
       mbar_arrive_expect_tx(&bars[warp][st], page < 0 ? 0u : (uint32_t)BLK);
-      if (page >= 0)
-        bulk_load(ring + (size_t)st * BLK, kv4_block(kv, rh / kv.heads, a.layer, page, rh % kv.heads, BLK), BLK,
-                  &bars[warp][st]);
+      if (page >= 0) bulk_load(ring + (size_t)st * BLK, ld_base + page * page_stride, BLK, &bars[warp][st]);
     }
   };
   auto wait = [&](int st, uint32_t parity) {
@@ -320,341 +394,432 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
     }
   };
 
-  // ---- sums of the open segment
-  uint32_t qf[2 * JW][2 * RT];    // Q fragments of each 16-channel step: a0, a2 (rows g), then a1, a3 (rows g + 8)
-  float qsum[RT][NG], mx[RT], l[RT], pmid[RT][NG];
+  // ---- sums of the open segment, for rows 8 x + 2 t + b.  All are in units of
+  // 2^R, R = mx * cs + ex - 14 (mx: the largest raw score, before the factor cs)
+  uint32_t qf[2 * JW][2 * RT];  // Q^T fragments of each 16-channel step
+  float q64[RT][NG][4];         // the scores' accumulators at their start
+  float qsum[RT][NG][2], mx[RT][2], l[RT][2], pmid[RT][NG][2], cs[RT][2];
   float o[RT][MT][4], ones[RT][NG][4];
-  int lim_hi[RT], lim_lo[RT], tile_hi = 0, tile_lo = 0;
+  int ex = kMinExp, lim_hi[RT][2], lim_lo[RT][2], tile_hi = 0, tile_lo = 0, tile_end = 0;
   auto open = [&]() {
-    const int rh = cu.seg / cu.q.tiles, tile = cu.seg % cu.q.tiles, rank = rh / kv.heads, head = rh % kv.heads;
+    const DecSeq sq = cuc.q;
+    const int rh = cuc.seg / sq.tiles, tile = cuc.seg - rh * sq.tiles, rank = rh / kv.heads, head = rh - rank * kv.heads;
+    ex = kMinExp;
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
       const int row = tile * ROWS + 8 * x + g, tok = row / a.share;
-      const bool in = row < cu.q.rows;
-      const T* q = static_cast<const T*>(a.q[rank]) + (size_t)(cu.q.begin + tok) * a.q_stride +
-                   (size_t)(head * a.share + row % a.share) * D;
-      lim_hi[x] = in ? cu.q.pos0 + tok : -1;
-      lim_lo[x] = a.window > 0 ? cu.q.pos0 + tok - a.window + 1 : 0;
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) qsum[x][gr] = 0.0f;
+      const bool in = row < sq.rows;
+      const T* q = static_cast<const T*>(a.q[rank]) + (size_t)(sq.begin + tok) * a.q_stride +
+                   (size_t)(head * a.share + row - tok * a.share) * D;
+      const int hi = in ? sq.pos0 + tok : -1, lo = a.window > 0 ? sq.pos0 + tok - a.window + 1 : 0;
+      uint4 v[JW];
+      float big = 0.0f;
 #pragma unroll
       for (int j = 0; j < JW; ++j) {
-        const uint4 v = in ? *reinterpret_cast<const uint4*>(q + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
+        v[j] = in ? *reinterpret_cast<const uint4*>(q + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = Half16<T>::widen2(u[e]);
+          big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // the row times 2^k has its largest channel in [2^14, 2^15); it takes the
+      // scale's sign, so that a larger raw score is a larger score
+      const int eb = (__float_as_int(big) >> 23) - 127;
+      const int k = big == 0.0f || eb > 127 ? 0 : min(14 - eb, 110);
+      const float up = a.scale < 0.0f ? -pow2(k) : pow2(k);
+      const float c = fabsf(a.scale) * 1.44269504088896341f * pow2(-k);
+      float qs[NG] = {};
+#pragma unroll
+      for (int j = 0; j < JW; ++j) {
+        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 w = Half16<T>::widen2(u[e]);
+          f[2 * e] = w.x * up;
+          f[2 * e + 1] = w.y * up;
+        }
         // channels (e, e + 4) share a register, as two nibbles of a word do
-        qf[2 * j][2 * x] = __byte_perm(v.x, v.z, 0x5410);
-        qf[2 * j][2 * x + 1] = __byte_perm(v.x, v.z, 0x7632);
-        qf[2 * j + 1][2 * x] = __byte_perm(v.y, v.w, 0x5410);
-        qf[2 * j + 1][2 * x + 1] = __byte_perm(v.y, v.w, 0x7632);
-        const float2 f0 = Half16<T>::widen2(v.x), f1 = Half16<T>::widen2(v.y), f2 = Half16<T>::widen2(v.z),
-                     f3 = Half16<T>::widen2(v.w);
-        qsum[x][32 * j / G] += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+        qf[2 * j][2 * x] = half2_bits(f[0], f[4]);
+        qf[2 * j][2 * x + 1] = half2_bits(f[1], f[5]);
+        qf[2 * j + 1][2 * x] = half2_bits(f[2], f[6]);
+        qf[2 * j + 1][2 * x + 1] = half2_bits(f[3], f[7]);
+        qs[32 * j / G] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
       }
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        qsum[x][gr] += __shfl_xor_sync(0xffffffffu, qsum[x][gr], 1);
-        qsum[x][gr] += __shfl_xor_sync(0xffffffffu, qsum[x][gr], 2);
-        pmid[x][gr] = 0.0f;
+        qs[gr] += __shfl_xor_sync(0xffffffffu, qs[gr], 1);
+        qs[gr] += __shfl_xor_sync(0xffffffffu, qs[gr], 2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) ones[x][gr][e] = 0.0f;
       }
-      mx[x] = -INFINITY;
-      l[x] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {  // of the rows that the accumulators hold here
+        const int src = 8 * t + 4 * b;
+        cs[x][b] = __shfl_sync(0xffffffffu, c, src);
+        lim_hi[x][b] = __shfl_sync(0xffffffffu, hi, src);
+        lim_lo[x][b] = __shfl_sync(0xffffffffu, lo, src);
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          qsum[x][gr][b] = __shfl_sync(0xffffffffu, qs[gr], src);
+          q64[x][gr][b] = q64[x][gr][2 + b] = -64.0f * qsum[x][gr][b];
+          pmid[x][gr][b] = 0.0f;
+        }
+        mx[x][b] = -INFINITY;
+        l[x][b] = 0.0f;
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
     }
-    // keys from tile_lo to tile_hi are seen by every row of the tile
-    tile_hi = cu.q.pos0 + tile * ROWS / a.share;
-    const int last = min(tile * ROWS + ROWS, cu.q.rows) - 1;
-    tile_lo = a.window > 0 ? cu.q.pos0 + last / a.share - a.window + 1 : 0;
+    // keys from tile_lo to tile_hi are seen by every row of the tile, none past tile_end by any
+    const int last = min(tile * ROWS + ROWS, sq.rows) - 1;
+    tile_hi = sq.pos0 + tile * ROWS / a.share;
+    tile_end = sq.pos0 + last / a.share;
+    tile_lo = a.window > 0 ? tile_end - a.window + 1 : 0;
   };
 
-  // The final value of each accumulator: centre the codes and add the fp32
-  // part.  Leaves l and pmid summed over the quad.
-  auto settle = [&]() {
+  // One page.  MASKED: some row does not see some key of it.
+  // kg: the key of accumulator row g (of 8); ka, kb: those of rows 2 t, 2 t +
+  // 1.  The order is the one in which a quad's V rows lie in different banks.
+  const int sw = D == 128 ? (t & 1) : (t >> 1);
+  const int ka = 2 * t + sw, kb = 2 * t + 1 - sw;
+  const int kg = D == 128 ? g ^ ((g >> 1) & 1) : g ^ (g >> 2);
+  auto page_pass = [&](auto masked, const char* blk, int key0) {
+    constexpr bool MASKED = decltype(masked)::value;
+    const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D)) + kg * NG;
+    const uint32_t* vpar = par + kKv4Page * NG;
+    float sc[4][RT][4];
 #pragma unroll
-    for (int x = 0; x < RT; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    for (int n = 0; n < 4; ++n) {  // 16 keys each
+      uint32_t w[2][JW];
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        float pm = pmid[x][gr];
-        pm += __shfl_xor_sync(0xffffffffu, pm, 1);
-        pm += __shfl_xor_sync(0xffffffffu, pm, 2);
-        const float p0 = __shfl_sync(0xffffffffu, pm, 8 * t), p1 = __shfl_sync(0xffffffffu, pm, 8 * t + 4);
-        const float k0 = fmaf(-(128.0f + kCenter), ones[x][gr][0], p0), k1 = fmaf(-(128.0f + kCenter), ones[x][gr][1], p1);
-#pragma unroll
-        for (int i = gr * G / 16; i < (gr + 1) * G / 16; ++i) {
-          o[x][i][0] += k0;
-          o[x][i][1] += k1;
-          o[x][i][2] += k0;
-          o[x][i][3] += k1;
+      for (int h = 0; h < 2; ++h) {
+        const char* row = blk + (16 * n + 8 * h + kg) * (D / 2) + t * (JW * 4);
+        if constexpr (JW == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(row);
+          w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(row);
+          w[h][0] = v.x, w[h][1] = v.y;
         }
       }
-    }
-  };
-  auto store_partial = [&](float* p) {
+      float acc[RT][NG][4];
 #pragma unroll
-    for (int x = 0; x < RT; ++x) {
-      if (t == 0) {
-        p[8 * x + g] = mx[x];
-        p[ROWS + 8 * x + g] = l[x];
+      for (int j = 0; j < JW; ++j) {
+        const uint32_t a0[4] = {code_pair<0>(w[0][j]), code_pair<0>(w[1][j]), code_pair<1>(w[0][j]), code_pair<1>(w[1][j])};
+        const uint32_t a1[4] = {code_pair<2>(w[0][j]), code_pair<2>(w[1][j]), code_pair<3>(w[0][j]), code_pair<3>(w[1][j])};
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+          const int gr = 32 * j / G;
+          if (32 * j % G == 0)
+            mma_16816_from(acc[x][gr], a0[0], a0[1], a0[2], a0[3], qf[2 * j][2 * x], qf[2 * j][2 * x + 1], q64[x][gr]);
+          else
+            mma_16816(acc[x][gr], a0[0], a0[1], a0[2], a0[3], qf[2 * j][2 * x], qf[2 * j][2 * x + 1]);
+          mma_16816(acc[x][gr], a1[0], a1[1], a1[2], a1[3], qf[2 * j + 1][2 * x], qf[2 * j + 1][2 * x + 1]);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int h = 0; h < 2; ++h) {
+        float2 sl[NG];  // step, lo
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[2 * ROWS + (8 * x + 2 * t + (e & 1)) * (D + 4) + 16 * i + g + 8 * (e >> 1)] = o[x][i][e];
+        for (int gr = 0; gr < NG; ++gr) sl[gr] = Half16<T>::widen2(par[(16 * n + 8 * h) * NG + gr]);
+#pragma unroll
+        for (int x = 0; x < RT; ++x)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float s = sl[0].y * qsum[x][0][b];
+#pragma unroll
+            for (int gr = 1; gr < NG; ++gr) s = fmaf(sl[gr].y, qsum[x][gr][b], s);
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) s = fmaf(sl[gr].x, acc[x][gr][2 * h + b], s);
+            if (MASKED) {
+              const int pos = key0 + 16 * n + 8 * h + kg;
+              if (pos > lim_hi[x][b] || pos < lim_lo[x][b]) s = -INFINITY;
+            }
+            sc[n][x][2 * h + b] = s;
+          }
+      }
     }
-  };
-  auto store_out = [&]() {
-    const int rh = cu.seg / cu.q.tiles, tile = cu.seg % cu.q.tiles, rank = rh / kv.heads, head = rh % kv.heads;
+    // the largest step of V (its exponent) and the running maximum; what was
+    // summed so far is rescaled where they grew
+    uint32_t top = 0;
 #pragma unroll
-    for (int x = 0; x < RT; ++x) {
-      const float inv = l[x] == 0.0f ? 0.0f : __frcp_rn(l[x]);
-      const float inv2[2] = {__shfl_sync(0xffffffffu, inv, 8 * t), __shfl_sync(0xffffffffu, inv, 8 * t + 4)};
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        const int key = 2 * lane + h;
+        uint32_t s = (vpar - kg * NG)[key * NG + gr] & 0x7fffu;
+        if (s >= kInf || (MASKED && key0 + key > tile_end)) s = 0;
+        top = max(top, s);
+      }
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int ex_new = max(ex, (__float_as_int(Half16<T>::widen((uint16_t)top)) >> 23) - 127);
+    bool grew = ex_new > ex;
+    float alpha[RT][2], ref[RT][2];
+#pragma unroll
+    for (int x = 0; x < RT; ++x)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int row = tile * ROWS + 8 * x + 2 * t + b;
-        if (row < cu.q.rows) {
-          const size_t at = (size_t)(cu.q.begin + row / a.share) * a.q_heads + head * a.share + row % a.share;
-          uint16_t* dst = static_cast<uint16_t*>(a.out[rank]) + at * D + g;
+        float m = mx[x][b];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) m = fmaxf(m, fmaxf(sc[n][x][b], sc[n][x][2 + b]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        grew |= m > mx[x][b];
+        // nothing seen so far: the sums are zero (or NaN) and stay so
+        alpha[x][b] = mx[x][b] == -INFINITY ? 1.0f : exp2_approx(fmaf(mx[x][b] - m, cs[x][b], (float)(ex - ex_new)));
+        mx[x][b] = m;
+        ref[x][b] = m == -INFINITY ? 0.0f : m;
+      }
+    ex = ex_new;
+    const float shift = (float)(14 - ex);
+    if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+      for (int x = 0; x < RT; ++x)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          l[x][b] *= alpha[x][b];
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            pmid[x][gr][b] *= alpha[x][b];
+            ones[x][gr][b] *= alpha[x][b];
+          }
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            dst[16 * i] = Half16<T>::narrow(o[x][i][b] * inv2[b]);
-            dst[16 * i + 8] = Half16<T>::narrow(o[x][i][2 + b] * inv2[b]);
+            o[x][i][b] *= alpha[x][b];
+            o[x][i][2 + b] *= alpha[x][b];
+          }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {  // 16 keys each
+      // P^T fragments: p * step, and in masked pages what its rounding left (a
+      // row that sees a handful of keys has no other errors to average it with)
+      uint32_t bp[RT][NG][2], bq[RT][NG][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 sv[NG];  // step, centre
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          sv[gr] = Half16<T>::widen2(vpar[(16 * n + 8 * h) * NG + gr]);
+          sv[gr].y = fmaf(kCenter, sv[gr].x, sv[gr].y);
+        }
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+          float p[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float s = sc[n][x][2 * h + b];
+            p[b] = exp2_approx(fmaf(s - ref[x][b], cs[x][b], shift));
+            if (MASKED && s == -INFINITY) p[b] = 0.0f;
+            l[x][b] += p[b];
+          }
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            float q[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              float c = sv[gr].y;
+              q[b] = p[b] * sv[gr].x;
+              if (MASKED && p[b] == 0.0f) q[b] = c = 0.0f;  // tokens that are not there may hold anything
+              pmid[x][gr][b] = fmaf(p[b], c, pmid[x][gr][b]);
+            }
+            const uint32_t w = half2_bits(q[0], q[1]);
+            bp[x][gr][h] = transpose8(w);
+            if (MASKED) {
+              const float2 f = Half16<__half>::widen2(w);
+              bq[x][gr][h] = transpose8(half2_bits(q[0] - f.x, q[1] - f.y));
+            }
           }
         }
       }
-      const int row = tile * ROWS + 8 * x + g;
-      if (t == 0 && row < cu.q.rows && a.lse[rank]) {
-        const size_t at = (size_t)(cu.q.begin + row / a.share) * a.q_heads + head * a.share + row % a.share;
-        a.lse[rank][at] = l[x] == 0.0f ? -INFINITY : (mx[x] + log2f(l[x])) * 0.69314718055994531f;
+#pragma unroll
+      for (int x = 0; x < RT; ++x)
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          constexpr uint32_t one = 0x3c003c00u;
+          mma_16816(ones[x][gr], one, one, one, one, bp[x][gr][0], bp[x][gr][1]);
+          if (MASKED) mma_16816(ones[x][gr], one, one, one, one, bq[x][gr][0], bq[x][gr][1]);
+        }
+      // V codes of the lane's chunk of 4 tokens: words of (first, second) key
+      uint32_t v[2][2][JW / 2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int tok = 16 * n + 8 * h + (b ? kb : ka);
+          const char* row = blk + kv4_codes_bytes(D) + tok * (D / 2) + kv4_v_chunk(D, g, tok) * (D / 16);
+          if constexpr (JW == 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(row);
+            v[h][b][0] = w.x, v[h][b][1] = w.y;
+          } else {
+            v[h][b][0] = *reinterpret_cast<const uint32_t*>(row);
+          }
+        }
+#pragma unroll
+      for (int q4 = 0; q4 < MT / 2; ++q4) {  // two 16-channel tiles from each half word
+        const int w = q4 >> 1;
+        const uint32_t x0 = __byte_perm(v[0][0][w], v[0][1][w], (q4 & 1) ? 0x7632 : 0x5410);
+        const uint32_t x1 = __byte_perm(v[1][0][w], v[1][1][w], (q4 & 1) ? 0x7632 : 0x5410);
+        const uint32_t f0[4] = {code_pair<0>(x0), code_pair<1>(x0), code_pair<0>(x1), code_pair<1>(x1)};
+        const uint32_t f1[4] = {code_pair<2>(x0), code_pair<3>(x0), code_pair<2>(x1), code_pair<3>(x1)};
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+          const int g0 = 32 * q4 / G;
+          mma_16816(o[x][2 * q4], f0[0], f0[1], f0[2], f0[3], bp[x][g0][0], bp[x][g0][1]);
+          mma_16816(o[x][2 * q4 + 1], f1[0], f1[1], f1[2], f1[3], bp[x][g0][0], bp[x][g0][1]);
+          if (MASKED) {
+            mma_16816(o[x][2 * q4], f0[0], f0[1], f0[2], f0[3], bq[x][g0][0], bq[x][g0][1]);
+            mma_16816(o[x][2 * q4 + 1], f1[0], f1[1], f1[2], f1[3], bq[x][g0][0], bq[x][g0][1]);
+          }
+        }
       }
     }
   };
 
-  const float c_log2 = a.scale * 1.44269504088896341f;
+  // The final value of each accumulator: less the codes' 64 and 8, and with the
+  // fp32 part.  Leaves l summed over the keys' lanes, and mx as R.
+  auto settle = [&]() {
+#pragma unroll
+    for (int x = 0; x < RT; ++x)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (mx[x][b] != -INFINITY) mx[x][b] = fmaf(mx[x][b], cs[x][b], (float)(ex - 14));
+#pragma unroll
+        for (int m = 4; m < 32; m <<= 1) l[x][b] += __shfl_xor_sync(0xffffffffu, l[x][b], m);
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          float pm = pmid[x][gr][b];
+#pragma unroll
+          for (int m = 4; m < 32; m <<= 1) pm += __shfl_xor_sync(0xffffffffu, pm, m);
+          pm = fmaf(-(64.0f + kCenter), ones[x][gr][b], pm);
+#pragma unroll
+          for (int i = gr * G / 16; i < (gr + 1) * G / 16; ++i) {
+            o[x][i][b] += pm;
+            o[x][i][2 + b] += pm;
+          }
+        }
+      }
+  };
+  auto store_partial = [&](float* p) {
+#pragma unroll
+    for (int x = 0; x < RT; ++x)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int row = 8 * x + 2 * t + b;
+        if (g == 0) {
+          p[row] = mx[x][b];
+          p[ROWS + row] = l[x][b];
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          p[2 * ROWS + row * (D + 4) + 16 * i + g] = o[x][i][b];
+          p[2 * ROWS + row * (D + 4) + 16 * i + g + 8] = o[x][i][2 + b];
+        }
+      }
+  };
+  auto store_out = [&]() {
+    const DecSeq sq = cuc.q;
+    const int rh = cuc.seg / sq.tiles, tile = cuc.seg - rh * sq.tiles, rank = rh / kv.heads, head = rh - rank * kv.heads;
+#pragma unroll
+    for (int x = 0; x < RT; ++x)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int row = tile * ROWS + 8 * x + 2 * t + b;
+        if (row >= sq.rows) continue;
+        const float inv = l[x][b] == 0.0f ? 0.0f : __frcp_rn(l[x][b]);
+        const size_t at = (size_t)(sq.begin + row / a.share) * a.q_heads + head * a.share + row % a.share;
+        uint16_t* dst = static_cast<uint16_t*>(a.out[rank]) + at * D + g;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          dst[16 * i] = Half16<T>::narrow(o[x][i][b] * inv);
+          dst[16 * i + 8] = Half16<T>::narrow(o[x][i][2 + b] * inv);
+        }
+        if (g == 0 && a.lse[rank])
+          a.lse[rank][at] = l[x][b] == 0.0f ? -INFINITY : (mx[x][b] + log2f(l[x][b])) * 0.69314718055994531f;
+      }
+  };
+
   float* part_ws = reinterpret_cast<float*>(a.ws + 1024);
   float* head_ws = part_ws + (size_t)kDecMaxCtas * 2 * SLOT + ((size_t)cta * W + warp) * SLOT;
 
   if (count > 0) {
-    seek(ld);
-    cu = ld;
-    int issued = 0;
-    for (; issued < S && issued < count; ++issued) {
-      issue(issued);
-      step(ld);
+    long long seg_begin;  // first unit of the open segment
+    int left;             // its units still to come
+    int key0;             // first key of its next page
+    {
+      const int j = s_page[warp];
+      const DecSeq q = ldc.q;
+      ld_open();
+      ld_slot += j;
+      seg_begin = u0 - j;
+      left = q.pages - j;
+      key0 = (q.page0 + j) * kKv4Page;
     }
+    int issued = 0;
+    for (; issued < S && issued < count; ++issued) issue(issued);
     bool fresh = true, alive = true;
-    long long seg_begin = u0 - cu.j;  // first unit of the open segment
-    int i = 0;
+    int st = 0, i = 0;
+    uint32_t parity = 0;
     for (; i < count; ++i) {
-      const int st = i % S;
       if (fresh) {
         open();
         fresh = false;
       }
-      if (!wait(st, (uint32_t)(i / S) & 1u)) {
+      if (!wait(st, parity)) {
         alive = false;
         break;
       }
       if (!((missing >> st) & 1u)) {
         const char* blk = ring + (size_t)st * BLK;
-        const int key0 = (cu.q.page0 + cu.j) * kKv4Page;
-        const bool masked = key0 + kKv4Page - 1 > tile_hi || key0 < tile_lo;
-        const int sw = D == 128 ? (t & 1) : (t >> 1);             // the quad's pair of keys, in the order
-        const int ka = 2 * t + sw, kb = 2 * t + 1 - sw;           // in which the V rows' banks differ
-        const int kg = D == 128 ? g ^ ((g >> 1) & 1) : g ^ (g >> 2);  // and the key of column g
-        float sc[8][2 * RT];
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {  // 8 keys each
-          uint32_t w[JW];
-          const char* row = blk + (8 * n + kg) * (D / 2) + t * (JW * 4);
-          if constexpr (JW == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(row);
-            w[0] = v.x, w[1] = v.y;
-          }
-          float acc[NG][4] = {};
-#pragma unroll
-          for (int j = 0; j < JW; ++j) {
-            float* d = acc[32 * j / G];
-            mma_16816<FP16>(d, qf[2 * j][0], RT > 1 ? qf[2 * j][2 * RT - 2] : 0u, qf[2 * j][1],
-                            RT > 1 ? qf[2 * j][2 * RT - 1] : 0u, unpack_pair<FP16, 0>(w[j]), unpack_pair<FP16, 1>(w[j]));
-            mma_16816<FP16>(d, qf[2 * j + 1][0], RT > 1 ? qf[2 * j + 1][2 * RT - 2] : 0u, qf[2 * j + 1][1],
-                            RT > 1 ? qf[2 * j + 1][2 * RT - 1] : 0u, unpack_pair<FP16, 2>(w[j]),
-                            unpack_pair<FP16, 3>(w[j]));
-          }
-          const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D));
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const uint32_t* pk = par + (8 * n + (b ? kb : ka)) * NG;
-            float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              const float2 sl = Half16<T>::widen2(pk[gr]);  // step, lo
-              const float lo = fmaf(-unpack_bias<FP16>(), sl.x, sl.y);
-              s0 = fmaf(sl.x, acc[gr][b], fmaf(lo, qsum[0][gr], s0));
-              if (RT > 1) s1 = fmaf(sl.x, acc[gr][2 + b], fmaf(lo, qsum[RT - 1][gr], s1));
-            }
-            sc[n][b] = s0 * c_log2;
-            if (RT > 1) sc[n][2 + b] = s1 * c_log2;
-            if (masked) {
-              const int pos = key0 + 8 * n + (b ? kb : ka);
-#pragma unroll
-              for (int x = 0; x < RT; ++x)
-                if (pos > lim_hi[x] || pos < lim_lo[x]) sc[n][2 * x + b] = -INFINITY;
-            }
-          }
-        }
-        // the running maximum; the sums so far are rescaled where it grew
-        bool grew = false;
-        float alpha[RT];
-#pragma unroll
-        for (int x = 0; x < RT; ++x) {
-          float m = mx[x];
-#pragma unroll
-          for (int n = 0; n < 8; ++n) m = fmaxf(m, fmaxf(sc[n][2 * x], sc[n][2 * x + 1]));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          alpha[x] = m > mx[x] ? exp2_approx(mx[x] - m) : 1.0f;
-          grew |= m > mx[x];
-          mx[x] = m;
-        }
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-          for (int x = 0; x < RT; ++x) {
-            l[x] *= alpha[x];
-            const float a0 = __shfl_sync(0xffffffffu, alpha[x], 8 * t), a1 = __shfl_sync(0xffffffffu, alpha[x], 8 * t + 4);
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              pmid[x][gr] *= alpha[x];
-              ones[x][gr][0] *= a0;
-              ones[x][gr][1] *= a1;
-            }
-#pragma unroll
-            for (int i2 = 0; i2 < MT; ++i2) {
-              o[x][i2][0] *= a0;
-              o[x][i2][1] *= a1;
-              o[x][i2][2] *= a0;
-              o[x][i2][3] *= a1;
-            }
-          }
-        }
-        const uint32_t* vpar = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D) + kv4_params_bytes(D, G));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // 16 keys each
-          uint32_t bh[RT][NG][2], bl[RT][NG][2];  // P^T fragments: p * step in bf16, and (fp16) what that leaves
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t* pa = vpar + (16 * k + 8 * h + ka) * NG;
-            const uint32_t* pb = vpar + (16 * k + 8 * h + kb) * NG;
-            float2 va[NG], vb[NG];  // step, centre
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              va[gr] = Half16<T>::widen2(pa[gr]);
-              vb[gr] = Half16<T>::widen2(pb[gr]);
-              va[gr].y = fmaf(kCenter, va[gr].x, va[gr].y);
-              vb[gr].y = fmaf(kCenter, vb[gr].x, vb[gr].y);
-            }
-#pragma unroll
-            for (int x = 0; x < RT; ++x) {
-              const float mu = mx[x] == -INFINITY ? 0.0f : mx[x];
-              const float p0 = exp2_approx(sc[2 * k + h][2 * x] - mu), p1 = exp2_approx(sc[2 * k + h][2 * x + 1] - mu);
-              l[x] += p0 + p1;
-#pragma unroll
-              for (int gr = 0; gr < NG; ++gr) {
-                float q0 = p0 * va[gr].x, q1 = p1 * vb[gr].x, c0 = p0 * va[gr].y, c1 = p1 * vb[gr].y;
-                if (masked) {  // rows that hold no token may hold anything
-                  if (p0 == 0.0f) q0 = c0 = 0.0f;
-                  if (p1 == 0.0f) q1 = c1 = 0.0f;
-                }
-                pmid[x][gr] += c0 + c1;
-                bh[x][gr][h] = Half16<__nv_bfloat16>::narrow2(q0, q1);
-                if (FP16) {
-                  const float2 f = Half16<__nv_bfloat16>::widen2(bh[x][gr][h]);
-                  bl[x][gr][h] = Half16<__nv_bfloat16>::narrow2(q0 - f.x, q1 - f.y);
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < RT; ++x)
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              constexpr uint32_t one = 0x3f803f80u;
-              mma_16816<false>(ones[x][gr], one, one, one, one, bh[x][gr][0], bh[x][gr][1]);
-              if (FP16) mma_16816<false>(ones[x][gr], one, one, one, one, bl[x][gr][0], bl[x][gr][1]);
-            }
-          // V codes of the lane's chunk of 4 tokens: words of (first, second) key
-          uint32_t v[2][2][JW / 2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const int tok = 16 * k + 8 * h + (b ? kb : ka);
-              const char* row = blk + kv4_codes_bytes(D) + tok * (D / 2) + kv4_v_chunk(D, g, tok) * (D / 16);
-              if constexpr (JW == 4) {
-                const uint2 w = *reinterpret_cast<const uint2*>(row);
-                v[h][b][0] = w.x, v[h][b][1] = w.y;
-              } else {
-                v[h][b][0] = *reinterpret_cast<const uint32_t*>(row);
-              }
-            }
-#pragma unroll
-          for (int q4 = 0; q4 < MT / 2; ++q4) {  // two 16-channel tiles from each half word
-            const int w = q4 >> 1;
-            const uint32_t x0 = __byte_perm(v[0][0][w], v[0][1][w], (q4 & 1) ? 0x7632 : 0x5410);
-            const uint32_t x1 = __byte_perm(v[1][0][w], v[1][1][w], (q4 & 1) ? 0x7632 : 0x5410);
-            const uint32_t f0[4] = {unpack_pair<false, 0>(x0), unpack_pair<false, 1>(x0), unpack_pair<false, 2>(x0),
-                                    unpack_pair<false, 3>(x0)};
-            const uint32_t f1[4] = {unpack_pair<false, 0>(x1), unpack_pair<false, 1>(x1), unpack_pair<false, 2>(x1),
-                                    unpack_pair<false, 3>(x1)};
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int i2 = 2 * q4 + y, gr = 16 * i2 / G;
-#pragma unroll
-              for (int x = 0; x < RT; ++x) {
-                mma_16816<false>(o[x][i2], f0[2 * y], f0[2 * y + 1], f1[2 * y], f1[2 * y + 1], bh[x][gr][0], bh[x][gr][1]);
-                if (FP16)
-                  mma_16816<false>(o[x][i2], f0[2 * y], f0[2 * y + 1], f1[2 * y], f1[2 * y + 1], bl[x][gr][0],
-                                   bl[x][gr][1]);
-              }
-            }
-          }
-        }
+        if (key0 + kKv4Page - 1 > tile_hi || key0 < tile_lo) page_pass(std::true_type{}, blk, key0);
+        else page_pass(std::false_type{}, blk, key0);
       }
       __syncwarp();  // every lane has read the stage
       if (issued < count) {
         issue(st);
-        step(ld);
         ++issued;
       }
-      if (cu.j + 1 == cu.q.pages || i + 1 == count) {  // the segment, or the range, ends
+      key0 += kKv4Page;
+      const bool ends = --left == 0;
+      if (ends || i + 1 == count) {  // the segment, or the range, ends
         settle();
-        const bool whole = seg_begin >= u0, ends = cu.j + 1 == cu.q.pages;
-        if (whole && ends) {
+        const DecSeq sq = cuc.q;
+        if (seg_begin >= u0 && ends) {
           store_out();
         } else {
           const int which = 2 * warp + (ends ? 0 : 1);
           if (ends) store_partial(head_ws);
           if (lane == 0) {
             s_seg[which][0] = seg_begin;
-            s_seg[which][1] = seg_begin + cu.q.pages;
-            s_who[which][0] = cu.s;
-            s_who[which][1] = cu.seg / cu.q.tiles;
-            s_who[which][2] = cu.seg % cu.q.tiles;
+            s_seg[which][1] = seg_begin + sq.pages;
+            const int rh = cuc.seg / sq.tiles;
+            s_who[which][0] = rh / kv.heads;
+            s_who[which][1] = rh % kv.heads;
+            s_who[which][2] = (cuc.seg - rh * sq.tiles) * ROWS;
+            s_who[which][3] = sq.rows;
+            s_who[which][4] = sq.begin;
           }
         }
-        if (ends) {
-          seg_begin += cu.q.pages;
+        if (ends && i + 1 < count) {
+          seg_begin += sq.pages;
+          next_segment(cuc);
+          left = cuc.q.pages;
+          key0 = cuc.q.page0 * kKv4Page;
           fresh = true;
         }
       }
-      if (i + 1 < count) step(cu);
+      if (++st == S) {
+        st = 0;
+        parity ^= 1u;
+      }
     }
     if (!alive)  // a copy never came: wait (bounded) for the others in flight, then leave
       for (int k = i + 1; k < issued; ++k) wait(k % S, (uint32_t)(k / S) & 1u);
@@ -663,47 +828,75 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
   // ---- join what the warps left open
   __syncthreads();  // every ring has been read
   float* tails = reinterpret_cast<float*>(dec_smem);
-  if (count > 0 && s_seg[2 * warp + 1][0] >= 0) store_partial(tails + (size_t)warp * SLOT);
+  float* parts = part_ws + (size_t)cta * 2 * SLOT;  // of the segment open at the CTA's begin, and at its end
+  const float* heads = part_ws + (size_t)kDecMaxCtas * 2 * SLOT + (size_t)cta * W * SLOT;
+  if (count > 0 && s_seg[2 * warp + 1][0] >= 0) {
+    // a tail that no other warp of the CTA shares goes straight to its place
+    const long long first = s_seg[2 * warp + 1][0];
+    const bool alone = u1 == c1 && s_seg[2 * warp + 1][1] > c1 && (first >= u0 || u0 == c0);
+    store_partial(alone ? parts + (first < c0 ? 0 : 1) * SLOT : tails + (size_t)warp * SLOT);
+  }
+  if (threadIdx.x < 2) s_open[threadIdx.x] = 0;
   __syncthreads();
   int* counters = reinterpret_cast<int*>(a.ws);
-  const float* heads = part_ws + (size_t)kDecMaxCtas * 2 * SLOT + (size_t)cta * W * SLOT;
-  int m0 = 0;
+  int open_at[2] = {-1, -1};
+  int m0 = 0, flip = 0;
   while (true) {
     while (m0 < 2 * W && s_seg[m0][0] < 0) ++m0;
     if (m0 >= 2 * W) break;
     const long long first = s_seg[m0][0], end = s_seg[m0][1];
-    int list[W + 1], n = 0, m1 = m0;  // the segment's partials, in order
+    int n = 0, m1 = m0;  // the segment's partials, in order
     for (; m1 < 2 * W; ++m1) {
       if (s_seg[m1][0] < 0) continue;
-      if (s_seg[m1][0] != first || n > W) break;
-      list[n++] = m1;
+      if (s_seg[m1][0] != first) break;
+      if (threadIdx.x == 0) s_list[flip][n] = m1;
+      ++n;
     }
-    const int seq = s_who[m0][0], rh = s_who[m0][1], tile = s_who[m0][2];
-    const DecSeq q = dec_seq(kv, a, seq, ROWS);
-    auto local = [&](int i) { return (list[i] & 1) ? tails + (size_t)(list[i] >> 1) * SLOT : heads + (size_t)(list[i] >> 1) * SLOT; };
+    __syncthreads();
+    const int* list = s_list[flip];
+    auto local = [&](int i) {
+      const int m = list[i];
+      return (m & 1) ? tails + (size_t)(m >> 1) * SLOT : heads + (size_t)(m >> 1) * SLOT;
+    };
     if (first >= c0 && end <= c1) {
-      dec_join<T, D, ROWS>(a, n, local, nullptr, rh / kv.heads, rh % kv.heads, tile * ROWS, q.rows, q.begin);
+      dec_join<T, D, ROWS>(a, n, local, nullptr, s_who[m0][0], s_who[m0][1], s_who[m0][2], s_who[m0][3], s_who[m0][4]);
     } else {
-      dec_join<T, D, ROWS>(a, n, local, part_ws + ((size_t)cta * 2 + (first < c0 ? 0 : 1)) * SLOT, 0, 0, 0, 0, 0);
-      // the CTAs whose ranges hold its first and its last unit
-      const int f = (int)(((first + 1) * C - 1) / units), e = (int)((end * C - 1) / units);
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const int old = atomicAdd(&counters[f], 1);
-        s_last = old == e - f;
-        if (old == e - f) counters[f] = 0;  // as it was found
-        __threadfence();
-      }
-      __syncthreads();
-      if (s_last) {
-        auto remote = [&](int i) { return part_ws + ((size_t)(f + i) * 2 + (i == 0 ? 1 : 0)) * SLOT; };
-        dec_join<T, D, ROWS>(a, e - f + 1, remote, nullptr, rh / kv.heads, rh % kv.heads, tile * ROWS, q.rows, q.begin);
-      }
-      __syncthreads();
+      const int side = first < c0 ? 0 : 1;
+      open_at[side] = m0;
+      if (!(n == 1 && (m0 & 1) && end > c1))
+        dec_join<T, D, ROWS>(a, n, local, parts + side * SLOT, 0, 0, 0, 0, 0);
     }
+    flip ^= 1;
     m0 = m1;
   }
+  if (open_at[0] < 0 && open_at[1] < 0) return;
+  // the CTA that comes last to an open segment joins its parts, in CTA order
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    const int side = (int)threadIdx.x;
+    s_last[side] = 0;
+    if (open_at[side] >= 0) {
+      // the CTAs whose ranges hold its first and its last unit
+      const long long first = s_seg[open_at[side]][0], end = s_seg[open_at[side]][1];
+      const int f = (int)(((first + 1) * C - 1) / units), e = (int)((end * C - 1) / units);
+      __threadfence();
+      const int old = atomicAdd(&counters[f], 1);
+      if (old == e - f) {
+        counters[f] = 0;  // as it was found
+        s_last[side] = e - f + 1;
+        s_open[side] = f;
+      }
+      __threadfence();
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+    if (s_last[side]) {
+      const int f = s_open[side], m = open_at[side];
+      auto remote = [&](int i) { return part_ws + ((size_t)(f + i) * 2 + (i == 0 ? 1 : 0)) * SLOT; };
+      dec_join<T, D, ROWS>(a, s_last[side], remote, nullptr, s_who[m][0], s_who[m][1], s_who[m][2], s_who[m][3], s_who[m][4]);
+    }
 }
 
 }  // namespace dcc
