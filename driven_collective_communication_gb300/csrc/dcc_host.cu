@@ -26,7 +26,7 @@
 #include "sync_kernels.cuh"
 
 namespace dcc {  // kernels of the calls without a communicator, for visit_kernels
-const void* linear_kernel(bool fp16);
+const void* linear_kernel(int which);
 const void* kv4_row_kernel(bool fp16, bool read, int dim, int group);
 const void* kv4_attention_kernel(bool fp16, int dim, int group, int which);
 const void* kv4_pages_kernel(int i);
@@ -360,7 +360,6 @@ bool visit_kernels(F&& visit) {
         !v(dcc::linear_allreduce_mma_kernel(n, 2, dcc::kMmaThreads, true)))
       return false;
   for (int fp16 = 0; fp16 < 2; ++fp16) {
-    if (!v(dcc::linear_kernel(fp16))) return false;
     for (int dim = 64; dim <= 128; dim += 64)
       for (int group = 32; group <= 64; group += 32)
         if (!v(dcc::kv4_row_kernel(fp16, false, dim, group)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group)) ||
@@ -368,7 +367,7 @@ bool visit_kernels(F&& visit) {
           return false;
   }
   for (int i = 0; i < 3; ++i)
-    if (!v(dcc::kv4_pages_kernel(i))) return false;
+    if (!v(dcc::kv4_pages_kernel(i)) || !v(dcc::linear_kernel(i))) return false;
   return v(dcc::ring_barrier_kernel()) && v(dcc::ring_barrier_cluster_kernel()) && v(dcc::channel_put_kernel()) &&
          v(dcc::channel_get_kernel());
 }

@@ -57,7 +57,7 @@ struct Kv4Dev {
   int32_t* len;    // [seqs]
   int32_t* refs;   // [pages] (page calls only)
   int n, layers, pages, seqs, max_pages, heads;
-  unsigned long long* status;  // first failure, 0 = none
+  unsigned long long* status;  // first number out of range, first wait that gave up; 0 = none
 };
 
 template <typename T>
@@ -120,7 +120,7 @@ __device__ __forceinline__ int kv4_seq_of(const int32_t* start, int seqs, int ro
 }  // namespace dcc
 
 namespace dcc_host {
-// Status word of the calls that use no communicator, on the current device
+// Status words (two) of the calls that use no communicator, on the current device
 // (ops_status.cu); null after a CUDA error.
 unsigned long long* local_status();
 // Checks a cache descriptor and makes its device view, without any CUDA call;

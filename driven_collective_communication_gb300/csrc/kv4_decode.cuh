@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
     for (unsigned it = 1;; ++it) {
       if (mbar_try_wait(&bars[warp][st], parity)) return true;
       if ((it & 15u) == 0 && global_timer_ns() - t0 > a.timeout_ns) {
-        atomicCAS(kv.status, 0ull, pack_status(kStatusTimeout, 0, 0, cta));
+        atomicCAS(kv.status + 1, 0ull, pack_status(kStatusTimeout, 0, 0, cta));
         return false;
       }
     }

@@ -8,8 +8,10 @@
 #include "kv4.cuh"
 
 namespace {
-// one word per device; its address comes from cudaGetSymbolAddress
-static __device__ unsigned long long g_local_status;
+// Two words per device: numbers out of range, and waits that gave up (a wait
+// of the linear layer gives up at once when the second is set).  The address
+// comes from cudaGetSymbolAddress.
+static __device__ unsigned long long g_local_status[2];
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 unsigned long long* g_addr[kMaxDevices];
@@ -92,18 +94,18 @@ int dcc_kv4_block_bytes(int head_dim, int group, size_t* bytes) {
 int dcc_local_check(dcc_stream_t s) {
   unsigned long long* p = dcc_host::local_status();
   if (!p) return DCC_ERR_CUDA;
-  unsigned long long st = 0;
+  unsigned long long st[2] = {0, 0};
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(s)) != cudaSuccess ||
-      cudaMemcpy(&st, p, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) {
+      cudaMemcpy(st, p, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) {
     cudaGetLastError();
     return DCC_ERR_CUDA;
   }
-  if (st == 0) return DCC_OK;
+  if (st[0] == 0 && st[1] == 0) return DCC_OK;
   if (cudaMemset(p, 0, sizeof st) != cudaSuccess) {
     cudaGetLastError();
     return DCC_ERR_CUDA;
   }
-  return (st & 0xffull) == dcc::kStatusTimeout ? DCC_ERR_TIMEOUT : DCC_ERR_BOUNDS;
+  return (st[1] & 0xffull) == dcc::kStatusTimeout ? DCC_ERR_TIMEOUT : DCC_ERR_BOUNDS;
 }
 
 }  // extern "C"

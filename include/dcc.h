@@ -672,8 +672,9 @@ int dcc_linear(int n_ranks, void* const* weight, void* const* x, void* const* bi
 /* Synchronise the stream and report what the calls of this section recorded
  * on the current device since the last check: DCC_OK, DCC_ERR_BOUNDS (a
  * sequence or page number out of range; the access was skipped) or
- * DCC_ERR_TIMEOUT (a wait inside a kernel gave up; its outputs are not
- * complete).  Clears the record. */
+ * DCC_ERR_TIMEOUT (a wait inside a kernel gave up; its outputs and those of
+ * calls since are not complete, and attention workspaces want zeroing again).
+ * Clears the record. */
 int dcc_local_check(dcc_stream_t s);
 
 #ifdef __cplusplus
