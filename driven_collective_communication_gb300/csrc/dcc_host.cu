@@ -363,7 +363,8 @@ bool visit_kernels(F&& visit) {
     for (int dim = 64; dim <= 128; dim += 64)
       for (int group = 32; group <= 64; group += 32)
         if (!v(dcc::kv4_row_kernel(fp16, false, dim, group)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group)) ||
-            !v(dcc::kv4_attention_kernel(fp16, dim, group, 1)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 2)))
+            !v(dcc::kv4_attention_kernel(fp16, dim, group, 1)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 2)) ||
+            !v(dcc::kv4_attention_kernel(fp16, dim, group, 3)))
           return false;
   }
   for (int i = 0; i < 3; ++i)

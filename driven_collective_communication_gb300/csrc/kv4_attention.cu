@@ -1,6 +1,6 @@
 // kv4_attention.cu -- host side of the attention over the 4-bit cache.
 #include "comm.h"
-#include "kv4_decode.cuh"
+#include "kv4_prompt.cuh"
 
 namespace dcc {
 namespace {
@@ -23,9 +23,30 @@ Kernel decode(bool fp16, int dim, int group, int tiles) {
   if (tiles > 1) return fp16 ? decode_for<__half, 2>(dim, group) : decode_for<__nv_bfloat16, 2>(dim, group);
   return fp16 ? decode_for<__half, 1>(dim, group) : decode_for<__nv_bfloat16, 1>(dim, group);
 }
+template <typename T, int D, int G>
+Kernel prompt_of() {
+  return {(const void*)&k_kv4_prompt<T, D, G>, kPromptThreads, PromptShape<D, G>::smem};
+}
+template <typename T>
+Kernel prompt_for(int dim, int group) {
+  if (dim == 128) return group == 64 ? prompt_of<T, 128, 64>() : prompt_of<T, 128, 32>();
+  return group == 64 ? prompt_of<T, 64, 64>() : prompt_of<T, 64, 32>();
+}
+Kernel prompt(bool fp16, int dim, int group) {
+  return fp16 ? prompt_for<__half>(dim, group) : prompt_for<__nv_bfloat16>(dim, group);
+}
 }  // namespace
-const void* kv4_attention_kernel(bool fp16, int dim, int group, int which) { return decode(fp16, dim, group, which).fn; }
+// which: 1 or 2 row tiles of the streaming kernel, 3 the prompt kernel
+const void* kv4_attention_kernel(bool fp16, int dim, int group, int which) {
+  return which == 3 ? prompt(fp16, dim, group).fn : decode(fp16, dim, group, which).fn;
+}
 }  // namespace dcc
+
+namespace {
+// Query rows per kv head (new tokens x the heads that share it) above which
+// the prompt kernel runs.
+constexpr long long kPromptMinRows = 64;
+}  // namespace
 
 extern "C" {
 
@@ -92,11 +113,27 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
     cudaGetLastError();
     return DCC_ERR_CUDA;
   }
-  const dcc::Kernel k = dcc::decode(kv->dtype == DCC_FP16, kv->head_dim, kv->group, max_new * a.share > 8 ? 2 : 1);
+  const bool fp16 = kv->dtype == DCC_FP16;
+  const long long rows = (long long)max_new * a.share;
+  cudaStream_t st = static_cast<cudaStream_t>(s);
+  if (rows > kPromptMinRows) {
+    const dcc::Kernel k = dcc::prompt(fp16, kv->head_dim, kv->group);
+    if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
+    const long long grid = (rows + dcc::kPromptRows - 1) / dcc::kPromptRows * kv->n_ranks * kv->kv_heads * kv->seqs;
+    if (grid > 0x7fffffffll) return DCC_ERR_INVALID_ARG;
+    dcc::DevComm dc{};
+    dc.n = kv->n_ranks;
+    dc.skip_signal_rank = -1;
+    dc.timeout_ns = a.timeout_ns;
+    dc.status = d.status + 1;
+    void* args[] = {&d, &a, &dc};
+    return dcc_host::launch(k.fn, (int)grid, k.threads, false, args, st, k.smem, true);
+  }
+  const dcc::Kernel k = dcc::decode(fp16, kv->head_dim, kv->group, rows > 8 ? 2 : 1);
   if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
   void* args[] = {&d, &a};
-  return dcc_host::launch(k.fn, sms < dcc::kDecMaxCtas ? sms : dcc::kDecMaxCtas, k.threads, false, args,
-                          static_cast<cudaStream_t>(s), k.smem, true);
+  return dcc_host::launch(k.fn, sms < dcc::kDecMaxCtas ? sms : dcc::kDecMaxCtas, k.threads, false, args, st, k.smem,
+                          true);
 }
 
 }  // extern "C"

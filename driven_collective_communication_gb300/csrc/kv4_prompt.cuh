@@ -1,0 +1,483 @@
+// kv4_prompt.cuh -- attention of many query rows over the 4-bit paged cache
+// (prompt chunks), on the fifth-generation tensor cores.
+//
+// With hundreds of query rows per kv head the products outweigh the cache's
+// bytes: bound by the tensor cores and, as closely, by the exponentials (128
+// keys x 256 rows take 2048 clocks of either on an SM).  A CTA owns 256 query
+// rows of one (sequence, rank, kv head) -- new tokens times the heads that
+// share it -- as two tiles of 128, and walks the keys in steps of 128 (two
+// pages).  The pages are unpacked once per step into 16-bit tiles in shared
+// memory, for both row tiles: K_j and V_j = lo + step * code, rounded once to
+// the cache's type (2^-9 or 2^-12 of a value whose own 4-bit step is a
+// fifteenth of its group's range).  Then per row tile
+//   S = Q K^T            tcgen05, Q and K in shared memory, S in tensor memory;
+//   P = 2^(c S - ref)    fp32, rounded to 16 bits, over S in tensor memory;
+//   O += P V             tcgen05, P in tensor memory, V^T in shared memory.
+// ref is a row's reference: it follows the running maximum only when that
+// grew by more than 2^8 (then O is rescaled in tensor memory), which is rare
+// after the first steps; sums l are fp32, of the unrounded P.  While one row
+// tile's P is made, the tensor cores work on the other's.
+//
+// Roles (448 threads): warp 0 loads pages (one bulk copy each, three in
+// flight); warp 1 issues the MMAs; warps 2..5 unpack; warps 6..9 and 10..13
+// make P of the two row tiles, one row per thread.
+//
+// K is unpacked in the order the codes have (channels e, e + 4 of a word side
+// by side), and Q's channels are put in the same order; V is unpacked
+// transposed, eight keys of a channel to a 16-byte store, so both operands are
+// K-major with the 128-byte swizzle.
+//
+// A key that no row may see (past the sequence, a missing page) has V = 0, and
+// its scores are replaced, not multiplied.  A V row that holds NaN or infinity
+// becomes 0 there and makes its K NaN instead, so that rows that see the key
+// get NaN and the others nothing.
+#pragma once
+#include "fused_mma.cuh"
+#include "kv4_decode.cuh"
+#include "tcgen05.cuh"
+
+namespace dcc {
+
+constexpr int kPromptThreads = 448;
+constexpr int kPromptRows = 256;  // per CTA: two tiles of 128
+constexpr int kPromptRing = 3;    // pages in flight
+
+template <int D, int G>
+struct PromptShape {
+  static constexpr int q_tile = 128 * D * 2;     // one row tile of Q
+  static constexpr int kv_tile = 128 * D * 2;    // K, or V^T, of 128 keys
+  static constexpr int block = kv4_block_bytes(D, G);
+  static constexpr size_t smem = 1024 + 2 * q_tile + 4 * kv_tile + kPromptRing * block + 256;
+};
+
+// Arithmetic on two 16-bit values of the cache's type, codes as biased numbers.
+template <typename T>
+struct Pair16;
+template <>
+struct Pair16<__half> {
+  static constexpr uint32_t kExp = 0x7c00u;
+  template <int P>
+  __device__ static uint32_t code(uint32_t w) {  // 64 + nibbles P, P + 4
+    return code_pair<P>(w);
+  }
+  __device__ static uint32_t value(uint32_t c, uint32_t step, uint32_t lo) {  // lo + step * code, one rounding
+    const uint32_t bias = 0x54005400u;
+    const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&bias));
+    const __half2 r = __hfma2(n, *reinterpret_cast<const __half2*>(&step), *reinterpret_cast<const __half2*>(&lo));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+template <>
+struct Pair16<__nv_bfloat16> {
+  static constexpr uint32_t kExp = 0x7f80u;
+  template <int P>
+  __device__ static uint32_t code(uint32_t w) {  // 128 + nibbles P, P + 4
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * P)), "r"(0x000f000fu), "r"(0x43004300u));
+    return r;
+  }
+  __device__ static uint32_t value(uint32_t c, uint32_t step, uint32_t lo) {
+    const uint32_t bias = 0x43004300u;
+    const __nv_bfloat162 n = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), *reinterpret_cast<const __nv_bfloat162*>(&bias));
+    const __nv_bfloat162 r = __hfma2(n, *reinterpret_cast<const __nv_bfloat162*>(&step), *reinterpret_cast<const __nv_bfloat162*>(&lo));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+// a (step, lo) pair neither of which may be NaN or infinite
+template <typename T>
+__device__ __forceinline__ bool param_finite(uint32_t w) {
+  constexpr uint32_t e = Pair16<T>::kExp;
+  return (w & e) != e && ((w >> 16) & e) != e;
+}
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, const __grid_constant__ AttnArgs a, DevComm dc) {
+  using Shape = PromptShape<D, G>;
+  constexpr bool FP16 = std::is_same<T, __half>::value;
+  constexpr int NG = D / G, BLK = Shape::block, R = kPromptRing, JW = D / 32;
+  constexpr float kShift = 6.0f;  // P is 2^6 times what ref says: fp16 keeps it normal down to 2^-20
+  extern __shared__ unsigned char prompt_raw[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t s_absent[8];  // by step: bits of pages that are not there
+  const uint32_t base = (smem_addr_u32(prompt_raw) + 1023u) & ~1023u;
+  const uint32_t sq = base, sk = sq + 2 * Shape::q_tile, sv = sk + 2 * Shape::kv_tile, raw = sv + 2 * Shape::kv_tile;
+  const unsigned char* raw_g = prompt_raw + (raw - smem_addr_u32(prompt_raw));
+  const uint32_t bars = raw + (uint32_t)(R * BLK);
+  auto rawf = [&](int s) { return bars + 8u * (uint32_t)s; };
+  auto rawe = [&](int s) { return bars + 8u * (uint32_t)(R + s); };
+  auto two = [&](int kind, int i) { return bars + 8u * (uint32_t)(2 * R + 2 * kind + i); };
+  enum { kFull = 0, kFree, vFull, vFree, sFull, pFull, pvDone, qFull };  // the last: one for both
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R; ++i) {
+      mma_mbar_init(rawf(i), 1);
+      mma_mbar_init(rawe(i), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mma_mbar_init(two(kFull, i), 4);
+      mma_mbar_init(two(kFree, i), 1);
+      mma_mbar_init(two(vFull, i), 4);
+      mma_mbar_init(two(vFree, i), 1);
+      mma_mbar_init(two(sFull, i), 1);
+      mma_mbar_init(two(pFull, i), 4);
+      mma_mbar_init(two(pvDone, i), 1);
+      mma_mbar_init(two(qFull, i), 4);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_prologue();
+
+  // ---- this CTA's rows; the last tiles (the most keys) come first
+  const int nh = kv.n * kv.heads, per = nh * kv.seqs;
+  const int turn = (int)blockIdx.x / per, rest = (int)blockIdx.x % per, seq = rest / nh, rh = rest % nh;
+  const int rank = rh / kv.heads, head = rh % kv.heads;
+  const DecSeq q = dec_seq(kv, a, seq, kPromptRows);
+  const int tile = q.tiles - 1 - turn;
+  if (tile < 0) return;
+  const int row_lo = tile * kPromptRows, row_hi = min(q.rows, row_lo + kPromptRows);  // rows of this CTA
+  const int pos_lo = q.pos0 + row_lo / a.share, pos_hi = q.pos0 + (row_hi - 1) / a.share;
+  const int key_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
+  const int page0 = key_lo / kKv4Page;
+  // one page past the row at most: it is reported there
+  const int pages = pos_hi < 0 ? 0 : min(pos_hi / kKv4Page, kv.max_pages) - page0 + 1;
+  const int steps = (pages + 1) / 2;
+  const int nt = row_hi - row_lo > 128 ? 2 : 1;
+  if (steps <= 0) {  // nothing to see
+    for (int i = threadIdx.x; i < (row_hi - row_lo) * (D / 8); i += kPromptThreads) {
+      const int row = row_lo + i / (D / 8);
+      const size_t at = (size_t)(q.begin + row / a.share) * a.q_heads + head * a.share + row % a.share;
+      *reinterpret_cast<uint4*>(static_cast<T*>(a.out[rank]) + at * D + i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+      if (i % (D / 8) == 0 && a.lse[rank]) a.lse[rank][at] = -INFINITY;
+    }
+    return;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr_u32(&tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;  // S / P of the two row tiles, then O: 128 columns each
+  auto wait = [&](uint32_t bar, int phase) { return mma_mbar_wait(bar, (uint32_t)phase & 1u, dc, rank, head); };
+
+  if (warp == 0) {  // ---- loads
+    int ids = -1, ids_at = -(1 << 30), unfinished = 0;
+    for (int p = 0; p < 2 * steps; ++p) {
+      if (p - ids_at >= 32) {
+        ids_at = p;
+        ids = p + lane < pages ? kv4_page(kv, seq, page0 + p + lane) : -1;
+      }
+      const int page = __shfl_sync(0xffffffffu, ids, p - ids_at), slot = p % R;
+      if (p >= R && !wait(rawe(slot), p / R - 1)) break;
+      if (lane == 0) {
+        uint32_t& absent = s_absent[(p / 2) & 7];
+        absent = (p & 1 ? absent : 0u) | (page < 0 ? 1u << (p & 1) : 0u);
+        mma_mbar_expect(rawf(slot), page < 0 ? 0u : (uint32_t)BLK);
+        if (page >= 0)
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  raw + (uint32_t)(slot * BLK)),
+              "l"(kv4_block(kv, rank, a.layer, page, head, BLK)), "r"((uint32_t)BLK), "r"(rawf(slot))
+              : "memory");
+      }
+      ++unfinished;
+    }
+    // (a copy in flight when a wait gave up ends before the CTA does: its
+    // barrier is waited for below, with the same limit)
+    for (int p = max(0, unfinished - R); p < unfinished; ++p) wait(rawf(p % R), p / R);
+  } else if (warp == 1) {  // ---- MMAs
+    if (lane == 0) {
+      const uint32_t ab = FP16 ? 0u : 1u;
+      const uint32_t id = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(128 >> 4) << 24);
+      const uint32_t id_s = id | ((uint32_t)(128 >> 3) << 17), id_o = id | ((uint32_t)(D >> 3) << 17);
+      bool ok = true;
+      auto scores = [&](int g, int j) {
+        ok = ok && wait(two(kFull, j & 1), j >> 1);
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (uint32_t)(kk / 4) * 16384u + (uint32_t)(kk % 4) * 32u;
+          const uint64_t ad = mma_smem_desc(sq + (uint32_t)(g * Shape::q_tile) + off);
+          const uint64_t bd = mma_smem_desc(sk + (uint32_t)((j & 1) * Shape::kv_tile) + off);
+          asm volatile(
+              "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+              "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + (uint32_t)g * 128u),
+              "l"(ad), "l"(bd), "r"(id_s), "r"(kk > 0 ? 1u : 0u)
+              : "memory");
+        }
+        tc_commit(two(sFull, g));
+        if (g == nt - 1) tc_commit(two(kFree, j & 1));
+      };
+      for (int g = 0; g < nt; ++g) ok = ok && wait(two(qFull, g), 0);
+      for (int g = 0; g < nt; ++g) scores(g, 0);
+      for (int j = 0; j < steps && ok; ++j)
+        for (int g = 0; g < nt && ok; ++g) {
+          ok = wait(two(pFull, g), j) && wait(two(vFull, j & 1), j >> 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t bd = mma_smem_desc(sv + (uint32_t)((j & 1) * Shape::kv_tile) + (uint32_t)(kk / 4) * (D * 128u) +
+                                              (uint32_t)(kk % 4) * 32u);
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem + 256u + (uint32_t)g * 128u),
+                "r"(tmem + (uint32_t)g * 128u + (uint32_t)kk * 8u), "l"(bd), "r"(id_o), "r"(j > 0 || kk > 0 ? 1u : 0u)
+                : "memory");
+          }
+          if (g == nt - 1) tc_commit(two(vFree, j & 1));
+          tc_commit(two(pvDone, g));
+          if (j + 1 < steps) scores(g, j + 1);
+        }
+    }
+    __syncwarp();
+  } else if (warp < 6) {  // ---- unpack
+    const int tid = (int)threadIdx.x - 64;
+    const int len = min(kv.len[seq], pos_hi + 1);  // keys that some row may see
+    bool ok = true;
+    for (int j = 0; j < steps && ok; ++j) {
+      const int buf = j & 1;
+      const uint32_t kt = sk + (uint32_t)(buf * Shape::kv_tile), vt = sv + (uint32_t)(buf * Shape::kv_tile);
+      if (j >= 2) ok = wait(two(kFree, buf), (j >> 1) - 1);
+      uint32_t absent = 0;
+      for (int h = 0; h < 2 && ok; ++h) {  // K of the two pages
+        const int p = 2 * j + h, slot = p % R;
+        ok = wait(rawf(slot), p / R);
+        if (!ok) break;
+        absent = s_absent[j & 7];
+        if ((absent >> h) & 1u) continue;
+        const unsigned char* blk = raw_g + slot * BLK;
+        const int key = tid >> 1, half = tid & 1;
+        const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D));
+        uint32_t step[NG], lo[NG];
+        bool fine = true;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) fine &= param_finite<T>(par[(kKv4Page + key) * NG + gr]);
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          const uint32_t w = fine ? par[key * NG + gr] : 0xffffffffu;  // NaN
+          step[gr] = __byte_perm(w, w, 0x1010);
+          lo[gr] = __byte_perm(w, w, 0x3232);
+        }
+        const uint32_t row = kt + (uint32_t)(64 * h + key) * 128u;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+          const int t = 2 * half + tt;
+          uint32_t w[JW];
+          const unsigned char* src = blk + key * (D / 2) + t * (JW * 4);
+          if constexpr (JW == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            w[0] = v.x, w[1] = v.y;
+          }
+#pragma unroll
+          for (int jj = 0; jj < JW; ++jj) {
+            const int u = 4 * jj + t, gr = 32 * jj / G;  // channels 8 u ..
+            const uint4 v = make_uint4(Pair16<T>::value(Pair16<T>::template code<0>(w[jj]), step[gr], lo[gr]),
+                                       Pair16<T>::value(Pair16<T>::template code<1>(w[jj]), step[gr], lo[gr]),
+                                       Pair16<T>::value(Pair16<T>::template code<2>(w[jj]), step[gr], lo[gr]),
+                                       Pair16<T>::value(Pair16<T>::template code<3>(w[jj]), step[gr], lo[gr]));
+            sts128(row + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (key & 7)) * 16), v);
+          }
+        }
+      }
+      if (!ok) break;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(two(kFull, buf));
+      if (j >= 2) ok = wait(two(vFree, buf), (j >> 1) - 1);
+      if (!ok) break;
+      // V: a thread takes a chunk's word of 8 neighbouring keys; D = 64 has one
+      // word a chunk, so each half of the threads takes a page
+      for (int h = D == 128 ? 0 : tid >> 6; h < 2; h += D == 128 ? 1 : 2) {
+        const int p = 2 * j + h;
+        const unsigned char* blk = raw_g + (p % R) * BLK;
+        const int c = tid & 7, oct = (tid >> 3) & 7, ws = D == 128 ? tid >> 6 : 0;
+        const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D)) + kKv4Page * NG;
+        const bool there = !((absent >> h) & 1u);
+        uint32_t out[8][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // pairs of keys
+          uint32_t w[2], pr[2][2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int key = 8 * oct + 2 * e + b;
+            const bool seen = there && (page0 + p) * kKv4Page + key < len;
+            w[b] = *reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + key * (D / 2) +
+                                                      kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
+            bool fine = seen;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) fine = fine && param_finite<T>(par[key * NG + gr]);
+            // the word's channels lie in one group (G = 64) or two (32)
+            const int g0 = 64 * ws / G;
+            pr[b][0] = fine ? par[key * NG + g0] : 0u;
+            pr[b][1] = G == 32 ? (fine ? par[key * NG + g0 + 1] : 0u) : pr[b][0];
+          }
+          const uint32_t step0 = __byte_perm(pr[0][0], pr[1][0], 0x5410), lo0 = __byte_perm(pr[0][0], pr[1][0], 0x7632);
+          const uint32_t step1 = __byte_perm(pr[0][1], pr[1][1], 0x5410), lo1 = __byte_perm(pr[0][1], pr[1][1], 0x7632);
+          const uint32_t x0 = __byte_perm(w[0], w[1], 0x5410), x1 = __byte_perm(w[0], w[1], 0x7632);
+          out[0][e] = Pair16<T>::value(Pair16<T>::template code<0>(x0), step0, lo0);
+          out[1][e] = Pair16<T>::value(Pair16<T>::template code<1>(x0), step0, lo0);
+          out[2][e] = Pair16<T>::value(Pair16<T>::template code<2>(x0), step0, lo0);
+          out[3][e] = Pair16<T>::value(Pair16<T>::template code<3>(x0), step0, lo0);
+          out[4][e] = Pair16<T>::value(Pair16<T>::template code<0>(x1), step1, lo1);
+          out[5][e] = Pair16<T>::value(Pair16<T>::template code<1>(x1), step1, lo1);
+          out[6][e] = Pair16<T>::value(Pair16<T>::template code<2>(x1), step1, lo1);
+          out[7][e] = Pair16<T>::value(Pair16<T>::template code<3>(x1), step1, lo1);
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int d = 64 * ws + 16 * (n >> 1) + c + 8 * (n & 1);
+          sts128(vt + (uint32_t)h * (D * 128u) + (uint32_t)d * 128u + (uint32_t)((oct ^ (d & 7)) * 16),
+                 make_uint4(out[n][0], out[n][1], out[n][2], out[n][3]));
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(two(vFull, buf));
+        mbar_arrive(rawe((2 * j) % R));
+        mbar_arrive(rawe((2 * j + 1) % R));
+      }
+    }
+  } else {  // ---- P, one row per thread
+    const int g = (warp - 6) >> 2, quad = warp & 3, r = quad * 32 + lane, row = row_lo + 128 * g + r;
+    if (g < nt) {
+      const bool in = row < row_hi;
+      const int tok = row / a.share, gh = row - tok * a.share;
+      const int hi = in ? q.pos0 + tok : -1, lo = a.window > 0 ? q.pos0 + tok - a.window + 1 : 0;
+      {  // Q into its tile, channels in the codes' order, with the scale's sign
+        const T* src = static_cast<const T*>(a.q[rank]) + (size_t)(q.begin + tok) * a.q_stride +
+                       (size_t)(head * a.share + gh) * D;
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        const uint32_t dst = sq + (uint32_t)(g * Shape::q_tile) + (uint32_t)r * 128u;
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+          const uint4 v = in ? *reinterpret_cast<const uint4*>(src + 8 * u) : make_uint4(0, 0, 0, 0);
+          const uint4 o = make_uint4(__byte_perm(v.x, v.z, 0x5410) ^ flip, __byte_perm(v.x, v.z, 0x7632) ^ flip,
+                                     __byte_perm(v.y, v.w, 0x5410) ^ flip, __byte_perm(v.y, v.w, 0x7632) ^ flip);
+          sts128(dst + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (r & 7)) * 16), o);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(two(qFull, g));
+      }
+      const float c = fabsf(a.scale) * 1.44269504088896341f;
+      const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+      const uint32_t ts = tmem + lanes + (uint32_t)g * 128u, to = tmem + lanes + 256u + (uint32_t)g * 128u;
+      // the keys that every row of this warp sees need no test
+      const int first = row_lo + 128 * g + quad * 32, last = min(first + 31, row_hi - 1);
+      const int all_hi = first < row_hi ? q.pos0 + first / a.share : 0x7fffffff;
+      const int all_lo = a.window > 0 && first < row_hi ? q.pos0 + last / a.share - a.window + 1 : 0;
+      float ref = 0.0f, l = 0.0f;
+      bool any = false, ok = true;
+      int j = 0;
+      for (; j < steps; ++j) {
+        if (!(ok = wait(two(sFull, g), j))) break;
+        tc_fence_after();
+        const int key0 = (page0 + 2 * j) * kKv4Page;
+        const uint32_t absent = s_absent[j & 7];
+        const bool masked = absent || key0 + 127 > all_hi || key0 < all_lo;
+        auto seen = [&](int i) {
+          const int key = key0 + i;
+          return key <= hi && key >= lo && !((absent >> (i >> 6)) & 1u);
+        };
+        float m = -INFINITY;
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t s[32];
+          tmem_ld32(ts + (uint32_t)c0, s);
+          tmem_ld_wait();
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (seen(c0 + i)) m = fmaxf(m, __uint_as_float(s[i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+          }
+        }
+        const float mc = m * c;
+        const bool grows = m != -INFINITY && (!any || mc > ref + 8.0f);
+        if (__any_sync(0xffffffffu, grows && any)) {  // rescale the sums so far
+          const float fix = grows && any ? exp2_approx(ref - mc) : 1.0f;
+          l *= fix;
+          if (!(ok = wait(two(pvDone, g), j - 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(to + (uint32_t)c0, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fix);
+            tmem_st16(to + (uint32_t)c0, v);
+          }
+        }
+        if (grows) {
+          ref = mc;
+          any = true;
+        }
+        const float off = kShift - ref;
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t s[32], w[16];
+          tmem_ld32(ts + (uint32_t)c0, s);
+          tmem_ld_wait();
+          float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float p0 = exp2_approx(fmaf(__uint_as_float(s[i]), c, off));
+            float p1 = exp2_approx(fmaf(__uint_as_float(s[i + 1]), c, off));
+            if (masked) {
+              if (!seen(c0 + i)) p0 = 0.0f;
+              if (!seen(c0 + i + 1)) p1 = 0.0f;
+            }
+            sum0 += p0;
+            sum1 += p1;
+            w[i / 2] = Half16<T>::narrow2(p0, p1);
+          }
+          l += sum0 + sum1;
+          tmem_st16(ts + (uint32_t)(c0 / 2), w);  // over scores that have been read
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(two(pFull, g));
+      }
+      if (ok) ok = wait(two(pvDone, g), steps - 1);
+      tc_fence_after();
+      const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
+      const size_t at = (size_t)(q.begin + tok) * a.q_heads + head * a.share + gh;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(to + (uint32_t)c0, v);
+        tmem_ld_wait();
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          w[i] = Half16<T>::narrow2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+        if (in && ok) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out[rank]) + at * D + c0);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      if (in && ok && a.lse[rank])
+        a.lse[rank][at] = l == 0.0f ? -INFINITY : (ref - kShift + log2f(l)) * 0.69314718055994531f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+}  // namespace dcc

@@ -19,6 +19,7 @@
 #pragma once
 #include "fused_mma.cuh"
 #include "linear.cuh"
+#include "tcgen05.cuh"
 
 namespace dcc {
 
@@ -30,13 +31,6 @@ struct LinMmaArgs {
   LinArgs l;
   int ntile, ks, stages, bm, tiles, rounds, fp16;  // tiles: row tiles of one rank
 };
-
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                 "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-               : "r"(addr));
-}
 
 // 8 sums of neighbouring rows -> bias, activation, residual, one rounding
 __device__ __forceinline__ uint4 lin_finish8(float* v, const uint4* bias, const uint4* res, int act, bool fp16) {
