@@ -83,12 +83,13 @@ struct Pair16<__nv_bfloat16> {
     return *reinterpret_cast<const uint32_t*>(&r);
   }
 };
-// a (step, lo) pair neither of which may be NaN or infinite
+// bits 15 or 31 are set where a (step, lo) pair holds a NaN or an infinity
 template <typename T>
-__device__ __forceinline__ bool param_finite(uint32_t w) {
-  constexpr uint32_t e = Pair16<T>::kExp;
-  return (w & e) != e && ((w >> 16) & e) != e;
+__device__ __forceinline__ uint32_t param_bad(uint32_t w) {
+  constexpr uint32_t one = 0x8000u - Pair16<T>::kExp;  // carries an exponent of all ones into the sign's place
+  return (w & 0x7fff7fffu) + (one | one << 16);
 }
+constexpr uint32_t kBad = 0x80008000u;
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, const __grid_constant__ AttnArgs a, DevComm dc) {
@@ -245,6 +246,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       const uint32_t kt = sk + (uint32_t)(buf * Shape::kv_tile), vt = sv + (uint32_t)(buf * Shape::kv_tile);
       if (j >= 2) ok = wait(two(kFree, buf), (j >> 1) - 1);
       uint32_t absent = 0;
+#pragma unroll 1
       for (int h = 0; h < 2 && ok; ++h) {  // K of the two pages
         const int p = 2 * j + h, slot = p % R;
         ok = wait(rawf(slot), p / R);
@@ -252,22 +254,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         absent = s_absent[j & 7];
         if ((absent >> h) & 1u) continue;
         const unsigned char* blk = raw_g + slot * BLK;
-        const int key = tid >> 1, half = tid & 1;
         const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D));
-        uint32_t step[NG], lo[NG];
-        bool fine = true;
+        // eight neighbouring lanes take the four quarters of rows r and r ^ 5
+        // (other half of the banks, other half of the swizzled chunks): no
+        // bank conflicts on either side
+        const int t = tid & 3;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          const int key = (2 * ((tid >> 3) + 16 * pass)) ^ ((tid & 4) ? 5 : 0);
+          uint32_t step[NG], lo[NG];
+          uint32_t bad = 0;
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) fine &= param_finite<T>(par[(kKv4Page + key) * NG + gr]);
+          for (int gr = 0; gr < NG; ++gr) bad |= param_bad<T>(par[(kKv4Page + key) * NG + gr]);
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          const uint32_t w = fine ? par[key * NG + gr] : 0xffffffffu;  // NaN
-          step[gr] = __byte_perm(w, w, 0x1010);
-          lo[gr] = __byte_perm(w, w, 0x3232);
-        }
-        const uint32_t row = kt + (uint32_t)(64 * h + key) * 128u;
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-          const int t = 2 * half + tt;
+          for (int gr = 0; gr < NG; ++gr) {
+            const uint32_t w = (bad & kBad) ? 0xffffffffu : par[key * NG + gr];  // NaN
+            step[gr] = __byte_perm(w, w, 0x1010);
+            lo[gr] = __byte_perm(w, w, 0x3232);
+          }
+          const uint32_t row = kt + (uint32_t)(64 * h + key) * 128u;
           uint32_t w[JW];
           const unsigned char* src = blk + key * (D / 2) + t * (JW * 4);
           if constexpr (JW == 4) {
@@ -294,35 +299,56 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       if (lane == 0) mbar_arrive(two(kFull, buf));
       if (j >= 2) ok = wait(two(vFree, buf), (j >> 1) - 1);
       if (!ok) break;
-      // V: a thread takes a chunk's word of 8 neighbouring keys; D = 64 has one
-      // word a chunk, so each half of the threads takes a page
+      // V: a thread takes a chunk's word of 8 neighbouring keys (at D = 128 every
+      // other run of keys in swapped order, so that the two runs a warp works
+      // on lie in different banks); D = 64 has one word a chunk, so each half
+      // of the threads takes a page
+#pragma unroll 1
       for (int h = D == 128 ? 0 : tid >> 6; h < 2; h += D == 128 ? 1 : 2) {
         const int p = 2 * j + h;
         const unsigned char* blk = raw_g + (p % R) * BLK;
-        const int c = tid & 7, oct = (tid >> 3) & 7, ws = D == 128 ? tid >> 6 : 0;
+        const int c = tid & 7, oct = D == 128 ? tid >> 4 : (tid >> 3) & 7, ws = D == 128 ? (tid >> 3) & 1 : 0;
+        const int swap = D == 128 ? oct & 1 : 0;
+        const uint32_t sel0 = swap ? 0x1054u : 0x5410u, sel1 = swap ? 0x3276u : 0x7632u;
         const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D)) + kKv4Page * NG;
         const bool there = !((absent >> h) & 1u);
+        // the word's channels lie in one group (G = 64) or two (32)
+        const int g0 = 64 * ws / G;
+        constexpr int GW = G == 32 ? 2 : 1;
+        uint32_t w[8], pr[8][GW], bad = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int key = 8 * oct + (k ^ swap);
+          w[k] = *reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + key * (D / 2) +
+                                                    kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
+#pragma unroll
+          for (int x = 0; x < GW; ++x) {
+            pr[k][x] = par[key * NG + g0 + x];
+            bad |= param_bad<T>(pr[k][x]);
+          }
+          if (NG > GW)  // the other groups, which K's check covers too
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) bad |= param_bad<T>(par[key * NG + gr]);
+        }
+        if ((bad & kBad) || !there || (page0 + p) * kKv4Page + 8 * oct + 7 >= len)  // some key must be zero
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int key = 8 * oct + (k ^ swap);
+            uint32_t any = 0;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) any |= param_bad<T>(par[key * NG + gr]);
+            if ((any & kBad) || !there || (page0 + p) * kKv4Page + key >= len)
+#pragma unroll
+              for (int x = 0; x < GW; ++x) pr[k][x] = 0u;
+          }
         uint32_t out[8][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // pairs of keys
-          uint32_t w[2], pr[2][2];
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int key = 8 * oct + 2 * e + b;
-            const bool seen = there && (page0 + p) * kKv4Page + key < len;
-            w[b] = *reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + key * (D / 2) +
-                                                      kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
-            bool fine = seen;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) fine = fine && param_finite<T>(par[key * NG + gr]);
-            // the word's channels lie in one group (G = 64) or two (32)
-            const int g0 = 64 * ws / G;
-            pr[b][0] = fine ? par[key * NG + g0] : 0u;
-            pr[b][1] = G == 32 ? (fine ? par[key * NG + g0 + 1] : 0u) : pr[b][0];
-          }
-          const uint32_t step0 = __byte_perm(pr[0][0], pr[1][0], 0x5410), lo0 = __byte_perm(pr[0][0], pr[1][0], 0x7632);
-          const uint32_t step1 = __byte_perm(pr[0][1], pr[1][1], 0x5410), lo1 = __byte_perm(pr[0][1], pr[1][1], 0x7632);
-          const uint32_t x0 = __byte_perm(w[0], w[1], 0x5410), x1 = __byte_perm(w[0], w[1], 0x7632);
+          const int k0 = 2 * e, k1 = 2 * e + 1;
+          const uint32_t step0 = __byte_perm(pr[k0][0], pr[k1][0], sel0), lo0 = __byte_perm(pr[k0][0], pr[k1][0], sel1);
+          const uint32_t step1 = GW > 1 ? __byte_perm(pr[k0][GW - 1], pr[k1][GW - 1], sel0) : step0;
+          const uint32_t lo1 = GW > 1 ? __byte_perm(pr[k0][GW - 1], pr[k1][GW - 1], sel1) : lo0;
+          const uint32_t x0 = __byte_perm(w[k0], w[k1], sel0), x1 = __byte_perm(w[k0], w[k1], sel1);
           out[0][e] = Pair16<T>::value(Pair16<T>::template code<0>(x0), step0, lo0);
           out[1][e] = Pair16<T>::value(Pair16<T>::template code<1>(x0), step0, lo0);
           out[2][e] = Pair16<T>::value(Pair16<T>::template code<2>(x0), step0, lo0);
@@ -389,33 +415,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           const int key = key0 + i;
           return key <= hi && key >= lo && !((absent >> (i >> 6)) & 1u);
         };
-        float m = -INFINITY;
-#pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t s[32];
-          tmem_ld32(ts + (uint32_t)c0, s);
-          tmem_ld_wait();
+        // Loops over 16 columns stay loops (the roles' code together must stay
+        // in the instruction cache); the next columns load under the current.
+        uint32_t s[2][16];
+        float m0 = -INFINITY, m1 = -INFINITY;
+        tmem_ld16(ts, s[0]);
+        auto top = [&](const uint32_t* v, int c0) {
           if (masked) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (seen(c0 + i)) m = fmaxf(m, __uint_as_float(s[i]));
+            for (int i = 0; i < 16; ++i)
+              if (seen(c0 + i)) m0 = fmaxf(m0, __uint_as_float(v[i]));
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+            for (int i = 0; i < 16; i += 4) {
+              m0 = max3(m0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+              m1 = max3(m1, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+            }
           }
+        };
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          tmem_ld_wait16(s[0]);
+          tmem_ld16(ts + (uint32_t)c0 + 16u, s[1]);
+          top(s[0], c0);
+          tmem_ld_wait16(s[1]);
+          tmem_ld16(ts + ((uint32_t)c0 + 32u) % 128u, s[0]);  // in the end the first columns again
+          top(s[1], c0 + 16);
         }
-        const float mc = m * c;
+        const float m = fmaxf(m0, m1), mc = m * c;
         const bool grows = m != -INFINITY && (!any || mc > ref + 8.0f);
         if (__any_sync(0xffffffffu, grows && any)) {  // rescale the sums so far
           const float fix = grows && any ? exp2_approx(ref - mc) : 1.0f;
           l *= fix;
           if (!(ok = wait(two(pvDone, g), j - 1))) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 16) {
             uint32_t v[16];
             tmem_ld16(to + (uint32_t)c0, v);
-            tmem_ld_wait();
+            tmem_ld_wait16(v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fix);
             tmem_st16(to + (uint32_t)c0, v);
@@ -425,28 +463,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           ref = mc;
           any = true;
         }
-        const float off = kShift - ref;
+        const float2 off = make_float2(kShift - ref, kShift - ref), cc = make_float2(c, c);
+        float2 sum = make_float2(0.0f, 0.0f);
+        auto pair = [&](const uint32_t* v, int i) {
+          const float2 x = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), cc, off);
+          return make_float2(exp2_approx(x.x), exp2_approx(x.y));
+        };
+        auto make = [&](const uint32_t* v, int c0) {
+          uint32_t w[8];
+          if (masked) {  // tested once, not per element
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t s[32], w[16];
-          tmem_ld32(ts + (uint32_t)c0, s);
-          tmem_ld_wait();
-          float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float p0 = exp2_approx(fmaf(__uint_as_float(s[i]), c, off));
-            float p1 = exp2_approx(fmaf(__uint_as_float(s[i + 1]), c, off));
-            if (masked) {
-              if (!seen(c0 + i)) p0 = 0.0f;
-              if (!seen(c0 + i + 1)) p1 = 0.0f;
+            for (int i = 0; i < 16; i += 2) {
+              float2 p = pair(v, i);
+              if (!seen(c0 + i)) p.x = 0.0f;
+              if (!seen(c0 + i + 1)) p.y = 0.0f;
+              sum = add2(sum, p);
+              w[i / 2] = Half16<T>::narrow2(p.x, p.y);
             }
-            sum0 += p0;
-            sum1 += p1;
-            w[i / 2] = Half16<T>::narrow2(p0, p1);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float2 p = pair(v, i);
+              sum = add2(sum, p);
+              w[i / 2] = Half16<T>::narrow2(p.x, p.y);
+            }
           }
-          l += sum0 + sum1;
-          tmem_st16(ts + (uint32_t)(c0 / 2), w);  // over scores that have been read
+          tmem_st8(ts + (uint32_t)(c0 / 2), w);  // over scores that have been read
+        };
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          tmem_ld_wait16(s[0]);
+          tmem_ld16(ts + (uint32_t)c0 + 16u, s[1]);
+          make(s[0], c0);
+          tmem_ld_wait16(s[1]);
+          if (c0 < 96) tmem_ld16(ts + (uint32_t)c0 + 32u, s[0]);
+          make(s[1], c0 + 16);
         }
+        l += sum.x + sum.y;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -460,7 +513,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       for (int c0 = 0; c0 < D; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(to + (uint32_t)c0, v);
-        tmem_ld_wait();
+        tmem_ld_wait16(v);
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)

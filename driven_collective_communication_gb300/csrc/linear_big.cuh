@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kBigThreads, 1)
       for (int c0 = 0; c0 < N; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)b * 256u + (uint32_t)c0, v);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        tmem_ld_wait16(v);
         if (c0 + 16 >= N) {  // the accumulator may be overwritten
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();

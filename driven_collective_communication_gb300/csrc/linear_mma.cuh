@@ -77,7 +77,7 @@ __device__ __forceinline__ void lin_epilogue(const DevComm& dc, const LinMmaArgs
     for (int c0 = w_lo + (warp >> 2) * 16; c0 < w_lo + W; c0 += 16 * (THREADS / 128)) {
       uint32_t v[16];
       tmem_ld16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)c0, v);
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      tmem_ld_wait16(v);
 #pragma unroll
       for (int j = 0; j < 16; ++j) part[(c0 - w_lo + j) * kMmaBM + row] = acc_ok ? __uint_as_float(v[j]) : 0.0f;
     }
