@@ -415,32 +415,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           const int key = key0 + i;
           return key <= hi && key >= lo && !((absent >> (i >> 6)) & 1u);
         };
-        // Loops over 16 columns stay loops (the roles' code together must stay
+        // Loops over 32 columns stay loops (the roles' code together must stay
         // in the instruction cache); the next columns load under the current.
-        uint32_t s[2][16];
+        uint32_t s[2][32];
         float m0 = -INFINITY, m1 = -INFINITY;
-        tmem_ld16(ts, s[0]);
+        tmem_ld32(ts, s[0]);
         auto top = [&](const uint32_t* v, int c0) {
           if (masked) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 32; ++i)
               if (seen(c0 + i)) m0 = fmaxf(m0, __uint_as_float(v[i]));
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
+            for (int i = 0; i < 32; i += 4) {
               m0 = max3(m0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
               m1 = max3(m1, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
             }
           }
         };
 #pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          tmem_ld_wait16(s[0]);
-          tmem_ld16(ts + (uint32_t)c0 + 16u, s[1]);
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+          tmem_ld_wait32(s[0]);
+          tmem_ld32(ts + (uint32_t)c0 + 32u, s[1]);
           top(s[0], c0);
-          tmem_ld_wait16(s[1]);
-          tmem_ld16(ts + ((uint32_t)c0 + 32u) % 128u, s[0]);  // in the end the first columns again
-          top(s[1], c0 + 16);
+          tmem_ld_wait32(s[1]);
+          tmem_ld32(ts + ((uint32_t)c0 + 64u) % 128u, s[0]);  // in the end the first columns again
+          top(s[1], c0 + 32);
         }
         const float m = fmaxf(m0, m1), mc = m * c;
         const bool grows = m != -INFINITY && (!any || mc > ref + 8.0f);
@@ -470,10 +470,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           return make_float2(exp2_approx(x.x), exp2_approx(x.y));
         };
         auto make = [&](const uint32_t* v, int c0) {
-          uint32_t w[8];
+          uint32_t w[16];
           if (masked) {  // tested once, not per element
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
+            for (int i = 0; i < 32; i += 2) {
               float2 p = pair(v, i);
               if (!seen(c0 + i)) p.x = 0.0f;
               if (!seen(c0 + i + 1)) p.y = 0.0f;
@@ -482,22 +482,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
+            for (int i = 0; i < 32; i += 2) {
               const float2 p = pair(v, i);
               sum = add2(sum, p);
               w[i / 2] = Half16<T>::narrow2(p.x, p.y);
             }
           }
-          tmem_st8(ts + (uint32_t)(c0 / 2), w);  // over scores that have been read
+          tmem_st16(ts + (uint32_t)(c0 / 2), w);  // over scores that have been read
         };
 #pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          tmem_ld_wait16(s[0]);
-          tmem_ld16(ts + (uint32_t)c0 + 16u, s[1]);
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+          tmem_ld_wait32(s[0]);
+          tmem_ld32(ts + (uint32_t)c0 + 32u, s[1]);
           make(s[0], c0);
-          tmem_ld_wait16(s[1]);
-          if (c0 < 96) tmem_ld16(ts + (uint32_t)c0 + 32u, s[0]);
-          make(s[1], c0 + 16);
+          tmem_ld_wait32(s[1]);
+          if (c0 == 0) tmem_ld32(ts + 64u, s[0]);
+          make(s[1], c0 + 32);
         }
         l += sum.x + sum.y;
         tmem_st_wait();
