@@ -326,17 +326,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
             pr[k][x] = par[key * NG + g0 + x];
             bad |= param_bad<T>(pr[k][x]);
           }
-          if (NG > GW)  // the other groups, which K's check covers too
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) bad |= param_bad<T>(par[key * NG + gr]);
         }
         if ((bad & kBad) || !there || (page0 + p) * kKv4Page + 8 * oct + 7 >= len)  // some key must be zero
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int key = 8 * oct + (k ^ swap);
-            uint32_t any = 0;
+            uint32_t any = 0;  // (another group of the key may be bad: its own unit sees to it)
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) any |= param_bad<T>(par[key * NG + gr]);
+            for (int x = 0; x < GW; ++x) any |= param_bad<T>(pr[k][x]);
             if ((any & kBad) || !there || (page0 + p) * kKv4Page + key >= len)
 #pragma unroll
               for (int x = 0; x < GW; ++x) pr[k][x] = 0u;
