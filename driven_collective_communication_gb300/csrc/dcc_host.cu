@@ -27,7 +27,7 @@
 
 namespace dcc {  // kernels of the calls without a communicator, for visit_kernels
 const void* linear_kernel(int which);
-const void* kv4_row_kernel(bool fp16, bool read, int dim, int group);
+const void* kv4_row_kernel(bool fp16, bool read, int dim, int group, bool several);
 const void* kv4_attention_kernel(bool fp16, int dim, int group, int which);
 const void* kv4_pages_kernel(int i);
 }  // namespace dcc
@@ -362,9 +362,10 @@ bool visit_kernels(F&& visit) {
   for (int fp16 = 0; fp16 < 2; ++fp16) {
     for (int dim = 64; dim <= 128; dim += 64)
       for (int group = 32; group <= 64; group += 32)
-        if (!v(dcc::kv4_row_kernel(fp16, false, dim, group)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group)) ||
+        if (!v(dcc::kv4_row_kernel(fp16, false, dim, group, false)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group, false)) ||
+            !v(dcc::kv4_row_kernel(fp16, false, dim, group, true)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group, true)) ||
             !v(dcc::kv4_attention_kernel(fp16, dim, group, 1)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 2)) ||
-            !v(dcc::kv4_attention_kernel(fp16, dim, group, 3)))
+            !v(dcc::kv4_attention_kernel(fp16, dim, group, 3)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 0)))
           return false;
   }
   for (int i = 0; i < 3; ++i)

@@ -19,7 +19,12 @@ Kernel decode_for(int dim, int group) {
   if (dim == 128) return group == 64 ? decode_of<T, 128, 64, RT>() : decode_of<T, 128, 32, RT>();
   return group == 64 ? decode_of<T, 64, 64, RT>() : decode_of<T, 64, 32, RT>();
 }
+template <typename T>
+Kernel decode_wide(int group) {  // 24 rows: 64-wide heads have the registers
+  return group == 64 ? decode_of<T, 64, 64, 3>() : decode_of<T, 64, 32, 3>();
+}
 Kernel decode(bool fp16, int dim, int group, int tiles) {
+  if (tiles > 2 && dim == 64) return fp16 ? decode_wide<__half>(group) : decode_wide<__nv_bfloat16>(group);
   if (tiles > 1) return fp16 ? decode_for<__half, 2>(dim, group) : decode_for<__nv_bfloat16, 2>(dim, group);
   return fp16 ? decode_for<__half, 1>(dim, group) : decode_for<__nv_bfloat16, 1>(dim, group);
 }
@@ -36,9 +41,9 @@ Kernel prompt(bool fp16, int dim, int group) {
   return fp16 ? prompt_for<__half>(dim, group) : prompt_for<__nv_bfloat16>(dim, group);
 }
 }  // namespace
-// which: 1 or 2 row tiles of the streaming kernel, 3 the prompt kernel
+// which: 1 to 3 row tiles of the streaming kernel (3: 64-wide heads), 0 the prompt kernel
 const void* kv4_attention_kernel(bool fp16, int dim, int group, int which) {
-  return which == 3 ? prompt(fp16, dim, group).fn : decode(fp16, dim, group, which).fn;
+  return which == 0 ? prompt(fp16, dim, group).fn : decode(fp16, dim, group, which).fn;
 }
 }  // namespace dcc
 
@@ -129,7 +134,10 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
     void* args[] = {&d, &a, &dc};
     return dcc_host::launch(k.fn, (int)grid, k.threads, false, args, st, k.smem, true);
   }
-  const dcc::Kernel k = dcc::decode(fp16, kv->head_dim, kv->group, rows > 8 ? 2 : 1);
+  // Row tiles: as few passes over the cache as the registers allow, then the
+  // fewest rows that make that many.
+  const int most = kv->head_dim == 64 ? 3 : 2, passes = ((int)rows + 8 * most - 1) / (8 * most);
+  const dcc::Kernel k = dcc::decode(fp16, kv->head_dim, kv->group, ((int)rows + 8 * passes - 1) / (8 * passes));
   if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
   void* args[] = {&d, &a};
   return dcc_host::launch(k.fn, sms < dcc::kDecMaxCtas ? sms : dcc::kDecMaxCtas, k.threads, false, args, st, k.smem,

@@ -18,6 +18,12 @@
 namespace dcc {
 
 constexpr int kKv4RowThreads = 256;
+// Tokens a group of lanes takes in large batches: their loads are in flight
+// together and the place in the cache is searched for once.
+constexpr int kKv4RowTokens = 4;
+// From this many (token, head, rank) on: enough groups of lanes to fill the
+// GPU (152 SMs x 64) with several tokens each.
+constexpr long long kKv4ManyRows = 152ll * 64 * kKv4RowTokens;
 
 struct Kv4RowArgs {
   void* k[DCC_MAX_RANKS];
@@ -27,155 +33,194 @@ struct Kv4RowArgs {
   int tokens, layer;
 };
 
-// Where row `tok` of the batch stands in the cache; page < 0: nowhere.
+// Where U rows of the batch, `step` apart, stand in the cache; page < 0: nowhere.
+// The first is searched for, the others follow it; their loads overlap.
 struct Kv4Place {
   int page, slot;
 };
-template <int LANES>
-__device__ __forceinline__ Kv4Place kv4_place(const Kv4Dev& kv, const int32_t* start, int tok) {
-  const int s = kv4_seq_of<LANES>(start, kv.seqs, tok);
-  if (s < 0) return {-1, 0};
-  const int pos = kv.len[s] - start[s + 1] + tok;
-  if (pos < 0) return {-1, 0};
-  return {kv4_page(kv, s, pos / kKv4Page), pos % kKv4Page};
+template <int LANES, int U>
+__device__ __forceinline__ void kv4_places(const Kv4Dev& kv, const int32_t* start, int tokens, int tok, Kv4Place* at) {
+  int s = kv4_seq_of<LANES>(start, kv.seqs, tok);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    at[u] = {-1, 0};
+    const int t = tok + u;
+    if (t >= tokens) continue;
+    if (u > 0) {
+      if (s < 0) s = kv4_seq_of<LANES>(start, kv.seqs, t);
+      else
+        while (s < kv.seqs && t >= start[s + 1]) ++s;
+      if (s >= kv.seqs || (s >= 0 && t < start[s])) s = -1;
+    }
+    if (s < 0) continue;
+    const int pos = kv.len[s] - start[s + 1] + t;
+    if (pos >= 0) at[u] = {kv4_page(kv, s, pos / kKv4Page), pos % kKv4Page};
+  }
 }
 
-template <typename T, int D, int G>
+// The (rank, first of U tokens, head) that D/8 lanes work on.
+struct Kv4Item {
+  int rank, tok, head;
+};
+template <int U>
+__device__ __forceinline__ Kv4Item kv4_item(const Kv4Dev& kv, int tokens, long long item) {
+  const long long per_rank = (long long)((tokens + U - 1) / U) * kv.heads;
+  const int rank = (int)(item / per_rank);
+  return {rank, (int)(item % per_rank / kv.heads) * U, (int)(item % kv.heads)};
+}
+
+template <typename T, int D, int G, int U>
 __global__ void __launch_bounds__(kKv4RowThreads) k_kv4_append(Kv4Dev kv, Kv4RowArgs a) {
   constexpr int LANES = D / 8, ITEMS = kKv4RowThreads / LANES, GL = G / 8, NG = D / G;
   __shared__ uint32_t vrow[ITEMS][D / 8];
   pdl_prologue();
   const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
   const unsigned mask = ((1ull << LANES) - 1ull) << ((threadIdx.x & 31) / LANES * LANES);
-  const long long item = (long long)blockIdx.x * ITEMS + sub;
-  const long long per_rank = (long long)a.tokens * kv.heads;
-  const int rank = (int)(item / per_rank);
-  if (rank >= kv.n) return;
-  const int tok = (int)(item % per_rank / kv.heads), head = (int)(item % kv.heads);
-  const size_t src = (size_t)tok * a.stride + (size_t)head * D + lane * 8;
-  uint4 raw[2];
-  raw[0] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k[rank]) + src);
-  raw[1] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v[rank]) + src);
-  const Kv4Place at = kv4_place<LANES>(kv, a.start, tok);
-  if (at.page < 0) return;
-  char* blk = kv4_block(kv, rank, a.layer, at.page, head, kv4_block_bytes(D, G));
+  const Kv4Item it = kv4_item<U>(kv, a.tokens, (long long)blockIdx.x * ITEMS + sub);
+  if (it.rank >= kv.n) return;
+  uint4 raw[U][2];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {  // K, then V
-    const uint32_t u[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-    float x[8];
+  for (int u = 0; u < U; ++u) {
+    const size_t src = (size_t)min(it.tok + u, a.tokens - 1) * a.stride + (size_t)it.head * D + lane * 8;
+    raw[u][0] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k[it.rank]) + src);
+    raw[u][1] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v[it.rank]) + src);
+  }
+  Kv4Place at[U];
+  kv4_places<LANES, U>(kv, a.start, a.tokens, it.tok, at);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = Half16<T>::widen2(u[j]);
-      x[2 * j] = f.x;
-      x[2 * j + 1] = f.y;
-    }
-    float lo = x[0], hi = x[0];
-    bool bad = false;  // a NaN or an infinity
+  for (int u = 0; u < U; ++u) {
+    if (at[u].page < 0) continue;
+    const int slot = at[u].slot;
+    char* blk = kv4_block(kv, it.rank, a.layer, at[u].page, it.head, kv4_block_bytes(D, G));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo = fminf(lo, x[j]);
-      hi = fmaxf(hi, x[j]);
-      bad |= !(x[j] - x[j] == 0.0f);
-    }
+    for (int w = 0; w < 2; ++w) {  // K, then V
+      const uint32_t r[4] = {raw[u][w].x, raw[u][w].y, raw[u][w].z, raw[u][w].w};
+      float x[8];
 #pragma unroll
-    for (int m = 1; m < GL; m <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(mask, lo, m));
-      hi = fmaxf(hi, __shfl_xor_sync(mask, hi, m));
-    }
-    const unsigned bads = __ballot_sync(mask, bad);
-    uint16_t step16 = Half16<T>::narrow(__fdiv_rn(hi - lo, 15.0f));
-    uint16_t lo16 = Half16<T>::narrow(lo);
-    const float step = Half16<T>::widen(step16);
-    bad = ((bads >> ((threadIdx.x & 31) / GL * GL)) & ((1u << GL) - 1u)) != 0u || !(step - step == 0.0f);
-    uint32_t codes = 0;
-    if (bad) {
-      step16 = lo16 = Half16<T>::narrow(__uint_as_float(0x7fc00000u));
-    } else if (step > 0.0f) {
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = Half16<T>::widen2(r[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+      }
+      float lo = x[0], hi = x[0];
+      bool bad = false;  // a NaN or an infinity
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float c = fminf(fmaxf(rintf(__fdiv_rn(x[j] - lo, step)), 0.0f), 15.0f);
-        codes |= (uint32_t)c << (4 * j);
+        lo = fminf(lo, x[j]);
+        hi = fmaxf(hi, x[j]);
+        bad |= !(x[j] - x[j] == 0.0f);
+      }
+#pragma unroll
+      for (int m = 1; m < GL; m <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(mask, lo, m));
+        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, m));
+      }
+      const unsigned bads = __ballot_sync(mask, bad);
+      uint16_t step16 = Half16<T>::narrow(__fdiv_rn(hi - lo, 15.0f));
+      uint16_t lo16 = Half16<T>::narrow(lo);
+      const float step = Half16<T>::widen(step16);
+      bad = ((bads >> ((threadIdx.x & 31) / GL * GL)) & ((1u << GL) - 1u)) != 0u || !(step - step == 0.0f);
+      uint32_t codes = 0;
+      if (bad) {
+        step16 = lo16 = Half16<T>::narrow(__uint_as_float(0x7fc00000u));
+      } else if (step > 0.0f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float c = fminf(fmaxf(rintf(__fdiv_rn(x[j] - lo, step)), 0.0f), 15.0f);
+          codes |= (uint32_t)c << (4 * j);
+        }
+      }
+      if (lane % GL == 0)
+        *reinterpret_cast<uint32_t*>(blk + 2 * kv4_codes_bytes(D) + w * kv4_params_bytes(D, G) +
+                                     (slot * NG + lane / GL) * 4) = (uint32_t)step16 | ((uint32_t)lo16 << 16);
+      char* row = blk + w * kv4_codes_bytes(D) + slot * (D / 2);
+      if (w == 0) {
+        reinterpret_cast<uint32_t*>(row)[kv4_k_word(D, lane)] = codes;
+      } else {
+        // channels 16 i + 8 half + e, i = lane / 2, half = lane & 1: nibble
+        // 2 i + half of chunk e, so lanes 2 i and 2 i + 1 share byte i of it
+        const uint32_t other = __shfl_xor_sync(mask, codes, 1);
+        const int i = lane >> 1, odd = lane & 1;
+        const uint32_t even_c = odd ? other : codes, odd_c = odd ? codes : other;
+        uint8_t* bytes = reinterpret_cast<uint8_t*>(vrow[sub]);
+        __syncwarp(mask);  // the row before has been read
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = 4 * odd + e;
+          bytes[kv4_v_chunk(D, c, slot) * (D / 16) + i] =
+              (uint8_t)(((even_c >> (4 * c)) & 15u) | (((odd_c >> (4 * c)) & 15u) << 4));
+        }
+        __syncwarp(mask);
+        reinterpret_cast<uint32_t*>(row)[lane] = vrow[sub][lane];
       }
     }
-    if (lane % GL == 0)
-      *reinterpret_cast<uint32_t*>(blk + 2 * kv4_codes_bytes(D) + w * kv4_params_bytes(D, G) +
-                                   (at.slot * NG + lane / GL) * 4) = (uint32_t)step16 | ((uint32_t)lo16 << 16);
-    char* row = blk + w * kv4_codes_bytes(D) + at.slot * (D / 2);
-    if (w == 0) {
-      reinterpret_cast<uint32_t*>(row)[kv4_k_word(D, lane)] = codes;
-    } else {
-      // channels 16 i + 8 half + e, i = lane / 2, half = lane & 1: nibble
-      // 2 i + half of chunk e, so lanes 2 i and 2 i + 1 share byte i of it
-      const uint32_t other = __shfl_xor_sync(mask, codes, 1);
-      const int i = lane >> 1, odd = lane & 1;
-      const uint32_t even_c = odd ? other : codes, odd_c = odd ? codes : other;
-      uint8_t* bytes = reinterpret_cast<uint8_t*>(vrow[sub]);
+  }
+}
+
+template <typename T, int D, int G, int U>
+__global__ void __launch_bounds__(kKv4RowThreads) k_kv4_read(Kv4Dev kv, Kv4RowArgs a) {
+  constexpr int LANES = D / 8, ITEMS = kKv4RowThreads / LANES, GL = G / 8, NG = D / G;
+  __shared__ uint32_t vrow[ITEMS][U][D / 8];
+  pdl_prologue();
+  const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+  const unsigned mask = ((1ull << LANES) - 1ull) << ((threadIdx.x & 31) / LANES * LANES);
+  const Kv4Item it = kv4_item<U>(kv, a.tokens, (long long)blockIdx.x * ITEMS + sub);
+  if (it.rank >= kv.n) return;
+  Kv4Place at[U];
+  kv4_places<LANES, U>(kv, a.start, a.tokens, it.tok, at);
+  uint32_t kword[U], vword[U], par[U][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = 4 * odd + e;
-        bytes[kv4_v_chunk(D, c, at.slot) * (D / 16) + i] =
-            (uint8_t)(((even_c >> (4 * c)) & 15u) | (((odd_c >> (4 * c)) & 15u) << 4));
-      }
-      __syncwarp(mask);
-      reinterpret_cast<uint32_t*>(row)[lane] = vrow[sub][lane];
+  for (int u = 0; u < U; ++u) {
+    kword[u] = vword[u] = par[u][0] = par[u][1] = 0;
+    if (at[u].page < 0) continue;
+    const char* blk = kv4_block(kv, it.rank, a.layer, at[u].page, it.head, kv4_block_bytes(D, G));
+    kword[u] = reinterpret_cast<const uint32_t*>(blk + at[u].slot * (D / 2))[kv4_k_word(D, lane)];
+    vword[u] = reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + at[u].slot * (D / 2))[lane];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      par[u][w] = *reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D) + w * kv4_params_bytes(D, G) +
+                                                     (at[u].slot * NG + lane / GL) * 4);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) vrow[sub][u][lane] = vword[u];
+  __syncwarp(mask);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (at[u].page < 0) continue;
+    uint32_t vcodes = 0;
+    const uint8_t* bytes = reinterpret_cast<const uint8_t*>(vrow[sub][u]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t b = bytes[kv4_v_chunk(D, c, at[u].slot) * (D / 16) + (lane >> 1)];
+      vcodes |= ((b >> (4 * (lane & 1))) & 15u) << (4 * c);
+    }
+    const size_t dst = (size_t)(it.tok + u) * a.stride + (size_t)it.head * D + lane * 8;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const float step = Half16<T>::widen((uint16_t)par[u][w]), lo = Half16<T>::widen((uint16_t)(par[u][w] >> 16));
+      const uint32_t codes = w ? vcodes : kword[u];
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = lo + step * (float)((codes >> (4 * j)) & 15u);  // the product is exact
+      const uint4 out = make_uint4(Half16<T>::narrow2(x[0], x[1]), Half16<T>::narrow2(x[2], x[3]),
+                                   Half16<T>::narrow2(x[4], x[5]), Half16<T>::narrow2(x[6], x[7]));
+      *reinterpret_cast<uint4*>(static_cast<T*>(w ? a.v[it.rank] : a.k[it.rank]) + dst) = out;
     }
   }
 }
 
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kKv4RowThreads) k_kv4_read(Kv4Dev kv, Kv4RowArgs a) {
-  constexpr int LANES = D / 8, ITEMS = kKv4RowThreads / LANES, GL = G / 8, NG = D / G;
-  __shared__ uint32_t vrow[ITEMS][D / 8];
-  pdl_prologue();
-  const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
-  const unsigned mask = ((1ull << LANES) - 1ull) << ((threadIdx.x & 31) / LANES * LANES);
-  const long long item = (long long)blockIdx.x * ITEMS + sub;
-  const long long per_rank = (long long)a.tokens * kv.heads;
-  const int rank = (int)(item / per_rank);
-  if (rank >= kv.n) return;
-  const int tok = (int)(item % per_rank / kv.heads), head = (int)(item % kv.heads);
-  const Kv4Place at = kv4_place<LANES>(kv, a.start, tok);
-  if (at.page < 0) return;
-  const char* blk = kv4_block(kv, rank, a.layer, at.page, head, kv4_block_bytes(D, G));
-  const uint32_t kword = reinterpret_cast<const uint32_t*>(blk + at.slot * (D / 2))[kv4_k_word(D, lane)];
-  vrow[sub][lane] = reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + at.slot * (D / 2))[lane];
-  uint32_t par[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w)
-    par[w] = *reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D) + w * kv4_params_bytes(D, G) +
-                                                (at.slot * NG + lane / GL) * 4);
-  __syncwarp(mask);
-  uint32_t vcodes = 0;
-  const uint8_t* bytes = reinterpret_cast<const uint8_t*>(vrow[sub]);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint32_t b = bytes[kv4_v_chunk(D, c, at.slot) * (D / 16) + (lane >> 1)];
-    vcodes |= ((b >> (4 * (lane & 1))) & 15u) << (4 * c);
-  }
-  const size_t dst = (size_t)tok * a.stride + (size_t)head * D + lane * 8;
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const float step = Half16<T>::widen((uint16_t)par[w]), lo = Half16<T>::widen((uint16_t)(par[w] >> 16));
-    const uint32_t codes = w ? vcodes : kword;
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = lo + step * (float)((codes >> (4 * j)) & 15u);  // the product is exact
-    const uint4 out = make_uint4(Half16<T>::narrow2(x[0], x[1]), Half16<T>::narrow2(x[2], x[3]),
-                                 Half16<T>::narrow2(x[4], x[5]), Half16<T>::narrow2(x[6], x[7]));
-    *reinterpret_cast<uint4*>(static_cast<T*>(w ? a.v[rank] : a.k[rank]) + dst) = out;
-  }
+static const void* row_kernel_of(bool read, bool several) {
+  if (several) return read ? (const void*)&k_kv4_read<T, D, G, kKv4RowTokens> : (const void*)&k_kv4_append<T, D, G, kKv4RowTokens>;
+  return read ? (const void*)&k_kv4_read<T, D, G, 1> : (const void*)&k_kv4_append<T, D, G, 1>;
 }
-
 template <typename T>
-static const void* row_kernel_of(bool read, int dim, int group) {
-  if (dim == 128)
-    return group == 64 ? (read ? (const void*)&k_kv4_read<T, 128, 64> : (const void*)&k_kv4_append<T, 128, 64>)
-                       : (read ? (const void*)&k_kv4_read<T, 128, 32> : (const void*)&k_kv4_append<T, 128, 32>);
-  return group == 64 ? (read ? (const void*)&k_kv4_read<T, 64, 64> : (const void*)&k_kv4_append<T, 64, 64>)
-                     : (read ? (const void*)&k_kv4_read<T, 64, 32> : (const void*)&k_kv4_append<T, 64, 32>);
+static const void* row_kernel_for(bool read, int dim, int group, bool several) {
+  if (dim == 128) return group == 64 ? row_kernel_of<T, 128, 64>(read, several) : row_kernel_of<T, 128, 32>(read, several);
+  return group == 64 ? row_kernel_of<T, 64, 64>(read, several) : row_kernel_of<T, 64, 32>(read, several);
 }
-const void* kv4_row_kernel(bool fp16, bool read, int dim, int group) {
-  return fp16 ? row_kernel_of<__half>(read, dim, group) : row_kernel_of<__nv_bfloat16>(read, dim, group);
+const void* kv4_row_kernel(bool fp16, bool read, int dim, int group, bool several) {
+  return fp16 ? row_kernel_for<__half>(read, dim, group, several) : row_kernel_for<__nv_bfloat16>(read, dim, group, several);
 }
 
 }  // namespace dcc
@@ -211,12 +256,14 @@ int rows_call(bool read, const dcc_kv4_t* kv, int layer, void* const* k, void* c
   a.tokens = (int)tokens;
   a.layer = layer;
   const int per_cta = dcc::kKv4RowThreads / (kv->head_dim / 8);
-  const long long items = (long long)tokens * kv->kv_heads * kv->n_ranks;
+  const bool several = (long long)tokens * kv->kv_heads * kv->n_ranks >= dcc::kKv4ManyRows;
+  const long long per = several ? dcc::kKv4RowTokens : 1;
+  const long long items = ((long long)tokens + per - 1) / per * kv->kv_heads * kv->n_ranks;
   const long long grid = (items + per_cta - 1) / per_cta;
   if (grid > 0x7fffffffll) return DCC_ERR_INVALID_ARG;
   if ((rc = dcc_host::kv4_ready(&d)) != DCC_OK) return rc;
   void* args[] = {&d, &a};
-  return dcc_host::launch(dcc::kv4_row_kernel(kv->dtype == DCC_FP16, read, kv->head_dim, kv->group), (int)grid,
+  return dcc_host::launch(dcc::kv4_row_kernel(kv->dtype == DCC_FP16, read, kv->head_dim, kv->group, several), (int)grid,
                           dcc::kKv4RowThreads, false, args, static_cast<cudaStream_t>(s), 0, true);
 }
 

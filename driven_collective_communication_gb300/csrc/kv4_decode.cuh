@@ -23,12 +23,15 @@
 // the exponent of 64 put around it, is the fp16 number 64 + n: one AND-OR
 // makes two codes an operand register, after a shift for three nibbles of
 // four (the left one runs on the multiply pipe).  The 64 comes off the scores
-// as the accumulators' initial value (-64 sum q), and off O, with the 8,
-// through a product with a row of ones, which sums the same rounded p * step:
-// nothing is subtracted or converted per code.  (Bare nibbles are fp16
-// subnormals and need no exponent, one instruction fewer in seven, but the
-// tensor core aligns its sums by nominal exponents: measured, the sums lost
-// some 9 bits.)  The fragments take the codes where they lie (kv4.cuh).
+// as the accumulators' initial value (-64 sum q), and off O, with the 8, by a
+// product of the same rounded p * step with a constant -72 before each product
+// with codes: nothing is subtracted or converted per code.  (Taken off in the
+// end, through one row of ones, it would cost fewer products, but the
+// accumulators then carry 72 sum p * step all along, and the tensor core
+// truncates its sums: over 131k keys the result lost 3 bits.  Bare nibbles are
+// fp16 subnormals and need no exponent, one instruction fewer in seven, but
+// the tensor core aligns its sums by nominal exponents: measured, the sums
+// lost some 9 bits.)  The fragments take the codes where they lie (kv4.cuh).
 // mma.sync with its operands in registers suits this: the tensor work is 8
 // rows wide, and tcgen05 would want the unpacked operands written to shared
 // or tensor memory first, which costs more than the products.
@@ -69,14 +72,13 @@ struct AttnArgs {
 
 constexpr int kDecMaxCtas = 160;
 constexpr int kDecMaxWarps = 12;
-constexpr int kDecMaxRows = 16;
 // floats of a partial: m and l per row, then rows of O, padded so that the
 // fragments' stores fall into different banks
 __host__ __device__ constexpr int dec_slot(int rows, int dim) { return rows * (dim + 6); }
+constexpr int kDecMaxSlot = dec_slot(16, 128) > dec_slot(24, 64) ? dec_slot(16, 128) : dec_slot(24, 64);
 // workspace: a counter per CTA, two partials per CTA, one per warp
 __host__ __device__ constexpr size_t dec_ws_bytes() {
-  return 1024 + (size_t)kDecMaxCtas * 2 * dec_slot(kDecMaxRows, 128) * 4 +
-         (size_t)kDecMaxCtas * kDecMaxWarps * dec_slot(kDecMaxRows, 128) * 4;
+  return 1024 + (size_t)kDecMaxCtas * (2 + kDecMaxWarps) * kDecMaxSlot * 4;
 }
 
 // Warps and stages: as many bytes in flight as shared memory holds, three
@@ -84,10 +86,7 @@ __host__ __device__ constexpr size_t dec_ws_bytes() {
 template <int D, int G, int RT>
 struct DecShape {
   static constexpr int block = kv4_block_bytes(D, G);
-#ifndef DEC_W
-#define DEC_W 12
-#endif
-  static constexpr int warps = RT > 1 || 12 * 2 * block > 222 * 1024 ? 8 : DEC_W;
+  static constexpr int warps = RT > 1 || 12 * 2 * block > 222 * 1024 ? 8 : 12;
   static constexpr int fit = 222 * 1024 / (warps * block);
   static constexpr int stages = fit > 4 ? 4 : fit;
   static constexpr size_t smem = (size_t)warps * stages * block + 128;
@@ -161,13 +160,14 @@ struct DecCursor {
 };
 
 // Join `n` partials (by `at`) of one segment and store the result: to `part`
-// (a partial again) or to the outputs.  All threads of the CTA.  Eight
-// partials' loads are in flight at a time: they come from other SMs.
+// (a partial again) or to the outputs.  One thread's share: four channels of a
+// row (e).  Eight partials' loads are in flight at a time: they come from
+// other SMs.
 template <typename T, int D, int ROWS, typename At>
-__device__ __forceinline__ void dec_join(const AttnArgs& a, int n, At at, float* part, int rank, int head, int row0,
-                                         int rows, int begin) {
+__device__ __forceinline__ void dec_join(const AttnArgs& a, int e, int n, At at, float* part, int rank, int head,
+                                         int row0, int rows, int begin) {
   constexpr int kBatch = 8;
-  for (int e = threadIdx.x; e < ROWS * (D / 4); e += blockDim.x) {
+  {
     const int row = e / (D / 4), d4 = e % (D / 4);
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
   constexpr int W = Shape::warps, S = Shape::stages, BLK = Shape::block, THREADS = W * 32;
   constexpr int NG = D / G, ROWS = 8 * RT, JW = D / 32, MT = D / 16, SLOT = dec_slot(ROWS, D);
   constexpr float kCenter = 8.0f;
+  constexpr uint32_t kBias = 0xd480d480u;  // fp16 -72 = -(64 + kCenter), twice
   constexpr int kMinExp = -60;  // steps below 2^-60 count as that: 2^(14 + 60) a key still sums in fp32
   constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
   extern __shared__ __align__(128) char dec_smem[];
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
   // it (head), one still open at its end (tail); by first and last unit
   __shared__ long long s_seg[2 * W][2];
   __shared__ int s_who[2 * W][5];  // rank, head, first row; rows and first token of the sequence
-  __shared__ int s_list[2][W + 1];
+  __shared__ int s_list[2 * W], s_group[2 * W + 1], s_groups;
   __shared__ int s_open[2];        // CTAs that hold parts of the two segments open at the CTA's ends
   __shared__ int s_last[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
   uint32_t qf[2 * JW][2 * RT];  // Q^T fragments of each 16-channel step
   float q64[RT][NG][4];         // the scores' accumulators at their start
   float qsum[RT][NG][2], mx[RT][2], l[RT][2], pmid[RT][NG][2], cs[RT][2];
-  float o[RT][MT][4], ones[RT][NG][4];
+  float o[RT][MT][4];
   int ex = kMinExp, lim_hi[RT][2], lim_lo[RT][2], tile_hi = 0, tile_lo = 0, tile_end = 0;
   auto open = [&]() {
     const DecSeq sq = cuc.q;
@@ -454,8 +455,6 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
       for (int gr = 0; gr < NG; ++gr) {
         qs[gr] += __shfl_xor_sync(0xffffffffu, qs[gr], 1);
         qs[gr] += __shfl_xor_sync(0xffffffffu, qs[gr], 2);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ones[x][gr][e] = 0.0f;
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {  // of the rows that the accumulators hold here
@@ -589,7 +588,6 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
             pmid[x][gr][b] *= alpha[x][b];
-            ones[x][gr][b] *= alpha[x][b];
           }
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
@@ -640,14 +638,6 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
           }
         }
       }
-#pragma unroll
-      for (int x = 0; x < RT; ++x)
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          constexpr uint32_t one = 0x3c003c00u;
-          mma_16816(ones[x][gr], one, one, one, one, bp[x][gr][0], bp[x][gr][1]);
-          if (MASKED) mma_16816(ones[x][gr], one, one, one, one, bq[x][gr][0], bq[x][gr][1]);
-        }
       // V codes of the lane's chunk of 4 tokens: words of (first, second) key
       uint32_t v[2][2][JW / 2];
 #pragma unroll
@@ -673,19 +663,20 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
           const int g0 = 32 * q4 / G;
-          mma_16816(o[x][2 * q4], f0[0], f0[1], f0[2], f0[3], bp[x][g0][0], bp[x][g0][1]);
-          mma_16816(o[x][2 * q4 + 1], f1[0], f1[1], f1[2], f1[3], bp[x][g0][0], bp[x][g0][1]);
-          if (MASKED) {
-            mma_16816(o[x][2 * q4], f0[0], f0[1], f0[2], f0[3], bq[x][g0][0], bq[x][g0][1]);
-            mma_16816(o[x][2 * q4 + 1], f1[0], f1[1], f1[2], f1[3], bq[x][g0][0], bq[x][g0][1]);
-          }
+          auto both = [&](const uint32_t* b) {
+            mma_16816(o[x][2 * q4], kBias, kBias, kBias, kBias, b[0], b[1]);
+            mma_16816(o[x][2 * q4 + 1], kBias, kBias, kBias, kBias, b[0], b[1]);
+            mma_16816(o[x][2 * q4], f0[0], f0[1], f0[2], f0[3], b[0], b[1]);
+            mma_16816(o[x][2 * q4 + 1], f1[0], f1[1], f1[2], f1[3], b[0], b[1]);
+          };
+          both(bp[x][g0]);
+          if (MASKED) both(bq[x][g0]);
         }
       }
     }
   };
 
-  // The final value of each accumulator: less the codes' 64 and 8, and with the
-  // fp32 part.  Leaves l summed over the keys' lanes, and mx as R.
+  // The final value of each accumulator: with the fp32 part.  Leaves l summed over the keys' lanes, and mx as R.
   auto settle = [&]() {
 #pragma unroll
     for (int x = 0; x < RT; ++x)
@@ -699,7 +690,6 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
           float pm = pmid[x][gr][b];
 #pragma unroll
           for (int m = 4; m < 32; m <<= 1) pm += __shfl_xor_sync(0xffffffffu, pm, m);
-          pm = fmaf(-(64.0f + kCenter), ones[x][gr][b], pm);
 #pragma unroll
           for (int i = gr * G / 16; i < (gr + 1) * G / 16; ++i) {
             o[x][i][b] += pm;
@@ -839,35 +829,40 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
   if (threadIdx.x < 2) s_open[threadIdx.x] = 0;
   __syncthreads();
   int* counters = reinterpret_cast<int*>(a.ws);
-  int open_at[2] = {-1, -1};
-  int m0 = 0, flip = 0;
-  while (true) {
-    while (m0 < 2 * W && s_seg[m0][0] < 0) ++m0;
-    if (m0 >= 2 * W) break;
-    const long long first = s_seg[m0][0], end = s_seg[m0][1];
-    int n = 0, m1 = m0;  // the segment's partials, in order
-    for (; m1 < 2 * W; ++m1) {
-      if (s_seg[m1][0] < 0) continue;
-      if (s_seg[m1][0] != first) break;
-      if (threadIdx.x == 0) s_list[flip][n] = m1;
-      ++n;
+  // the segments' lists of partials, in order; all are joined side by side
+  if (warp == 0) {
+    const long long first = lane < 2 * W ? s_seg[lane][0] : -1;
+    const uint32_t there = __ballot_sync(0xffffffffu, first >= 0), below = there & ((1u << lane) - 1u);
+    const bool begins = first >= 0 && (below == 0 || s_seg[31 - __clz(below)][0] != first);
+    const uint32_t begin = __ballot_sync(0xffffffffu, begins);
+    if (first >= 0) s_list[__popc(below)] = lane;
+    if (begins) s_group[__popc(begin & ((1u << lane) - 1u))] = __popc(below);
+    if (lane == 0) {
+      s_groups = __popc(begin);
+      s_group[__popc(begin)] = __popc(there);
     }
-    __syncthreads();
-    const int* list = s_list[flip];
+  }
+  __syncthreads();
+  const int groups = s_groups;
+  constexpr int kShares = ROWS * (D / 4);
+  for (int it = threadIdx.x; it < groups * kShares; it += THREADS) {
+    const int grp = it / kShares, e = it - grp * kShares, l0 = s_group[grp], n = s_group[grp + 1] - l0, m = s_list[l0];
+    const long long first = s_seg[m][0], end = s_seg[m][1];
     auto local = [&](int i) {
-      const int m = list[i];
-      return (m & 1) ? tails + (size_t)(m >> 1) * SLOT : heads + (size_t)(m >> 1) * SLOT;
+      const int x = s_list[l0 + i];
+      return (x & 1) ? tails + (size_t)(x >> 1) * SLOT : heads + (size_t)(x >> 1) * SLOT;
     };
-    if (first >= c0 && end <= c1) {
-      dec_join<T, D, ROWS>(a, n, local, nullptr, s_who[m0][0], s_who[m0][1], s_who[m0][2], s_who[m0][3], s_who[m0][4]);
-    } else {
-      const int side = first < c0 ? 0 : 1;
-      open_at[side] = m0;
-      if (!(n == 1 && (m0 & 1) && end > c1))
-        dec_join<T, D, ROWS>(a, n, local, parts + side * SLOT, 0, 0, 0, 0, 0);
-    }
-    flip ^= 1;
-    m0 = m1;
+    const bool whole = first >= c0 && end <= c1;
+    if (!whole && n == 1 && (m & 1) && end > c1) continue;  // went straight to its place
+    dec_join<T, D, ROWS>(a, e, n, local, whole ? nullptr : parts + (first < c0 ? 0 : 1) * SLOT, s_who[m][0], s_who[m][1],
+                         s_who[m][2], s_who[m][3], s_who[m][4]);
+  }
+  // the segments open at the CTA's ends are the first and the last
+  int open_at[2] = {-1, -1};
+  if (groups > 0) {
+    const int m = s_list[0], z = s_list[s_group[groups - 1]];
+    if (s_seg[m][0] < c0) open_at[0] = m;
+    if (s_seg[z][1] > c1 && s_seg[z][0] >= c0) open_at[1] = z;
   }
   if (open_at[0] < 0 && open_at[1] < 0) return;
   // the CTA that comes last to an open segment joins its parts, in CTA order
@@ -895,7 +890,9 @@ __global__ void __launch_bounds__(DecShape<D, G, RT>::warps * 32, 1) k_kv4_decod
     if (s_last[side]) {
       const int f = s_open[side], m = open_at[side];
       auto remote = [&](int i) { return part_ws + ((size_t)(f + i) * 2 + (i == 0 ? 1 : 0)) * SLOT; };
-      dec_join<T, D, ROWS>(a, s_last[side], remote, nullptr, s_who[m][0], s_who[m][1], s_who[m][2], s_who[m][3], s_who[m][4]);
+      for (int e = threadIdx.x; e < kShares; e += THREADS)
+        dec_join<T, D, ROWS>(a, e, s_last[side], remote, nullptr, s_who[m][0], s_who[m][1], s_who[m][2], s_who[m][3],
+                             s_who[m][4]);
     }
 }
 

@@ -113,6 +113,30 @@ def test_append_then_read(dcc, dtype, dim, group, n, heads, lens, news, layer, l
             assert same[~touched].all()
 
 
+@pytest.mark.parametrize("dtype,dim,group", [("bf16", 128, 64), ("fp16", 64, 32), ("bf16", 64, 64), ("fp16", 128, 32)])
+def test_append_then_read_of_many_rows(dcc, dtype, dim, group):
+    """Batches large enough that a group of lanes takes several rows: runs that
+    cross sequences (some without rows) and pages, rows before position zero,
+    rows of no sequence at the end, a row count that is no multiple."""
+    n, heads = 8, 4
+    lens = [700, 3, 0, 64, 129] + [1] * 30 + [5, 401]
+    news = [650, 5, 0, 64, 2] + [1] * 30 + [0, 401]
+    g = torch.Generator().manual_seed(12)
+    cache, _, _ = make_cache(dcc, g, n, lens, heads, dim, group, dtype)
+    T = sum(news) + 67
+    k, v = ([torch.randn(T, heads, dim, generator=g).to(TD[dtype]) for _ in range(n)] for _ in range(2))
+    start = batch(news)
+    cache.append([x.cuda() for x in k], [x.cuda() for x in v], start)
+    ko, vo = ([torch.full((T, heads, dim), 7.0, dtype=TD[dtype], device="cuda") for _ in range(n)] for _ in range(2))
+    cache.read(ko, vo, start)
+    assert dcc.dcc_local_check() == dcc.DCC_OK
+    there = torch.tensor([m - t + i >= 0 for m, t in zip(lens, news) for i in range(t)] + [False] * 67)
+    for got, x in zip(ko + vo, k + v):
+        want = R.quantise(x, group, dtype).to(torch.float32).to(TD[dtype])
+        want[~there] = 7.0
+        assert torch.equal(got.cpu(), want)
+
+
 def test_append_of_special_values(dcc):
     """NaN and infinities read back as NaN in their own group only; a range
     that overflows the type as well; the largest finite values survive."""
