@@ -69,6 +69,37 @@ __device__ __forceinline__ Kv4Item kv4_item(const Kv4Dev& kv, int tokens, long l
   return {rank, (int)(item % per_rank / kv.heads) * U, (int)(item % kv.heads)};
 }
 
+// Two values at once, in their 16-bit type.
+template <typename T>
+struct MinMax;
+template <>
+struct MinMax<__half> {
+  static constexpr uint32_t kOne = 0x0400u;  // the exponent's last bit
+  __device__ static uint32_t min2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmin2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+template <>
+struct MinMax<__nv_bfloat16> {
+  static constexpr uint32_t kOne = 0x0080u;
+  __device__ static uint32_t min2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r =
+        __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+
+// d / step correctly rounded, as a division would: with inv = 1 / step correctly
+// rounded, the remainder of q = d * inv is exact and one step from it lands on
+// the correctly rounded quotient (Markstein's theorem; step is no number of
+// all-ones mantissa, it has at most 11 bits).  A division per value instead
+// took 64 instructions a value, 125 us where this takes the time given above.
+__device__ __forceinline__ float kv4_quotient(float d, float step, float inv) {
+  const float q = d * inv;
+  return fmaf(fmaf(-q, step, d), inv, q);
+}
+
 template <typename T, int D, int G, int U>
 __global__ void __launch_bounds__(kKv4RowThreads) k_kv4_append(Kv4Dev kv, Kv4RowArgs a) {
   constexpr int LANES = D / 8, ITEMS = kKv4RowThreads / LANES, GL = G / 8, NG = D / G;
@@ -95,40 +126,46 @@ __global__ void __launch_bounds__(kKv4RowThreads) k_kv4_append(Kv4Dev kv, Kv4Row
 #pragma unroll
     for (int w = 0; w < 2; ++w) {  // K, then V
       const uint32_t r[4] = {raw[u][w].x, raw[u][w].y, raw[u][w].z, raw[u][w].w};
-      float x[8];
+      // (min, -max) of the group, two values at a time; a NaN or an infinity is
+      // an exponent of all ones, which the addition carries into the sign
+      uint32_t lo2 = r[0], hi2 = r[0] ^ 0x80008000u, bad = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 f = Half16<T>::widen2(r[j]);
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
+        constexpr uint32_t one = MinMax<T>::kOne * 0x10001u;
+        bad |= (r[j] & 0x7fff7fffu) + one;
+        lo2 = MinMax<T>::min2(lo2, r[j]);
+        hi2 = MinMax<T>::min2(hi2, r[j] ^ 0x80008000u);
       }
-      float lo = x[0], hi = x[0];
-      bool bad = false;  // a NaN or an infinity
+      uint32_t ends = MinMax<T>::min2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        lo = fminf(lo, x[j]);
-        hi = fmaxf(hi, x[j]);
-        bad |= !(x[j] - x[j] == 0.0f);
-      }
-#pragma unroll
-      for (int m = 1; m < GL; m <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(mask, lo, m));
-        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, m));
-      }
-      const unsigned bads = __ballot_sync(mask, bad);
-      uint16_t step16 = Half16<T>::narrow(__fdiv_rn(hi - lo, 15.0f));
-      uint16_t lo16 = Half16<T>::narrow(lo);
-      const float step = Half16<T>::widen(step16);
-      bad = ((bads >> ((threadIdx.x & 31) / GL * GL)) & ((1u << GL) - 1u)) != 0u || !(step - step == 0.0f);
+      for (int m = 1; m < GL; m <<= 1) ends = MinMax<T>::min2(ends, __shfl_xor_sync(mask, ends, m));
+      const unsigned bads = __ballot_sync(mask, (bad & 0x80008000u) != 0u);
+      const float2 e2 = Half16<T>::widen2(ends);
+      float lo = e2.x;
+      uint16_t step16 = Half16<T>::narrow(__fdiv_rn(-e2.y - lo, 15.0f)), lo16 = (uint16_t)ends;
+      float step = Half16<T>::widen(step16);
       uint32_t codes = 0;
-      if (bad) {
+      if (((bads >> ((threadIdx.x & 31) / GL * GL)) & ((1u << GL) - 1u)) != 0u || !(step - step == 0.0f)) {
         step16 = lo16 = Half16<T>::narrow(__uint_as_float(0x7fc00000u));
       } else if (step > 0.0f) {
+        // steps whose reciprocal may overflow: the group times 2^100 (a step is
+        // at least 2^-12 of the group's values, so nothing overflows)
+        const float up = step < 1e-25f ? 1.2676506002282294e30f : 1.0f;
+        step *= up;
+        lo *= up;
+        const float inv = __fdiv_rn(1.0f, step);
+        // adding 1.5 * 2^23 rounds to the nearest even integer, whose bits end
+        // the sum's; the constant's own come off all eight at once
+        constexpr float kMagic = 12582912.0f;
+        constexpr uint32_t kMagicBits = 0x4b400000u * 0x11111111u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float c = fminf(fmaxf(rintf(__fdiv_rn(x[j] - lo, step)), 0.0f), 15.0f);
-          codes |= (uint32_t)c << (4 * j);
+        for (int j = 3; j >= 0; --j) {
+          const float2 f = Half16<T>::widen2(r[j]);
+          const float c0 = fminf(kv4_quotient(fmaf(f.x, up, -lo), step, inv), 15.0f) + kMagic;
+          const float c1 = fminf(kv4_quotient(fmaf(f.y, up, -lo), step, inv), 15.0f) + kMagic;
+          codes = (codes * 16u + __float_as_uint(c1)) * 16u + __float_as_uint(c0);
         }
+        codes -= kMagicBits;
       }
       if (lane % GL == 0)
         *reinterpret_cast<uint32_t*>(blk + 2 * kv4_codes_bytes(D) + w * kv4_params_bytes(D, G) +
@@ -201,7 +238,7 @@ __global__ void __launch_bounds__(kKv4RowThreads) k_kv4_read(Kv4Dev kv, Kv4RowAr
       const uint32_t codes = w ? vcodes : kword[u];
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = lo + step * (float)((codes >> (4 * j)) & 15u);  // the product is exact
+      for (int j = 0; j < 8; ++j) x[j] = fmaf(step, (float)((codes >> (4 * j)) & 15u), lo);
       const uint4 out = make_uint4(Half16<T>::narrow2(x[0], x[1]), Half16<T>::narrow2(x[2], x[3]),
                                    Half16<T>::narrow2(x[4], x[5]), Half16<T>::narrow2(x[6], x[7]));
       *reinterpret_cast<uint4*>(static_cast<T*>(w ? a.v[it.rank] : a.k[it.rank]) + dst) = out;
