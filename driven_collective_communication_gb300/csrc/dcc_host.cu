@@ -369,7 +369,9 @@ bool visit_kernels(F&& visit) {
           return false;
   }
   for (int i = 0; i < 3; ++i)
-    if (!v(dcc::kv4_pages_kernel(i)) || !v(dcc::linear_kernel(i))) return false;
+    if (!v(dcc::linear_kernel(i))) return false;
+  for (int i = 0; i < 5; ++i)
+    if (!v(dcc::kv4_pages_kernel(i))) return false;
   return v(dcc::ring_barrier_kernel()) && v(dcc::ring_barrier_cluster_kernel()) && v(dcc::channel_put_kernel()) &&
          v(dcc::channel_get_kernel());
 }

@@ -48,9 +48,22 @@ const void* kv4_attention_kernel(bool fp16, int dim, int group, int which) {
 }  // namespace dcc
 
 namespace {
-// Query rows per kv head (new tokens x the heads that share it) above which
-// the prompt kernel runs.
-constexpr long long kPromptMinRows = 64;
+// Whether the prompt kernel runs.  It keeps the tensor cores busy but does not
+// split a segment's keys over CTAs; the streaming kernel spreads any work
+// evenly but goes over the cache once per row tile.  Per key, on GB300: a
+// wave of the prompt kernel takes 0.017 us, a pass of the streaming kernel
+// over one segment 5.6e-5 us, a 300th; with few pages its latency shows and it
+// is a 100th.  (`segments`: ranks x kv heads x sequences.)  Measured,
+// streaming / prompt, us, 8 heads per kv head of 128 channels: 8 segments of
+// 8192 keys, 64 tokens 121 / 154, 128 tokens 224 / 154; 1 segment of 60,000
+// keys, 128 tokens 200 / 1027; 128 segments of up to 4096 keys, 4 tokens 68 /
+// 75, 8 tokens 115 / 75, 128 tokens 1876 / 235; 8 segments of 700 keys x 4
+// heads, 64 tokens 29.8 / 29.5, 128 tokens 43 / 30.
+bool prompt_runs(long long segments, long long rows, int dim, int max_pages, int sms) {
+  const long long tile = dim == 64 ? 24 : 16, passes = (rows + tile - 1) / tile;
+  const long long ctas = segments * ((rows + dcc::kPromptRows - 1) / dcc::kPromptRows), waves = (ctas + sms - 1) / sms;
+  return rows > 16 && segments * passes > (max_pages <= 32 ? 100 : 300) * waves;
+}
 }  // namespace
 
 extern "C" {
@@ -121,7 +134,7 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
   const bool fp16 = kv->dtype == DCC_FP16;
   const long long rows = (long long)max_new * a.share;
   cudaStream_t st = static_cast<cudaStream_t>(s);
-  if (rows > kPromptMinRows) {
+  if (prompt_runs((long long)kv->n_ranks * kv->kv_heads * kv->seqs, rows, kv->head_dim, kv->max_pages, sms)) {
     const dcc::Kernel k = dcc::prompt(fp16, kv->head_dim, kv->group);
     if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
     const long long grid = (rows + dcc::kPromptRows - 1) / dcc::kPromptRows * kv->n_ranks * kv->kv_heads * kv->seqs;

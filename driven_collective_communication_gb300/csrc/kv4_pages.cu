@@ -6,11 +6,13 @@
 // in order, both by prefix sums; reference counts change by atomic adds,
 // whose order does not show.
 //
-// Two kernels.  The first is one cluster of 8 CTAs: each CTA owns one eighth
-// of the pages (and strides over the sequences), the phases are separated by
-// cluster barriers, and the CTAs' totals are exchanged through their
-// workspace words -- the scan of the counts is the only long part, and eight
-// SMs read them eight times as fast as one, without a launch per phase.  It
+// Two kernels.  The first is one CTA, or for large pools one cluster of 8: each
+// CTA owns one eighth of the pages (and strides over the sequences), the
+// phases are separated by barriers, and the CTAs' totals are exchanged through
+// their workspace words -- the scan of the counts is the only long part, and
+// eight SMs read them eight times as fast as one, without a launch per phase.
+// It is bound by latency, and a cluster's barrier with its fence costs more
+// than a CTA's (BOOK_MEASURED).  It
 // writes the list of page copies to the workspace.  The second kernel copies:
 // the number of copies is only known on the device, so its CTAs (as many as
 // the GPU holds) stride over (copy, rank, layer, chunk), 16 bytes a thread and
@@ -22,6 +24,9 @@ namespace dcc {
 
 constexpr int kBookCtas = 8;       // one portable cluster
 constexpr int kBookThreads = 1024;
+// Up to this many page counts, and as many table entries to go through, one CTA
+// keeps the books: 4 to a thread.
+constexpr long long kBookOneCta = 4 * kBookThreads;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;     // 16-byte vectors a thread has in flight
 
@@ -45,7 +50,12 @@ struct BookArgs {
   PagesWs ws;
 };
 
-__device__ __forceinline__ void book_sync() {  // the whole grid is one cluster
+template <int CTAS>
+__device__ __forceinline__ void book_sync() {  // the whole grid is one CTA or one cluster
+  if (CTAS == 1) {
+    __syncthreads();
+    return;
+  }
   __threadfence();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -87,12 +97,13 @@ __device__ __forceinline__ void book_bad(const Kv4Dev& kv, int what) {
   atomicCAS(kv.status, 0ull, kStatusBounds | ((unsigned long long)(uint32_t)what << 32));
 }
 
-// The pages this CTA looks after: one eighth of them, in order.
+// The pages this CTA looks after: an equal part of them, in order.
 struct Span {
   int b, e;
 };
+template <int CTAS>
 __device__ __forceinline__ Span my_pages(int pages, int cta) {
-  return {(int)((long long)pages * cta / kBookCtas), (int)((long long)pages * (cta + 1) / kBookCtas)};
+  return {(int)((long long)pages * cta / CTAS), (int)((long long)pages * (cta + 1) / CTAS)};
 }
 // Counts are read past L1: other CTAs' atomics change them.
 __device__ __forceinline__ int ld_count(const int32_t* p) { return __ldcg(p); }
@@ -128,11 +139,12 @@ __device__ __forceinline__ int book_want(const Kv4Dev& kv, const BookArgs& a, in
   return *ok && add > 0 ? (int)pages - (len + kKv4Page - 1) / kKv4Page : 0;
 }
 
+template <int CTAS>
 __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a, int mode) {
   __shared__ int smem[32];
   pdl_prologue();
   const int cta = (int)blockIdx.x, tid = cta * kBookThreads + (int)threadIdx.x;
-  constexpr int kAll = kBookCtas * kBookThreads;
+  constexpr int kAll = CTAS * kBookThreads;
   constexpr long long kCap = 1 << 30;
   const PagesWs ws = a.ws;
   const int n_req = mode == kBookReserve ? kv.seqs : a.count;
@@ -141,13 +153,13 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
   for (int i = tid; i < kWsWords; i += kAll) ws.w[i] = 0;
   if (mode != kBookReserve) {
     for (int i = tid; i < kv.seqs; i += kAll) ws.mark[i] = 0x7fffffff;
-    book_sync();
+    book_sync<CTAS>();
     for (int i = tid; i < n_req; i += kAll) {
       const int d = a.dst[i];
       if (d >= 0 && d < kv.seqs) atomicMin(&ws.mark[d], i);
       else book_bad(kv, d);
     }
-    book_sync();
+    book_sync<CTAS>();
     // the dropped sequences give up their pages: one warp per sequence
     int skipped = 0;
     for (int i = tid >> 5; i < n_req; i += kAll / 32) {
@@ -169,10 +181,10 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
     }
     if (skipped && mode == kBookFree) atomicAdd(&ws.w[kWsFails], skipped);
   }
-  book_sync();
+  book_sync<CTAS>();
 
   // free pages, by CTA
-  const Span my = my_pages(kv.pages, cta);
+  const Span my = my_pages<CTAS>(kv.pages, cta);
   int mine = 0;
   for (int p = my.b + (int)threadIdx.x; p < my.e; p += kBookThreads) mine += ld_count(kv.refs + p) == 0;
   mine = cta_sum(mine, smem);
@@ -193,9 +205,9 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
     }
     if (threadIdx.x == 0) ws.pre[n_req] = (int)(base < kCap ? base : kCap);
   }
-  book_sync();
+  book_sync<CTAS>();
   int nfree = 0, before = 0;
-  for (int c = 0; c < kBookCtas; ++c) {
+  for (int c = 0; c < CTAS; ++c) {
     const int t = __ldcg(ws.w + kWsTotal + c);
     if (c < cta) before += t;
     nfree += t;
@@ -210,7 +222,7 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
   }
   const int wanted = __ldcg(ws.pre + n_req);
   list_free(kv, my, before, wanted < nfree ? wanted : nfree, ws.to, smem);
-  book_sync();
+  book_sync<CTAS>();
 
   // serve the requests: one warp each
   int fails = 0, given = 0;
@@ -265,7 +277,7 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
   if (fails) atomicAdd(&ws.w[kWsFails], fails);
   if (given) atomicAdd(&ws.w[kWsFreed], given);
   // forks are served in order of their place in the list, so the copies are its first entries
-  book_sync();
+  book_sync<CTAS>();
   if (tid == 0) {
     const int g = __ldcg(ws.w + kWsFreed);
     ws.w[kWsCopies] = mode == kBookFork ? g : 0;
@@ -285,20 +297,21 @@ struct CompactArgs {
   PagesWs ws;
 };
 
+template <int CTAS>
 __global__ void __launch_bounds__(kBookThreads) k_kv4_compact_book(Kv4Dev kv, CompactArgs a) {
   __shared__ int smem[32];
   pdl_prologue();
   const int cta = (int)blockIdx.x, tid = cta * kBookThreads + (int)threadIdx.x;
-  constexpr int kAll = kBookCtas * kBookThreads;
+  constexpr int kAll = CTAS * kBookThreads;
   const PagesWs ws = a.ws;
-  const Span my = my_pages(kv.pages, cta);
+  const Span my = my_pages<CTAS>(kv.pages, cta);
   int mine = 0;
   for (int p = my.b + (int)threadIdx.x; p < my.e; p += kBookThreads) mine += kv.refs[p] > 0;
   mine = cta_sum(mine, smem);
   if (threadIdx.x == 0) ws.w[kWsTotal + cta] = mine;
-  book_sync();
+  book_sync<CTAS>();
   int live = 0, live_before = 0;
-  for (int c = 0; c < kBookCtas; ++c) {
+  for (int c = 0; c < CTAS; ++c) {
     const int t = __ldcg(ws.w + kWsTotal + c);
     if (c < cta) live_before += t;
     live += t;
@@ -311,9 +324,9 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_compact_book(Kv4Dev kv, Co
   for (int p = my.b + (int)threadIdx.x; p < my.e && p < live; p += kBookThreads) low += kv.refs[p] > 0;
   low = cta_sum(low, smem);
   if (threadIdx.x == 0) ws.w[kWsTotal + 8 + cta] = low;
-  book_sync();
+  book_sync<CTAS>();
   int low_before = 0, low_all = 0;
-  for (int c = 0; c < kBookCtas; ++c) {
+  for (int c = 0; c < CTAS; ++c) {
     const int t = __ldcg(ws.w + kWsTotal + 8 + c);
     if (c < cta) low_before += t;
     low_all += t;
@@ -338,13 +351,13 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_compact_book(Kv4Dev kv, Co
     slot += ts;
     mover += tm;
   }
-  book_sync();
+  book_sync<CTAS>();
   for (int i = tid; i < moves; i += kAll) {
     const int p = __ldcg(ws.from + i), q = __ldcg(ws.to + i);
     a.remap[p] = q;
     a.new_refs[q] = kv.refs[p];
   }
-  book_sync();  // (new_refs may be refs) the movers' counts have been read
+  book_sync<CTAS>();  // (new_refs may be refs) the movers' counts have been read
   for (int p = live + tid; p < kv.pages; p += kAll) a.new_refs[p] = 0;
   if (tid == 0) {
     ws.w[kWsCopies] = moves;
@@ -406,9 +419,11 @@ __global__ void __launch_bounds__(kCopyThreads) k_kv4_copy(Kv4Dev kv, CopyArgs a
 
 const void* kv4_pages_kernel(int i) {
   switch (i) {
-    case 0: return (const void*)&k_kv4_book;
-    case 1: return (const void*)&k_kv4_compact_book;
-    case 2: return (const void*)&k_kv4_copy;
+    case 0: return (const void*)&k_kv4_book<1>;
+    case 1: return (const void*)&k_kv4_book<kBookCtas>;
+    case 2: return (const void*)&k_kv4_compact_book<1>;
+    case 3: return (const void*)&k_kv4_compact_book<kBookCtas>;
+    case 4: return (const void*)&k_kv4_copy;
     default: return nullptr;
   }
 }
@@ -442,7 +457,7 @@ int copy_launch(const dcc_kv4_t* kv, dcc::Kv4Dev& d, dcc::CopyArgs& a, cudaStrea
   a.vecs = (unsigned)((size_t)kv->kv_heads * dcc::kv4_block_bytes(kv->head_dim, kv->group) / 16);
   constexpr unsigned per = dcc::kCopyThreads * dcc::kCopyUnroll;
   a.chunks = (a.vecs + per - 1) / per;
-  const void* fn = dcc::kv4_pages_kernel(2);
+  const void* fn = dcc::kv4_pages_kernel(4);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -453,6 +468,13 @@ int copy_launch(const dcc_kv4_t* kv, dcc::Kv4Dev& d, dcc::CopyArgs& a, cudaStrea
   if (per_sm < 1) return DCC_ERR_LAUNCH;
   void* args[] = {&d, &a};
   return launch(fn, sms * per_sm, dcc::kCopyThreads, false, args, s, 0, true);
+}
+
+// Kernel `which` for one CTA, which + 1 for a cluster, by the numbers to go through.
+int launch_book(int which, long long numbers, void** args, cudaStream_t s) {
+  const bool one = numbers <= dcc::kBookOneCta;
+  return launch(dcc::kv4_pages_kernel(one ? which : which + 1), one ? 1 : dcc::kBookCtas, dcc::kBookThreads, false, args,
+                s, 0, true, one ? 0 : dcc::kBookCtas);
 }
 
 int book_call(const dcc_kv4_t* kv, int mode, const int32_t* src, const int32_t* dst, size_t count, int32_t* info,
@@ -470,7 +492,8 @@ int book_call(const dcc_kv4_t* kv, int mode, const int32_t* src, const int32_t* 
   a.info = info;
   if ((rc = dcc_host::kv4_ready(&d)) != DCC_OK) return rc;
   void* args[] = {&d, &a, &mode};
-  rc = launch(dcc::kv4_pages_kernel(0), dcc::kBookCtas, dcc::kBookThreads, false, args, s, 0, true, dcc::kBookCtas);
+  const long long rows = mode == dcc::kBookReserve ? 0 : (long long)count * kv->max_pages;
+  rc = launch_book(0, kv->pages > rows ? kv->pages : rows, args, s);
   if (rc != DCC_OK || mode != dcc::kBookFork || count == 0) return rc;
   dcc::CopyArgs c{};
   c.from = a.ws.from;
@@ -538,7 +561,7 @@ int dcc_kv4_compact(const dcc_kv4_t* kv, int32_t* new_table, int32_t* new_refs, 
   if ((rc = dcc_host::kv4_ready(&d)) != DCC_OK) return rc;
   void* args[] = {&d, &a};
   cudaStream_t st = static_cast<cudaStream_t>(s);
-  rc = launch(dcc::kv4_pages_kernel(1), dcc::kBookCtas, dcc::kBookThreads, false, args, st, 0, true, dcc::kBookCtas);
+  rc = launch_book(2, kv->pages, args, st);
   if (rc != DCC_OK) return rc;
   dcc::CopyArgs c{};
   c.from = a.ws.from;

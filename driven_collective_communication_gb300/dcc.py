@@ -168,9 +168,18 @@ def _ptrs(xs):
     return (ctypes.c_void_p * len(xs))(*[_ptr(x) for x in xs])
 
 
+def _current_stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+    def _current_stream():  # noqa: F811  the same handle without a Stream object: 0.2 us instead of 3 a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _stream(s):
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, torch.cuda.Stream):
         return s.cuda_stream
     return int(s)

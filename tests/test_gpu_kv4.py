@@ -9,8 +9,9 @@ truncation, per operation): keys may enter the first product rounded to the
 type (u per element), so a score is off by at most ds = (u + (D + 8) e) *
 scale * sum|q K|; the probabilities are off by a factor within exp(+-2 ds) and
 another rounding u, values by u, sums of n terms by n e relative to sum p|V|,
-and the result is rounded once:
-  |out - exact| <= (2 u + expm1(2 ds) + 2 n e) * sum p|V| (1 + small) + u |exact|
+and the result is rounded once (by half the smallest subnormal, 2^-25 in fp16,
+where it lies below the normal numbers):
+  |out - exact| <= (2 u + expm1(2 ds) + 2 n e) * sum p|V| (1 + small) + u |exact| + tiny
   |lse - exact| <= ds + n e + 4 e |lse|
 """
 import math
@@ -23,6 +24,7 @@ import kv4_reference as R
 pytestmark = pytest.mark.gpu
 TD, U, PAGE = R.TD, R.U, R.PAGE
 E = 2.0 ** -23
+TINY = {"bf16": 1e-30, "fp16": 2.0 ** -25}
 
 
 @pytest.fixture(scope="module")
@@ -214,7 +216,7 @@ def check_attention(dcc, dtype, dim, group, n, heads, share, lens, news, window=
                     o, l, pv, mag = R.attention(Kh, Vh, qq, pos, window, sc)
                     o, l, pv, mag = o.cuda(), l.cuda(), pv.cuda(), mag.cuda()
                     ds = (u + (dim + 8) * E) * mag
-                    tol = (2 * u + torch.expm1(2 * ds) + 2 * max(m, 1) * E)[:, None] * pv * 1.01 + u * o.abs() + 1e-30
+                    tol = (2 * u + torch.expm1(2 * ds) + 2 * max(m, 1) * E)[:, None] * pv * 1.01 + u * o.abs() + TINY[dtype]
                     err = (got_o[rows, h * share + x] - o).abs()
                     assert (err <= tol).all(), (r, s, h, x, (err / tol).max())
                     if with_lse:
@@ -303,6 +305,96 @@ def test_nan_reaches_only_the_rows_that_see_it(dcc, new):
         sees = torch.arange(m - new, m) >= m - 30
         bad = out[:new].isnan().any(-1).any(-1).cpu()
         assert torch.equal(bad, sees) and not out[new:].isnan().any()
+
+
+# The prompt kernel runs where (ranks x kv heads x sequences) x (rows / 16)
+# passes 100 (few pages): these do.
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group", [(64, 32), (64, 64), (128, 32), (128, 64)])
+@pytest.mark.parametrize("heads,share,lens,news,window", [
+    (4, 4, [90, 300, 64, 1], [30, 20, 25, 1], 0),        # a single, partial row tile
+    (2, 8, [16, 200, 129], [16, 33, 129], 0),            # exactly one row tile; two
+    (1, 3, [2000, 30, 500, 0], [90, 90, 85, 4], 70),     # window, more rows than tokens, an idle slot
+    (4, 16, [65, 1000], [17, 40], 1), (4, 1, [128, 256, 383], [128, 100, 129], 0)])
+def test_prompt_kernel(dcc, dtype, dim, group, heads, share, lens, news, window):
+    check_attention(dcc, dtype, dim, group, 8, heads, share, lens, news, window, extra_rows=2)
+
+
+def test_prompt_kernel_scores_scales_and_streams(dcc):
+    check_attention(dcc, "bf16", 128, 64, 8, 2, 8, [500, 64], [60, 40], scale=4.0)
+    check_attention(dcc, "fp16", 64, 32, 8, 2, 8, [500, 300], [60, 100], scale=-2.0)
+    check_attention(dcc, "fp16", 128, 32, 8, 2, 8, [500, 64], [60, 40], scale=0.0)
+    check_attention(dcc, "bf16", 128, 64, 8, 2, 8, [500, 64], [60, 40], with_lse=False, strided=True, layers=2, layer=1,
+                    stream=torch.cuda.Stream(), max_new=60)
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("dtype,group", [("bf16", 64), ("fp16", 32)])
+def test_nan_in_the_prompt_kernel(dcc, which, dtype, group):
+    g = torch.Generator().manual_seed(10)
+    n, m, new = 8, 200, 60
+    cache, _, _ = make_cache(dcc, g, n, [m, m], 1, 128, group, dtype)
+    x = torch.randn(2 * m, 1, 128, generator=g).to(TD[dtype])
+    y = x.clone()
+    y[m - 30, 0, 5], y[m - 10, 0, 120] = math.nan, math.inf
+    k, v = (y, x) if which == "k" else (x, y)
+    cache.append([k.cuda()] * n, [v.cuda()] * n, batch([m, m]))
+    q = torch.randn(2 * new, 8, 128, generator=g).to(TD[dtype]).cuda()
+    out = [torch.empty_like(q) for _ in range(n)]
+    cache.attention([q] * n, out, batch([new, new]), max_new=new, workspace=cache.attention_workspace(8))
+    sees = torch.arange(m - new, m) >= m - 30
+    for o in out:
+        assert torch.equal(o[:new].isnan().any(-1).any(-1).cpu(), sees) and not o[new:].isnan().any()
+
+
+def test_bad_pages_in_the_prompt_kernel(dcc):
+    """A missing page is skipped: its keys are seen by nobody."""
+    g = torch.Generator().manual_seed(11)
+    n, lens, new = 8, [300, 300], 100
+    cache, _, table = make_cache(dcc, g, n, lens, 1, 128, 64, "bf16")
+    q = [torch.randn(2 * new, 8, 128, generator=g).bfloat16().cuda() for _ in range(n)]
+    out = [torch.empty_like(x) for x in q]
+    cache.table[1, 2] = cache.pages + 3
+    cache.attention(q, out, batch([new, new]), max_new=new, workspace=cache.attention_workspace(8))
+    assert dcc.dcc_local_check() == dcc.DCC_ERR_BOUNDS
+    K, V = R.values(cache.pools[3][0], 128, 64, "bf16")
+    keep = torch.tensor([j for j in range(300) if not 128 <= j < 192])
+    pg = table[1, :5].long().cuda()
+    Kh, Vh = K[pg, 0].reshape(-1, 128)[:300].cpu(), V[pg, 0].reshape(-1, 128)[:300].cpu()
+    for i in (0, 57, 99):
+        pos = 200 + i
+        seen = keep[keep <= pos]
+        for h in (0, 7):
+            o, _, pv, mag = R.attention(Kh[seen], Vh[seen], q[3][new + i, h].double().cpu()[None],
+                                        torch.tensor([10 ** 6]), 0, 128 ** -0.5)
+            ds = (U["bf16"] + 136 * E) * mag
+            tol = (2 * U["bf16"] + torch.expm1(2 * ds) + 600 * E)[:, None] * pv * 1.01 + U["bf16"] * o.abs()
+            assert ((out[3][new + i, h].cpu().double() - o).abs() <= tol).all()
+
+
+def test_prompt_kernel_past_four_gigabytes(dcc):
+    block = R.block_bytes(128, 64)
+    pages = (1 << 32) // block + 300
+    pool = torch.zeros(1, pages, 1, block, dtype=torch.uint8, device="cuda")
+    row = [pages - 1, 3, pages - 200]
+    one = dcc.Kv4Cache([pool], torch.tensor([row], dtype=torch.int32, device="cuda"),
+                       torch.tensor([150], dtype=torch.int32, device="cuda"), None, 1, 128, 64, "bf16")
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(150, 1, 128, generator=g).bfloat16() for _ in range(2))
+    one.append([k.cuda()], [v.cuda()], batch([150]))
+    many = dcc.Kv4Cache([pool], torch.tensor([row] * 16, dtype=torch.int32, device="cuda"),
+                        torch.full((16,), 150, dtype=torch.int32, device="cuda"), None, 1, 128, 64, "bf16")
+    q = torch.randn(1600, 4, 128, generator=g).bfloat16()
+    out = torch.empty(1600, 4, 128, dtype=torch.bfloat16, device="cuda")
+    many.attention([q.cuda()], [out], batch([100] * 16), max_new=100, workspace=many.attention_workspace(4))
+    K, V = R.quantise(k, 64, "bf16")[:, 0], R.quantise(v, 64, "bf16")[:, 0]
+    for s in (0, 15):
+        for h in (0, 3):
+            rows = slice(100 * s, 100 * s + 100)
+            o, _, pv, mag = R.attention(K, V, q[rows, h].double(), torch.arange(50, 150), 0, 128 ** -0.5)
+            ds = (U["bf16"] + 136 * E) * mag
+            tol = (2 * U["bf16"] + torch.expm1(2 * ds) + 300 * E)[:, None] * pv * 1.01 + U["bf16"] * o.abs()
+            assert ((out[rows, h].cpu().double() - o).abs() <= tol).all()
 
 
 def test_pages_past_four_gigabytes(dcc):
