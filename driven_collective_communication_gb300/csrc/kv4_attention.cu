@@ -93,7 +93,9 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
   const size_t width = (size_t)q_heads * kv->head_dim;
   if (tokens > (size_t)1 << 26 || q_stride > (size_t)1 << 32 || (tokens > 1 && q_stride < width))
     return DCC_ERR_INVALID_ARG;
+  if (tokens * (size_t)(q_heads / kv->kv_heads) > (size_t)1 << 30) return DCC_ERR_INVALID_ARG;  // rows are 32-bit
   if (tokens == 0) return DCC_OK;
+  if ((size_t)max_new > tokens) max_new = (int)tokens;
   const size_t qb = ((tokens - 1) * q_stride + width) * 2, ob = tokens * width * 2, lb = tokens * q_heads * 4;
   const size_t pool = (size_t)kv->layers * kv->pages * kv->kv_heads * dcc::kv4_block_bytes(kv->head_dim, kv->group);
   dcc::AttnArgs a{};
@@ -137,7 +139,18 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
   if (prompt_runs((long long)kv->n_ranks * kv->kv_heads * kv->seqs, rows, kv->head_dim, kv->max_pages, sms)) {
     const dcc::Kernel k = dcc::prompt(fp16, kv->head_dim, kv->group);
     if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
-    const long long grid = (rows + dcc::kPromptRows - 1) / dcc::kPromptRows * kv->n_ranks * kv->kv_heads * kv->seqs;
+    // whole waves of 256-row tiles; what is left in 128-row tiles if they fit one wave
+    const long long segments = (long long)kv->n_ranks * kv->kv_heads * kv->seqs;
+    long long wide = (rows + dcc::kPromptRows - 1) / dcc::kPromptRows, narrow = 0;
+    const long long whole = segments * wide / sms * sms / segments;
+    const long long left = (rows - whole * dcc::kPromptRows + 127) / 128;
+    if (whole < wide && segments * left <= sms) {
+      wide = whole;
+      narrow = left;
+    }
+    if (wide > (1 << 24)) return DCC_ERR_INVALID_ARG;
+    a.wide = (int)wide;
+    const long long grid = (wide + narrow) * segments;
     if (grid > 0x7fffffffll) return DCC_ERR_INVALID_ARG;
     dcc::DevComm dc{};
     dc.n = kv->n_ranks;
