@@ -40,7 +40,11 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-ftz=fal
 SOURCES = ["dcc_host.cu", "sync_kernels.cu", "coll_allgather.cu",
            "coll_int32.cu", "coll_fp32.cu", "coll_fp16.cu", "coll_bf16.cu", "noalloc.cu",
            "proxy.cu", "coll_fused_bulk.cu", "coll_max.cu", "coll_min.cu", "coll_fused_mma.cu",
-           "ops_status.cu", "kv4_cache.cu", "kv4_pages.cu", "kv4_attention.cu", "linear.cu"]
+           "ops_status.cu", "kv4_cache.cu", "kv4_pages.cu", "kv4_attention.cu",
+           "kv4_attention_bf16.cu", "kv4_attention_fp16.cu", "linear.cu"]
+# Sources without data accesses that DCC_CHECK_BOUNDS checks (their kernels check
+# what they read from tables by themselves): one object serves both builds.
+SHARED = [s for s in SOURCES if s.startswith(("kv4_", "linear", "ops_"))]
 
 
 def nvcc():
@@ -128,8 +132,13 @@ def _build_locked(verbose, extra_flags, lib, objdir):
     write_tuning_header()
     os.makedirs(objdir, exist_ok=True)
 
+    deps = _deps()
+
     def compile_one(src):
-        obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
+        shared = src in SHARED and "-DDCC_CHECK_BOUNDS=1" in extra_flags
+        obj = os.path.join(BUILD if shared else objdir, os.path.splitext(src)[0] + ".o")
+        if shared and not _stale(obj, deps):
+            return obj
         cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)

@@ -365,7 +365,8 @@ bool visit_kernels(F&& visit) {
         if (!v(dcc::kv4_row_kernel(fp16, false, dim, group, false)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group, false)) ||
             !v(dcc::kv4_row_kernel(fp16, false, dim, group, true)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group, true)) ||
             !v(dcc::kv4_attention_kernel(fp16, dim, group, 1)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 2)) ||
-            !v(dcc::kv4_attention_kernel(fp16, dim, group, 3)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 0)))
+            !v(dcc::kv4_attention_kernel(fp16, dim, group, 3)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 0)) ||
+            !v(dcc::kv4_attention_kernel(fp16, dim, group, 4)))
           return false;
   }
   for (int i = 0; i < 3; ++i)

@@ -1,50 +1,12 @@
 // kv4_attention.cu -- host side of the attention over the 4-bit cache.
 #include "comm.h"
-#include "kv4_prompt.cuh"
+#include "kv4_attention.cuh"
 
 namespace dcc {
-namespace {
-struct Kernel {
-  const void* fn;
-  int threads;
-  size_t smem;
-};
-template <typename T, int D, int G, int RT>
-Kernel decode_of() {
-  using S = DecShape<D, G, RT>;
-  return {(const void*)&k_kv4_decode<T, D, G, RT>, S::warps * 32, S::smem};
+AttnKernel attn_kernel(bool fp16, int dim, int group, int which) {
+  return fp16 ? attn_kernel_fp16(dim, group, which) : attn_kernel_bf16(dim, group, which);
 }
-template <typename T, int RT>
-Kernel decode_for(int dim, int group) {
-  if (dim == 128) return group == 64 ? decode_of<T, 128, 64, RT>() : decode_of<T, 128, 32, RT>();
-  return group == 64 ? decode_of<T, 64, 64, RT>() : decode_of<T, 64, 32, RT>();
-}
-template <typename T>
-Kernel decode_wide(int group) {  // 24 rows: 64-wide heads have the registers
-  return group == 64 ? decode_of<T, 64, 64, 3>() : decode_of<T, 64, 32, 3>();
-}
-Kernel decode(bool fp16, int dim, int group, int tiles) {
-  if (tiles > 2 && dim == 64) return fp16 ? decode_wide<__half>(group) : decode_wide<__nv_bfloat16>(group);
-  if (tiles > 1) return fp16 ? decode_for<__half, 2>(dim, group) : decode_for<__nv_bfloat16, 2>(dim, group);
-  return fp16 ? decode_for<__half, 1>(dim, group) : decode_for<__nv_bfloat16, 1>(dim, group);
-}
-template <typename T, int D, int G>
-Kernel prompt_of() {
-  return {(const void*)&k_kv4_prompt<T, D, G>, kPromptThreads, PromptShape<D, G>::smem};
-}
-template <typename T>
-Kernel prompt_for(int dim, int group) {
-  if (dim == 128) return group == 64 ? prompt_of<T, 128, 64>() : prompt_of<T, 128, 32>();
-  return group == 64 ? prompt_of<T, 64, 64>() : prompt_of<T, 64, 32>();
-}
-Kernel prompt(bool fp16, int dim, int group) {
-  return fp16 ? prompt_for<__half>(dim, group) : prompt_for<__nv_bfloat16>(dim, group);
-}
-}  // namespace
-// which: 1 to 3 row tiles of the streaming kernel (3: 64-wide heads), 0 the prompt kernel
-const void* kv4_attention_kernel(bool fp16, int dim, int group, int which) {
-  return which == 0 ? prompt(fp16, dim, group).fn : decode(fp16, dim, group, which).fn;
-}
+const void* kv4_attention_kernel(bool fp16, int dim, int group, int which) { return attn_kernel(fp16, dim, group, which).fn; }
 }  // namespace dcc
 
 namespace {
@@ -137,7 +99,7 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
   const long long rows = (long long)max_new * a.share;
   cudaStream_t st = static_cast<cudaStream_t>(s);
   if (prompt_runs((long long)kv->n_ranks * kv->kv_heads * kv->seqs, rows, kv->head_dim, kv->max_pages, sms)) {
-    const dcc::Kernel k = dcc::prompt(fp16, kv->head_dim, kv->group);
+    const dcc::AttnKernel k = dcc::attn_kernel(fp16, kv->head_dim, kv->group, dcc::kAttnPrompt);
     if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
     // whole waves of 256-row tiles; what is left in 128-row tiles if they fit one wave
     const long long segments = (long long)kv->n_ranks * kv->kv_heads * kv->seqs;
@@ -163,7 +125,10 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
   // Row tiles: as few passes over the cache as the registers allow, then the
   // fewest rows that make that many.
   const int most = kv->head_dim == 64 ? 3 : 2, passes = ((int)rows + 8 * most - 1) / (8 * most);
-  const dcc::Kernel k = dcc::decode(fp16, kv->head_dim, kv->group, ((int)rows + 8 * passes - 1) / (8 * passes));
+  const long long most_units = (long long)kv->n_ranks * kv->kv_heads * kv->seqs * kv->max_pages;
+  const bool small = rows <= 8 && most_units <= (long long)sms * dcc::kDecSmallWarps;
+  const dcc::AttnKernel k = dcc::attn_kernel(fp16, kv->head_dim, kv->group,
+                                             small ? dcc::kAttnSmall : ((int)rows + 8 * passes - 1) / (8 * passes));
   if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
   void* args[] = {&d, &a};
   return dcc_host::launch(k.fn, sms < dcc::kDecMaxCtas ? sms : dcc::kDecMaxCtas, k.threads, false, args, st, k.smem,
