@@ -19,8 +19,8 @@
 // tile's P is made, the tensor cores work on the other's.
 //
 // Measured on GB300, bf16, 2048 new tokens on 8192 keys, 8 ranks x 8 query heads
-// x 128 channels: 531 us, 0.91 PFLOP/s, 48 % of a library product's rate (the
-// MMAs alone: 326 us; 512 CTAs in 3.4 waves cost 15 %).  What bounds it is
+// x 128 channels: 520 us, 0.93 PFLOP/s, 49 % of a library product's rate (the
+// MMAs alone: 326 us).  What bounds it is
 // shared memory: the S products read 128 bytes a clock, all there is, and the
 // unpacking warps' accesses and every barrier queue behind them.  Tried without
 // gain: separate warps for K and V, a row of scores held in registers, P handed

@@ -164,6 +164,7 @@ int run_mma(const dcc::LinArgs& l, bool fp16, dcc::DevComm& dc, cudaStream_t s) 
   const Plan& p = better ? pair : one;
   if (p.rounds < 1 || clusters(r, p.fn, p.threads, p.ks, p.smem) < 1) return DCC_ERR_LAUNCH;
   dcc::LinMaps maps;
+  std::memset(&maps, 0, sizeof maps);
   for (int i = 0; i < l.n; ++i) {
     rc = make_map(l.w[i], (size_t)l.k, (size_t)l.rows, (unsigned)p.bm, fp16, &maps.w[i]);
     if (rc == DCC_OK && (i == 0 || l.x[i] != l.x[i - 1]))
@@ -204,6 +205,7 @@ int run_big(const dcc::LinArgs& l, bool fp16, dcc::DevComm& dc, cudaStream_t s) 
   const long long tiles = (long long)l.n * a.row_tiles * a.tok_tiles;
   if (tiles > 0x3fffffffll) return DCC_ERR_INVALID_ARG;
   dcc::LinMaps maps;
+  std::memset(&maps, 0, sizeof maps);
   for (int i = 0; i < l.n; ++i) {
     rc = make_map(l.w[i], (size_t)l.k, (size_t)l.rows, 128, fp16, &maps.w[i]);
     if (rc == DCC_OK && (i == 0 || l.x[i] != l.x[i - 1]))

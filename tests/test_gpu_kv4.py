@@ -273,6 +273,16 @@ def test_large_and_tiny_scores(dcc):
     check_attention(dcc, "bf16", 64, 32, 1, 2, 2, [500, 300], [100, 2], scale=-0.5)
 
 
+@pytest.mark.parametrize("dtype,dim,group", [("bf16", 128, 64), ("fp16", 64, 32)])
+def test_zero_scale_and_unusual_queries(dcc, dtype, dim, group):
+    """Scale 0 (every key counts the same), queries far from 1, many tiny pages."""
+    check_attention(dcc, dtype, dim, group, 1, 1, 8, [500, 64, 0], [1, 1, 1], scale=0.0)
+    check_attention(dcc, dtype, dim, group, 1, 2, 3, [500, 70], [4, 1], scale=1e-4, q_scale=1000.0)
+    check_attention(dcc, dtype, dim, group, 1, 1, 8, [300], [1], scale=1000.0, q_scale=1e-3)
+    check_attention(dcc, "bf16", dim, group, 2, 1, 8, [300, 20], [1, 1], scale=1e-28, q_scale=1e27)
+    check_attention(dcc, dtype, dim, group, 1, 1, 2, [33] * 700, [1] * 700)  # more sequences than a CTA's threads
+
+
 def test_without_lse_layers_and_strided_queries(dcc):
     check_attention(dcc, "bf16", 128, 64, 2, 2, 4, [100, 300], [1, 1], with_lse=False, layers=3, layer=2, strided=True)
     check_attention(dcc, "fp16", 64, 32, 2, 2, 4, [100, 300], [90, 20], with_lse=False, layers=2, layer=1, strided=True)
