@@ -53,7 +53,7 @@
 //
 // Measured on GB300, bf16, 8 ranks x 1 kv head x 8 query heads x 128 channels, G
 // = 64, one token each: 64 sequences of up to 8192 keys 92 us (326 MB, 3.5 TB/s,
-// 52 % of a plain copy's rate); one of 777 keys 14 us.  fp16, 2 kv heads x 4, G =
+// 52 % of a plain copy's rate); one of 777 keys 13 us.  fp16, 2 kv heads x 4, G =
 // 32, one sequence of 131,109 keys: 89 us (336 MB, 3.8 TB/s).  The loads alone
 // take 74 and 63 us, loads and scores 82 and 69: of the rest about 10 us are the
 // start (plan, page numbers, first pages) and 10 the joins and uneven ends, and
@@ -92,8 +92,8 @@ __host__ __device__ constexpr size_t dec_ws_bytes() {
 
 // Warps and stages: as many bytes in flight as shared memory holds, three
 // warps to a scheduler where a tile's registers allow (8 rows), two otherwise.
-// SMALL: four warps with two stages, two or three CTAs to an SM, for calls whose pages
-// are no more than the warps of one such wave: the next kernel's CTAs then find
+// SMALL: four warps with two stages, two CTAs to an SM, for calls whose pages are
+// no more than the warps of one such wave: the next kernel's CTAs then find
 // room beside this one's and start under its end (measured on GB300, one
 // sequence of 777 keys, 8 ranks, back to back: 13.0 us instead of 13.6).
 template <int D, int G, int RT, bool SMALL>

@@ -6,29 +6,39 @@
 // keys x 256 rows take 2048 clocks of either on an SM).  A CTA owns 256 query
 // rows of one (sequence, rank, kv head) -- new tokens times the heads that
 // share it -- as two tiles of 128, and walks the keys in steps of 128 (two
-// pages).  The pages are unpacked once per step into 16-bit tiles in shared
-// memory, for both row tiles: K_j and V_j = lo + step * code, rounded once to
-// the cache's type (2^-9 or 2^-12 of a value whose own 4-bit step is a
-// fifteenth of its group's range).  Then per row tile
+// pages).  The pages are unpacked once per step into fp16 tiles in shared
+// memory, for both row tiles: K_j and V_j = lo + step * code, rounded once (2^-12
+// of a value whose own 4-bit step is a fifteenth of its group's range).  Then per
+// row tile
 //   S = Q K^T            tcgen05, Q and K in shared memory, S in tensor memory;
-//   P = 2^(c S - ref)    fp32, rounded to 16 bits, over S in tensor memory;
+//   P = 2^(c S - ref)    fp32, rounded to fp16, over S in tensor memory;
 //   O += P V             tcgen05, P in tensor memory, V^T in shared memory.
 // ref is a row's reference: it follows the running maximum only when that
 // grew by more than 2^8 (then O is rescaled in tensor memory), which is rare
 // after the first steps; sums l are fp32, of the unrounded P.  While one row
 // tile's P is made, the tensor cores work on the other's.
 //
-// Measured on GB300, bf16, 2048 new tokens on 8192 keys, 8 ranks x 8 query heads
-// x 128 channels: 520 us, 0.93 PFLOP/s, 49 % of a library product's rate (the
-// MMAs alone: 326 us).  What bounds it is
-// shared memory: the S products read 128 bytes a clock, all there is, and the
-// unpacking warps' accesses and every barrier queue behind them.  Tried without
-// gain: separate warps for K and V, a row of scores held in registers, P handed
-// over in halves, an MMA warp that polls both tiles.
+// The bf16 cache's operands are fp16 as well: with bf16 tiles (2^-9) three
+// roundings put the output 3.0e-3 off where its own rounding is 1.7e-3 (441
+// keys); now it is the latter.  Q's rows are scaled by a power of two, exactly.
+// Keys of K out of fp16's range have a power of two of their own, which is put
+// back on S; a page with such a V stays bf16, and so do its P.  Neither is met
+// in ordinary caches, so their forms are short rather than fast.
 //
-// Roles (448 threads): warp 0 loads pages (one bulk copy each, three in
+// Measured on GB300, 2048 new tokens on 8192 keys, 8 ranks x 8 query heads x 128
+// channels: fp16 523 us, 0.93 PFLOP/s; bf16 551 us, 0.88 PFLOP/s, 46 % of a
+// library product's rate (the MMAs alone: 326 us; bf16 tiles: 521 us).  What
+// bounds it is shared memory (the S products read 128 bytes a clock, all there
+// is, and the unpacking warps' accesses and every barrier queue behind them) and
+// the instructions of P and the unpacking.  Tried without gain: separate warps
+// for K and V, a row of scores held in registers, P handed over in halves, an
+// MMA warp that polls both tiles, rings of K's and V's codes apart (a deeper
+// prefetch: 542 us for 523).
+//
+// Roles (512 threads): warp 0 loads pages (one bulk copy each, three in
 // flight); warp 1 issues the MMAs; warps 2..5 unpack; warps 6..9 and 10..13
-// make P of the two row tiles, one row per thread.
+// make P of the two row tiles, one row per thread; warps 14 and 15 take the bf16
+// cache's parameters to fp16, each those of its slots of the ring.
 //
 // The last wave of CTAs would leave most SMs idle where the row tiles are few
 // more than the SMs hold: the host then cuts the rows left over, which see the
@@ -51,7 +61,7 @@
 
 namespace dcc {
 
-constexpr int kPromptThreads = 448;
+constexpr int kPromptThreads = 512;
 constexpr int kPromptRows = 256;  // per CTA: two tiles of 128
 constexpr int kPromptRing = 3;    // pages in flight
 
@@ -104,6 +114,24 @@ __device__ __forceinline__ uint32_t param_bad(uint32_t w) {
 }
 constexpr uint32_t kBad = 0x80008000u;
 
+// The bf16 cache's parameters as fp16 operands.  A group's largest magnitude m
+// decides: fp16 holds the group to 2^-13 of m for m from 2^-8 up.
+__device__ __forceinline__ float2 param_floats(uint32_t w) {  // step, lo
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float param_top(uint32_t w) {
+  const float2 p = param_floats(w);
+  return fmaxf(fabsf(p.y), fabsf(fmaf(15.0f, p.x, p.y)));
+}
+__device__ __forceinline__ bool fp16_fits(float m, float top) { return m == 0.0f || (m >= 0x1p-8f && m <= top); }
+__device__ __forceinline__ uint32_t param_half(uint32_t w) {
+  const float2 p = param_floats(w);
+  return Half16<__half>::narrow2(p.x, p.y);
+}
+__device__ __forceinline__ float power2(int e) { return __int_as_float((127 + e) << 23); }  // e from -126 to 127
+constexpr float kTopK = 0x1p15f;  // larger groups of K do not fit fp16
+constexpr float kTopV = 0x1p11f;  // the smallest P that fp16 holds, times this, is 2^-12 of a V of 2^-8
+
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, const __grid_constant__ AttnArgs a, DevComm dc) {
   using Shape = PromptShape<D, G>;
@@ -113,12 +141,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   extern __shared__ unsigned char prompt_raw[];
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t s_absent[8];  // by step: bits of pages that are not there
+  // bf16 cache, by step and page: 1 where a key of K has its own scale, 2 where V stays bf16
+  __shared__ __align__(2) uint8_t s_range[8][2];
+  __shared__ int8_t s_exp[4][128];  // by step: K's powers of two
   const uint32_t base = (smem_addr_u32(prompt_raw) + 1023u) & ~1023u;
   const uint32_t sq = base, sk = sq + 2 * Shape::q_tile, sv = sk + 2 * Shape::kv_tile, raw = sv + 2 * Shape::kv_tile;
-  const unsigned char* raw_g = prompt_raw + (raw - smem_addr_u32(prompt_raw));
+  unsigned char* raw_g_rw = prompt_raw + (raw - smem_addr_u32(prompt_raw));
+  const unsigned char* raw_g = raw_g_rw;
   const uint32_t bars = raw + (uint32_t)(R * BLK);
   auto rawf = [&](int s) { return bars + 8u * (uint32_t)s; };
   auto rawe = [&](int s) { return bars + 8u * (uint32_t)(R + s); };
+  auto ready = [&](int s) { return bars + 8u * (uint32_t)(2 * R + 16 + s); };
   auto two = [&](int kind, int i) { return bars + 8u * (uint32_t)(2 * R + 2 * kind + i); };
   enum { kFull = 0, kFree, vFull, vFree, sFull, pFull, pvDone, qFull };  // the last: one for both
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -127,6 +160,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
     for (int i = 0; i < R; ++i) {
       mma_mbar_init(rawf(i), 1);
       mma_mbar_init(rawe(i), 4);
+      mma_mbar_init(ready(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mma_mbar_init(two(kFull, i), 4);
@@ -177,6 +211,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;  // S / P of the two row tiles, then O: 128 columns each
+  auto range = [&](int j) { return FP16 ? 0u : (uint32_t)*reinterpret_cast<const volatile uint16_t*>(s_range[j & 7]); };
+  auto wide_v = [&](int j, int h) { return (range(j) & (2u << 8 * h)) != 0; };
+  const int len = min(kv.len[seq], pos_hi + 1);  // keys that some row may see
   auto wait = [&](uint32_t bar, int phase) { return mma_mbar_wait(bar, (uint32_t)phase & 1u, dc, rank, head); };
 
   if (warp == 0) {  // ---- loads
@@ -206,9 +243,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
     for (int p = max(0, unfinished - R); p < unfinished; ++p) wait(rawf(p % R), p / R);
   } else if (warp == 1) {  // ---- MMAs
     if (lane == 0) {
-      const uint32_t ab = FP16 ? 0u : 1u;
-      const uint32_t id = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(128 >> 4) << 24);
+      const uint32_t id = (1u << 4) | ((uint32_t)(128 >> 4) << 24);  // fp16 operands; bf16: bits 7 and 10
       const uint32_t id_s = id | ((uint32_t)(128 >> 3) << 17), id_o = id | ((uint32_t)(D >> 3) << 17);
+      uint32_t rg0 = 0, rg1 = 0;  // of even and odd steps
       bool ok = true;
       auto scores = [&](int g, int j) {
         ok = ok && wait(two(kFull, j & 1), j >> 1);
@@ -227,6 +264,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         }
         tc_commit(two(sFull, g));
         if (g == nt - 1) tc_commit(two(kFree, j & 1));
+        (j & 1 ? rg1 : rg0) = range(j);
       };
       for (int g = 0; g < nt; ++g) ok = ok && wait(two(qFull, g), 0);
       for (int g = 0; g < nt; ++g) scores(g, 0);
@@ -235,6 +273,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           ok = wait(two(pFull, g), j) && wait(two(vFull, j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
+          const uint32_t bf = (1u << 7) | (1u << 10);
+          const uint32_t ids[2] = {id_o | ((j & 1 ? rg1 : rg0) & 2u ? bf : 0u), id_o | ((j & 1 ? rg1 : rg0) & 0x200u ? bf : 0u)};
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint64_t bd = mma_smem_desc(sv + (uint32_t)((j & 1) * Shape::kv_tile) + (uint32_t)(kk / 4) * (D * 128u) +
@@ -242,7 +282,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
             asm volatile(
                 "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem + 256u + (uint32_t)g * 128u),
-                "r"(tmem + (uint32_t)g * 128u + (uint32_t)kk * 8u), "l"(bd), "r"(id_o), "r"(j > 0 || kk > 0 ? 1u : 0u)
+                "r"(tmem + (uint32_t)g * 128u + (uint32_t)kk * 8u), "l"(bd), "r"(ids[kk / 4]), "r"(j > 0 || kk > 0 ? 1u : 0u)
                 : "memory");
           }
           if (g == nt - 1) tc_commit(two(vFree, j & 1));
@@ -253,8 +293,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
     __syncwarp();
   } else if (warp < 6) {  // ---- unpack
     const int tid = (int)threadIdx.x - 64;
-    const int len = min(kv.len[seq], pos_hi + 1);  // keys that some row may see
     bool ok = true;
+    auto done_with = [&](int p) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rawe(p % R));
+    };
     for (int j = 0; j < steps && ok; ++j) {
       const int buf = j & 1;
       const uint32_t kt = sk + (uint32_t)(buf * Shape::kv_tile), vt = sv + (uint32_t)(buf * Shape::kv_tile);
@@ -263,12 +307,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
 #pragma unroll 1
       for (int h = 0; h < 2 && ok; ++h) {  // K of the two pages
         const int p = 2 * j + h, slot = p % R;
-        ok = wait(rawf(slot), p / R);
+        ok = wait(rawf(slot), p / R) && (FP16 || wait(ready(slot), p / R));
         if (!ok) break;
         absent = s_absent[j & 7];
-        if ((absent >> h) & 1u) continue;
+        const bool there = !((absent >> h) & 1u);
         const unsigned char* blk = raw_g + slot * BLK;
         const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D));
+        if (!there) continue;
         // eight neighbouring lanes take the four quarters of rows r and r ^ 5
         // (other half of the banks, other half of the swizzled chunks): no
         // bank conflicts on either side
@@ -278,8 +323,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           const int key = (2 * ((tid >> 3) + 16 * pass)) ^ ((tid & 4) ? 5 : 0);
           uint32_t step[NG], lo[NG];
           uint32_t bad = 0;
+          if constexpr (FP16)
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) bad |= param_bad<T>(par[(kKv4Page + key) * NG + gr]);
+            for (int gr = 0; gr < NG; ++gr) bad |= param_bad<T>(par[(kKv4Page + key) * NG + gr]);
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
             const uint32_t w = (bad & kBad) ? 0xffffffffu : par[key * NG + gr];  // NaN
@@ -299,10 +345,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
 #pragma unroll
           for (int jj = 0; jj < JW; ++jj) {
             const int u = 4 * jj + t, gr = 32 * jj / G;  // channels 8 u ..
-            const uint4 v = make_uint4(Pair16<T>::value(Pair16<T>::template code<0>(w[jj]), step[gr], lo[gr]),
-                                       Pair16<T>::value(Pair16<T>::template code<1>(w[jj]), step[gr], lo[gr]),
-                                       Pair16<T>::value(Pair16<T>::template code<2>(w[jj]), step[gr], lo[gr]),
-                                       Pair16<T>::value(Pair16<T>::template code<3>(w[jj]), step[gr], lo[gr]));
+            const uint4 v = make_uint4(Pair16<__half>::value(Pair16<__half>::code<0>(w[jj]), step[gr], lo[gr]),
+                                       Pair16<__half>::value(Pair16<__half>::code<1>(w[jj]), step[gr], lo[gr]),
+                                       Pair16<__half>::value(Pair16<__half>::code<2>(w[jj]), step[gr], lo[gr]),
+                                       Pair16<__half>::value(Pair16<__half>::code<3>(w[jj]), step[gr], lo[gr]));
             sts128(row + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (key & 7)) * 16), v);
           }
         }
@@ -320,15 +366,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
 #pragma unroll 1
       for (int h = D == 128 ? 0 : tid >> 6; h < 2; h += D == 128 ? 1 : 2) {
         const int p = 2 * j + h;
+        if (D == 128 && h) done_with(p - 1);
         const unsigned char* blk = raw_g + (p % R) * BLK;
         const int c = tid & 7, oct = D == 128 ? tid >> 4 : (tid >> 3) & 7, ws = D == 128 ? (tid >> 3) & 1 : 0;
         const int swap = D == 128 ? oct & 1 : 0;
         const uint32_t sel0 = swap ? 0x1054u : 0x5410u, sel1 = swap ? 0x3276u : 0x7632u;
         const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D)) + kKv4Page * NG;
-        const bool there = !((absent >> h) & 1u);
+        const bool there = !((absent >> h) & 1u), wide = !FP16 && wide_v(j, h);
         // the word's channels lie in one group (G = 64) or two (32)
         const int g0 = 64 * ws / G;
         constexpr int GW = G == 32 ? 2 : 1;
+        if (wide) {  // rare, so little code rather than fast: two keys of a channel at a time
+#pragma unroll 1
+          for (int i = 0; i < 32; ++i) {
+            const int n = i >> 2, gr = g0 + (GW > 1 ? n >> 2 : 0), d = 64 * ws + 16 * (n >> 1) + c + 8 * (n & 1);
+            float v[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int key = 8 * oct + 2 * (i & 3) + x;
+              const uint32_t word = *reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + key * (D / 2) +
+                                                                       kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
+              const uint32_t pw = par[key * NG + gr];
+              const float2 f = param_floats(pw);
+              const bool none = (param_bad<T>(pw) & kBad) || !there || (page0 + p) * kKv4Page + key >= len;
+              v[x] = none ? 0.0f : fmaf((float)((word >> (4 * n)) & 15u), f.x, f.y);
+            }
+            const uint32_t pair = Half16<T>::narrow2(v[0], v[1]);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(vt + (uint32_t)h * (D * 128u) + (uint32_t)d * 128u +
+                                                         (uint32_t)((oct ^ (d & 7)) * 16 + 4 * (i & 3))),
+                         "r"(pair)
+                         : "memory");
+          }
+          continue;
+        }
         uint32_t w[8], pr[8][GW], bad = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -338,7 +408,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
 #pragma unroll
           for (int x = 0; x < GW; ++x) {
             pr[k][x] = par[key * NG + g0 + x];
-            bad |= param_bad<T>(pr[k][x]);
+            bad |= param_bad<__half>(pr[k][x]);
           }
         }
         if ((bad & kBad) || !there || (page0 + p) * kKv4Page + 8 * oct + 7 >= len)  // some key must be zero
@@ -347,7 +417,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
             const int key = 8 * oct + (k ^ swap);
             uint32_t any = 0;  // (another group of the key may be bad: its own unit sees to it)
 #pragma unroll
-            for (int x = 0; x < GW; ++x) any |= param_bad<T>(pr[k][x]);
+            for (int x = 0; x < GW; ++x) any |= param_bad<__half>(pr[k][x]);
             if ((any & kBad) || !there || (page0 + p) * kKv4Page + key >= len)
 #pragma unroll
               for (int x = 0; x < GW; ++x) pr[k][x] = 0u;
@@ -360,14 +430,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           const uint32_t step1 = GW > 1 ? __byte_perm(pr[k0][GW - 1], pr[k1][GW - 1], sel0) : step0;
           const uint32_t lo1 = GW > 1 ? __byte_perm(pr[k0][GW - 1], pr[k1][GW - 1], sel1) : lo0;
           const uint32_t x0 = __byte_perm(w[k0], w[k1], sel0), x1 = __byte_perm(w[k0], w[k1], sel1);
-          out[0][e] = Pair16<T>::value(Pair16<T>::template code<0>(x0), step0, lo0);
-          out[1][e] = Pair16<T>::value(Pair16<T>::template code<1>(x0), step0, lo0);
-          out[2][e] = Pair16<T>::value(Pair16<T>::template code<2>(x0), step0, lo0);
-          out[3][e] = Pair16<T>::value(Pair16<T>::template code<3>(x0), step0, lo0);
-          out[4][e] = Pair16<T>::value(Pair16<T>::template code<0>(x1), step1, lo1);
-          out[5][e] = Pair16<T>::value(Pair16<T>::template code<1>(x1), step1, lo1);
-          out[6][e] = Pair16<T>::value(Pair16<T>::template code<2>(x1), step1, lo1);
-          out[7][e] = Pair16<T>::value(Pair16<T>::template code<3>(x1), step1, lo1);
+          out[0][e] = Pair16<__half>::value(Pair16<__half>::template code<0>(x0), step0, lo0);
+          out[1][e] = Pair16<__half>::value(Pair16<__half>::template code<1>(x0), step0, lo0);
+          out[2][e] = Pair16<__half>::value(Pair16<__half>::template code<2>(x0), step0, lo0);
+          out[3][e] = Pair16<__half>::value(Pair16<__half>::template code<3>(x0), step0, lo0);
+          out[4][e] = Pair16<__half>::value(Pair16<__half>::template code<0>(x1), step1, lo1);
+          out[5][e] = Pair16<__half>::value(Pair16<__half>::template code<1>(x1), step1, lo1);
+          out[6][e] = Pair16<__half>::value(Pair16<__half>::template code<2>(x1), step1, lo1);
+          out[7][e] = Pair16<__half>::value(Pair16<__half>::template code<3>(x1), step1, lo1);
         }
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
@@ -380,8 +450,75 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(two(vFull, buf));
-        mbar_arrive(rawe((2 * j) % R));
+        if (D == 64) mbar_arrive(rawe((2 * j) % R));
         mbar_arrive(rawe((2 * j + 1) % R));
+      }
+    }
+  } else if (warp >= 14) {  // ---- the bf16 cache's parameters, in place as fp16
+    if constexpr (!FP16) {
+      // a slot's pages are all one warp's: one that skipped a page of a slot could
+      // take the barrier's state before that page for the next page's arrival
+      for (int p = 0; p < 2 * steps; ++p) {
+        const int slot = p % R, j = p >> 1, h = p & 1;
+        if ((slot == 1) != (warp == 15)) continue;
+        if (!wait(rawf(slot), p / R)) break;
+        uint32_t ranges = 0;
+        if (!((s_absent[j & 7] >> h) & 1u)) {
+          uint32_t* par = reinterpret_cast<uint32_t*>(raw_g_rw + slot * BLK + 2 * kv4_codes_bytes(D));
+          uint32_t k[2][NG], v[2][NG], most = 0, least = 0xffffffffu;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+              k[x][gr] = par[(lane + 32 * x) * NG + gr];
+              v[x][gr] = par[(kKv4Page + lane + 32 * x) * NG + gr];
+              const uint32_t a = k[x][gr] & 0x7fff7fffu, b = v[x][gr] & 0x7fff7fffu;
+              most = __vmaxu2(most, __vmaxu2(a, b));
+              least = __vminu2(least, __vminu2(a, b));
+            }
+          // Mostly all are far inside: steps of 2^-10 .. 2^6 and lo up to 2^10
+          // make groups of 2^-8 .. 2^11.
+          const bool inside = (least & 0xffffu) >= 0x3a80u && (most & 0xffffu) <= 0x4280u && (most >> 16) <= 0x4480u;
+          if (!__all_sync(0xffffffffu, inside)) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int key = lane + 32 * x;
+              const bool counts = (page0 + p) * kKv4Page + key < len;
+              uint32_t bad = 0;
+              float m = 0.0f;
+              bool fits = true;
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) {
+                m = fmaxf(m, param_top(k[x][gr]));
+                fits = fits && fp16_fits(param_top(v[x][gr]), kTopV);
+                bad |= param_bad<T>(v[x][gr]);
+              }
+              const int e = fp16_fits(m, kTopK) ? 0 : max(-120, min(126, (int)(__float_as_uint(m) >> 23) - 127));
+              s_exp[j & 3][64 * h + key] = (int8_t)e;
+              ranges |= counts ? (e ? 1u : 0u) | (fits ? 0u : 2u) : 0u;
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) {
+                const float2 f = param_floats(k[x][gr]);
+                par[key * NG + gr] = (bad & kBad) ? 0xffffffffu : Half16<__half>::narrow2(f.x * power2(-e), f.y * power2(-e));
+              }
+            }
+            ranges = __reduce_or_sync(0xffffffffu, ranges);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) par[(lane + 32 * x) * NG + gr] = param_half(k[x][gr]);
+          }
+          if (!(ranges & 2u))
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) par[(kKv4Page + lane + 32 * x) * NG + gr] = param_half(v[x][gr]);
+        }
+        if (lane == 0) s_range[j & 7][h] = (uint8_t)ranges;
+        // (the fence before a new page comes over these is the readers')
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready(slot));
       }
     }
   } else {  // ---- P, one row per thread
@@ -390,23 +527,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       const bool in = row < row_hi;
       const int tok = row / a.share, gh = row - tok * a.share;
       const int hi = in ? q.pos0 + tok : -1, lo = a.window > 0 ? q.pos0 + tok - a.window + 1 : 0;
+      float c = fabsf(a.scale) * 1.44269504088896341f;
       {  // Q into its tile, channels in the codes' order, with the scale's sign
         const T* src = static_cast<const T*>(a.q[rank]) + (size_t)(q.begin + tok) * a.q_stride +
                        (size_t)(head * a.share + gh) * D;
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
         const uint32_t dst = sq + (uint32_t)(g * Shape::q_tile) + (uint32_t)r * 128u;
+        float f = 1.0f;
+        if constexpr (!FP16) {  // a bf16 row as fp16: its largest value goes to 2^8 .. 2^9, exactly
+          uint32_t top = 0;
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 v = in ? *reinterpret_cast<const uint4*>(src + 8 * u) : make_uint4(0, 0, 0, 0);
+            top = __vmaxu2(__vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu)),
+                           v.w & 0x7fff7fffu);
+          }
+          top = max(top & 0xffffu, top >> 16);
+          const int e = top ? max(-100, min(119, (int)(top >> 7) - 127 - 8)) : 0;
+          f = power2(-e);
+          c *= power2(e);
+        }
+        auto half = [&](uint32_t w) {  // two values
+          if constexpr (FP16) return w ^ flip;
+          const float2 x = param_floats(w);
+          return Half16<__half>::narrow2(x.x * f, x.y * f) ^ flip;
+        };
 #pragma unroll
         for (int u = 0; u < D / 8; ++u) {
           const uint4 v = in ? *reinterpret_cast<const uint4*>(src + 8 * u) : make_uint4(0, 0, 0, 0);
-          const uint4 o = make_uint4(__byte_perm(v.x, v.z, 0x5410) ^ flip, __byte_perm(v.x, v.z, 0x7632) ^ flip,
-                                     __byte_perm(v.y, v.w, 0x5410) ^ flip, __byte_perm(v.y, v.w, 0x7632) ^ flip);
+          const uint4 o = make_uint4(half(__byte_perm(v.x, v.z, 0x5410)), half(__byte_perm(v.x, v.z, 0x7632)),
+                                     half(__byte_perm(v.y, v.w, 0x5410)), half(__byte_perm(v.y, v.w, 0x7632)));
           sts128(dst + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (r & 7)) * 16), o);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(two(qFull, g));
       }
-      const float c = fabsf(a.scale) * 1.44269504088896341f;
       const uint32_t lanes = (uint32_t)(quad * 32) << 16;
       const uint32_t ts = tmem + lanes + (uint32_t)g * 128u, to = tmem + lanes + 256u + (uint32_t)g * 128u;
       // the keys that every row of this warp sees need no test
@@ -421,7 +577,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         tc_fence_after();
         const int key0 = (page0 + 2 * j) * kKv4Page;
         const uint32_t absent = s_absent[j & 7];
-        const bool masked = absent || key0 + 127 > all_hi || key0 < all_lo;
+        const uint32_t rg = range(j);
+        // (a page's V in bf16, so P too: tested in the masked form only)
+        const bool masked = absent || key0 + 127 > all_hi || key0 < all_lo || (rg & 0x202u);
+        if (rg & 0x101u) {  // keys with scales of their own
+#pragma unroll 1
+          for (int c0 = rg & 1u ? 0 : 64; c0 < (rg & 0x100u ? 128 : 64); c0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(ts + (uint32_t)c0, v);
+            tmem_ld_wait16(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * power2(s_exp[j & 3][c0 + i]));
+            tmem_st16(ts + (uint32_t)c0, v);
+          }
+          tmem_st_wait();
+        }
         auto seen = [&](int i) {
           const int key = key0 + i;
           return key <= hi && key >= lo && !((absent >> (i >> 6)) & 1u);
@@ -483,20 +653,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         auto make = [&](const uint32_t* v, int c0) {
           uint32_t w[16];
           if (masked) {  // tested once, not per element
+            const bool wide = (rg & (c0 < 64 ? 2u : 0x200u)) != 0;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float2 p = pair(v, i);
               if (!seen(c0 + i)) p.x = 0.0f;
               if (!seen(c0 + i + 1)) p.y = 0.0f;
               sum = add2(sum, p);
-              w[i / 2] = Half16<T>::narrow2(p.x, p.y);
+              w[i / 2] = wide ? Half16<T>::narrow2(p.x, p.y) : Half16<__half>::narrow2(p.x, p.y);
             }
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 p = pair(v, i);
               sum = add2(sum, p);
-              w[i / 2] = Half16<T>::narrow2(p.x, p.y);
+              w[i / 2] = Half16<__half>::narrow2(p.x, p.y);
             }
           }
           tmem_st16(ts + (uint32_t)(c0 / 2), w);  // over scores that have been read

@@ -178,9 +178,16 @@ def test_append_strided_rows(dcc):
 
 
 def check_attention(dcc, dtype, dim, group, n, heads, share, lens, news, window=0, scale=None, seed=0, q_scale=1.0,
-                    with_lse=True, max_new=None, layers=1, layer=0, extra_rows=0, stream=None, strided=False):
+                    with_lse=True, max_new=None, layers=1, layer=0, extra_rows=0, stream=None, strided=False, powers=None):
     g = torch.Generator().manual_seed(seed + 31 * dim + group + heads + share)
     cache, pools, table = make_cache(dcc, g, n, lens, heads, dim, group, dtype, layers)
+    if powers:  # K and V of single tokens multiplied by powers of two: powers = (of K, of V), drawn from
+        for pool in cache.pools:
+            par = pool.view(TD[dtype]).view(*pool.shape[:-1], -1)[..., PAGE * dim // 2:]
+            par = par.view(*pool.shape[:-1], 2, PAGE, -1)
+            for side, of in enumerate(powers):
+                e = torch.tensor(of)[torch.randint(len(of), (*par.shape[:-3], PAGE, 1), generator=g)]
+                par[..., side, :, :] *= torch.exp2(e.double()).to(TD[dtype]).cuda()
     T, Hq = sum(news) + extra_rows, heads * share
     wide = Hq + (2 * heads if strided else 0)
     q = [(q_scale * torch.randn(T, wide, dim, generator=g)).to(TD[dtype]).cuda()[:, :Hq] for _ in range(n)]
@@ -455,3 +462,39 @@ def test_bad_page_numbers_are_reported_and_skipped(dcc):
     cache.lengths.fill_(64 * cache.max_pages + 5)  # longer than its row
     cache.attention([q], [torch.empty_like(q)], batch([1]), max_new=1, workspace=ws)
     assert dcc.dcc_local_check() == dcc.DCC_ERR_BOUNDS
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (64, 64), (128, 32), (128, 64)])
+@pytest.mark.parametrize("powers,q_scale,scale", [
+    (([0, 0, -30, 5], [0]), 1.0, None), (([0, -3, 18], [0]), 1.0, 2.0 ** -21), (([0], [0, 0, -25, 9]), 1.0, None),
+    (([100, 90], [-60, 60]), 1e-30, 0.05), (([-90, -100], [-20]), 1e27, -0.5),
+    (([0] * 299 + [-30], [0] * 299 + [20]), 1.0, None)])  # some pages only
+def test_prompt_wide_ranges(dcc, dim, group, powers, q_scale, scale):
+    """bf16 tokens whose values leave the range of 16-bit floats, beside others that do not."""
+    check_attention(dcc, "bf16", dim, group, 8, 2, 8, [500, 300], [60, 100], scale=scale, q_scale=q_scale, powers=powers)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_prompt_calls_back_to_back(dcc, dtype):
+    """Calls on caches in turn, nothing waited for between them: pages come from memory in any order."""
+    g = torch.Generator().manual_seed(5)
+    sets = []
+    for _ in range(3):
+        cache, _, _ = make_cache(dcc, g, 8, [4096], 1, 128, 64, dtype)
+        q = [torch.randn(512, 8, 128, generator=g).to(TD[dtype]).cuda() for _ in range(8)]
+        sets.append((cache, q, [torch.empty_like(x) for x in q], cache.attention_workspace(8)))
+    start = batch([512])
+
+    def run(s):
+        s[0].attention(s[1], s[2], start, max_new=512, workspace=s[3])
+
+    want = []
+    for s in sets:
+        run(s)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in s[2]])
+    for i in range(240):
+        run(sets[i % 3])
+    assert dcc.dcc_local_check() == dcc.DCC_OK
+    for s, w in zip(sets, want):
+        assert all(torch.equal(a, b) for a, b in zip(s[2], w))
