@@ -464,7 +464,7 @@ class Ranks:
     """One tensor per rank, all of one shape, type and row stride, with their
     device pointers marshalled once (a serving loop passes the same buffers
     every step).  Rows may be strided (a slice of a fused projection); the rest
-    of each row is dense."""
+    of each row is dense, and a vector is one row."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -475,8 +475,8 @@ class Ranks:
             if not o.is_cuda:
                 raise ValueError("the ranks' tensors are on a CUDA device")
         self.shape, self.dtype = tuple(t.shape), t.dtype
-        dense = 1
-        for size, step in list(zip(t.shape, t.stride()))[:0:-1]:
+        dense, inner = 1, 0 if t.dim() < 2 else 1  # the dimensions of a row: all of a vector's
+        for size, step in list(zip(t.shape, t.stride()))[inner:][::-1]:
             if size > 1 and step != dense:
                 raise ValueError("a row of the tensors is not dense")
             dense *= size
