@@ -26,14 +26,14 @@
 // in ordinary caches, so their forms are short rather than fast.
 //
 // Measured on GB300, 2048 new tokens on 8192 keys, 8 ranks x 8 query heads x 128
-// channels: fp16 523 us, 0.93 PFLOP/s; bf16 551 us, 0.88 PFLOP/s, 46 % of a
+// channels: fp16 530 us, 0.92 PFLOP/s; bf16 551 us, 0.88 PFLOP/s, 46 % of a
 // library product's rate (the MMAs alone: 326 us; bf16 tiles: 521 us).  What
 // bounds it is shared memory (the S products read 128 bytes a clock, all there
 // is, and the unpacking warps' accesses and every barrier queue behind them) and
 // the instructions of P and the unpacking.  Tried without gain: separate warps
 // for K and V, a row of scores held in registers, P handed over in halves, an
 // MMA warp that polls both tiles, rings of K's and V's codes apart (a deeper
-// prefetch: 542 us for 523).
+// prefetch: 542 us where this took 523).
 //
 // Roles (512 threads): warp 0 loads pages (one bulk copy each, three in
 // flight); warp 1 issues the MMAs; warps 2..5 unpack; warps 6..9 and 10..13
@@ -53,7 +53,10 @@
 // A key that no row may see (past the sequence, a missing page) has V = 0, and
 // its scores are replaced, not multiplied.  A V row that holds NaN or infinity
 // becomes 0 there and makes its K NaN instead, so that rows that see the key
-// get NaN and the others nothing.
+// get NaN and the others nothing.  A value past the type's largest (by an ulp,
+// where the step was rounded up) counts as the largest: as an infinity it would
+// reach the rows that do not see the key, whose P is 0.  (Looking for such
+// groups in the fp16 cache costs 523 -> 530 us.)
 #pragma once
 #include "fused_mma.cuh"
 #include "kv4_decode.cuh"
@@ -113,6 +116,10 @@ __device__ __forceinline__ uint32_t param_bad(uint32_t w) {
   return (w & 0x7fff7fffu) + (one | one << 16);
 }
 constexpr uint32_t kBad = 0x80008000u;
+// The same for fp16 pairs whose lo + 15 step may be more than fp16 holds: a step
+// of 2^11 or a lo of 2^15 on (below both it is at most 63,488 of 65,504).  NaN and
+// infinities are among them.
+__device__ __forceinline__ uint32_t param_large(uint32_t w) { return (w & 0x7fff7fffu) + 0x08001800u; }
 
 // The bf16 cache's parameters as fp16 operands.  A group's largest magnitude m
 // decides: fp16 holds the group to 2^-13 of m for m from 2^-8 up.
@@ -127,6 +134,14 @@ __device__ __forceinline__ bool fp16_fits(float m, float top) { return m == 0.0f
 __device__ __forceinline__ uint32_t param_half(uint32_t w) {
   const float2 p = param_floats(w);
   return Half16<__half>::narrow2(p.x, p.y);
+}
+// Two values, none of them NaN, rounded to T and kept finite: a step rounded up may
+// put a group's last code past the type's largest number, by an ulp of it (0 ..
+// 65,504 in fp16: 15 steps of 4368 are 65,520).
+template <typename T>
+__device__ __forceinline__ uint32_t narrow_finite(float a, float b) {
+  const uint32_t w = Half16<T>::narrow2(a, b), most = std::is_same<T, __half>::value ? 0x7bff7bffu : 0x7f7f7f7fu;
+  return (w & 0x80008000u) | __vminu2(w & 0x7fff7fffu, most);
 }
 __device__ __forceinline__ float power2(int e) { return __int_as_float((127 + e) << 23); }  // e from -126 to 127
 constexpr float kTopK = 0x1p15f;  // larger groups of K do not fit fp16
@@ -321,20 +336,38 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
           const int key = (2 * ((tid >> 3) + 16 * pass)) ^ ((tid & 4) ? 5 : 0);
-          uint32_t step[NG], lo[NG];
-          uint32_t bad = 0;
-          if constexpr (FP16)
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) bad |= param_bad<T>(par[(kKv4Page + key) * NG + gr]);
+          const uint32_t row = kt + (uint32_t)(64 * h + key) * 128u;
+          const unsigned char* src = blk + key * (D / 2) + t * (JW * 4);
+          uint32_t step[NG], lo[NG], w[JW];
+          uint32_t odd = 0;  // fp16: large or not finite, K or V (the bf16 cache's parameters have been seen to)
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
-            const uint32_t w = (bad & kBad) ? 0xffffffffu : par[key * NG + gr];  // NaN
-            step[gr] = __byte_perm(w, w, 0x1010);
-            lo[gr] = __byte_perm(w, w, 0x3232);
+            const uint32_t pw = par[key * NG + gr];
+            if (FP16) odd |= param_large(par[(kKv4Page + key) * NG + gr]) | param_large(pw);
+            step[gr] = __byte_perm(pw, pw, 0x1010);
+            lo[gr] = __byte_perm(pw, pw, 0x3232);
           }
-          const uint32_t row = kt + (uint32_t)(64 * h + key) * 128u;
-          uint32_t w[JW];
-          const unsigned char* src = blk + key * (D / 2) + t * (JW * 4);
+          if (FP16 && (odd & kBad)) {  // rare, so little code: a pair at a time, in fp32
+            uint32_t bad = 0;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) bad |= param_bad<T>(par[(kKv4Page + key) * NG + gr]);
+#pragma unroll 1
+            for (int i = 0; i < 4 * JW; ++i) {
+              const int u = 4 * (i >> 2) + t;
+              const uint32_t c = reinterpret_cast<const uint32_t*>(src)[i >> 2] >> (4 * (i & 3));
+              const uint32_t pw = par[key * NG + 8 * u / G];
+              const float2 f = Half16<T>::widen2(pw);
+              const uint32_t pair = (bad | param_bad<T>(pw)) & kBad
+                                        ? 0xffffffffu  // NaN
+                                        : narrow_finite<T>(fmaf((float)(c & 15u), f.x, f.y),
+                                                           fmaf((float)((c >> 16) & 15u), f.x, f.y));
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (uint32_t)(u / 8) * 16384u +
+                                                           (uint32_t)(((u % 8) ^ (key & 7)) * 16 + 4 * (i & 3))),
+                           "r"(pair)
+                           : "memory");
+            }
+            continue;
+          }
           if constexpr (JW == 4) {
             const uint4 v = *reinterpret_cast<const uint4*>(src);
             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
@@ -372,11 +405,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         const int swap = D == 128 ? oct & 1 : 0;
         const uint32_t sel0 = swap ? 0x1054u : 0x5410u, sel1 = swap ? 0x3276u : 0x7632u;
         const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D)) + kKv4Page * NG;
-        const bool there = !((absent >> h) & 1u), wide = !FP16 && wide_v(j, h);
+        const bool there = !((absent >> h) & 1u);
+        bool wide = !FP16 && wide_v(j, h);
         // the word's channels lie in one group (G = 64) or two (32)
         const int g0 = 64 * ws / G;
         constexpr int GW = G == 32 ? 2 : 1;
-        if (wide) {  // rare, so little code rather than fast: two keys of a channel at a time
+        auto by_pairs = [&]() {  // rare, so little code rather than fast: two keys of a channel at a time, in fp32
 #pragma unroll 1
           for (int i = 0; i < 32; ++i) {
             const int n = i >> 2, gr = g0 + (GW > 1 ? n >> 2 : 0), d = 64 * ws + 16 * (n >> 1) + c + 8 * (n & 1);
@@ -387,16 +421,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
               const uint32_t word = *reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + key * (D / 2) +
                                                                        kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
               const uint32_t pw = par[key * NG + gr];
-              const float2 f = param_floats(pw);
+              const float2 f = Half16<T>::widen2(pw);
               const bool none = (param_bad<T>(pw) & kBad) || !there || (page0 + p) * kKv4Page + key >= len;
               v[x] = none ? 0.0f : fmaf((float)((word >> (4 * n)) & 15u), f.x, f.y);
             }
-            const uint32_t pair = Half16<T>::narrow2(v[0], v[1]);
+            const uint32_t pair = narrow_finite<T>(v[0], v[1]);
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(vt + (uint32_t)h * (D * 128u) + (uint32_t)d * 128u +
                                                          (uint32_t)((oct ^ (d & 7)) * 16 + 4 * (i & 3))),
                          "r"(pair)
                          : "memory");
           }
+        };
+        if (!FP16 && wide) {
+          by_pairs();
           continue;
         }
         uint32_t w[8], pr[8][GW], bad = 0;
@@ -408,10 +445,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
 #pragma unroll
           for (int x = 0; x < GW; ++x) {
             pr[k][x] = par[key * NG + g0 + x];
-            bad |= param_bad<__half>(pr[k][x]);
+            bad |= FP16 ? param_large(pr[k][x]) : param_bad<__half>(pr[k][x]);
           }
         }
-        if ((bad & kBad) || !there || (page0 + p) * kKv4Page + 8 * oct + 7 >= len)  // some key must be zero
+        if ((bad & kBad) || !there || (page0 + p) * kKv4Page + 8 * oct + 7 >= len) {  // some key must be zero
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int key = 8 * oct + (k ^ swap);
@@ -421,7 +458,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
             if ((any & kBad) || !there || (page0 + p) * kKv4Page + key >= len)
 #pragma unroll
               for (int x = 0; x < GW; ++x) pr[k][x] = 0u;
+#pragma unroll
+            for (int x = 0; x < GW; ++x) wide |= FP16 && (param_large(pr[k][x]) & kBad);  // or is large
           }
+          if (FP16 && wide) {
+            by_pairs();
+            continue;
+          }
+        }
         uint32_t out[8][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // pairs of keys

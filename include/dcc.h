@@ -560,7 +560,9 @@ int dcc_kernel_binary_version(int* version);
  * minimum, step = R((max - lo) / 15), code = (x - lo) / step rounded to the
  * nearest even in 0..15, value = lo + step * code, with step and lo in the
  * cache's type; a group that holds a NaN or an infinity, or whose range
- * overflows fp32, reads back as NaN.  fp16 / bf16, head_dim 64 or 128,
+ * overflows fp32, reads back as NaN.  (step is rounded, so a group's largest
+ * value may come back an ulp past what the type holds, as infinity; attention
+ * takes lo + step * code as it is or as the type's largest number.)  fp16 / bf16, head_dim 64 or 128,
  * group 32 or 64 (UNSUPPORTED otherwise).  Pools are 16-byte aligned. */
 typedef struct {
   void* const* pool; /* HOST array of n_ranks device pointers */
