@@ -520,10 +520,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMmaPairThreads ? 2 : 1)
       for (int h = 1; h < MACC; ++h)
         tma_prefetch_2d(h == MACC - 1 ? &maps.w2[g / kpb] : &maps.w[g / kpb], (g % kpb) * kMmaBK, m0 + h * kMmaBM);
     }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_wait();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  pdl_trigger();  // not before the allocation
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_slot;
 

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  pdl_prologue();
+  pdl_wait();
 
   // ---- this CTA's rows; the last tiles (the most keys) come first
   const int nh = kv.n * kv.heads, per = nh * kv.seqs;
@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   }
   tc_fence_before();
   __syncthreads();
+  pdl_trigger();  // not before the allocation
   tc_fence_after();
   const uint32_t tmem = tmem_slot;  // S / P of the two row tiles, then O: 128 columns each
   auto range = [&](int j) { return FP16 ? 0u : (uint32_t)*reinterpret_cast<const volatile uint16_t*>(s_range[j & 7]); };

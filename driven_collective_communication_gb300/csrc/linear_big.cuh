@@ -108,9 +108,10 @@ __global__ void __launch_bounds__(kBigThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  pdl_prologue();
+  pdl_wait();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  pdl_trigger();  // not before the allocation
   mma_cluster_sync();  // both CTAs' barriers stand
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_slot;

@@ -169,9 +169,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMmaPairThreads ? 2 : 1)
   // overlaps the end of the previous kernel on the stream, as do these prefetches into L2
   if (warp == 3 && lane == 0)
     for (int i = 0; i < nk && i < S; ++i) tma_prefetch_2d(&maps.w[rank], (b0 + i) * kMmaBK, m0);
-  pdl_prologue();
+  pdl_wait();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  pdl_trigger();  // not before the allocation
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_slot;
 

@@ -65,10 +65,18 @@ __device__ __forceinline__ unsigned long long global_timer_ns() {
 // any access to global memory.  launch_dependents lets the next such kernel
 // begin launching (it waits in turn).  Both are no-ops in a launch without
 // the attribute.  Only kernels whose CTAs never wait on one another take it.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_prologue() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_wait();
+  pdl_trigger();
 }
+// A kernel that allocates tensor memory takes the two apart: a CTA's allocation
+// waits for other CTAs' columns without a limit, and the next kernel's CTAs may
+// allocate theirs before they wait for this kernel.  So no CTA triggers before
+// its own columns are allocated (pdl_trigger after the __syncthreads that
+// follows the allocation); by the time the next kernel starts, all of this
+// one's have theirs, and need nothing to finish.
 
 // 16-byte vector accesses.  Peer data that another CTA wrote in this kernel is
 // read at L2 (ld.global.cg) so that no stale L1 line can be returned.
