@@ -83,7 +83,9 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
   a.layer = layer;
   a.q_heads = q_heads;
   a.max_new = max_new;
-  a.window = window;
+  // positions stay below 2^30 (kv4_view), so a window that long hides nothing;
+  // kept, position - window + 1 would leave 32 bits for rows before position zero
+  a.window = window < (1 << 30) ? window : 0;
   a.scale = scale;
   a.share = q_heads / kv->kv_heads;
   a.ws = static_cast<char*>(workspace);

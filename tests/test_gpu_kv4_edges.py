@@ -116,3 +116,18 @@ def test_nan_and_infinities_beside_large_groups(dcc, form):
         sees = torch.arange(m - new, m) >= m - 30
         assert torch.equal(out[:new].isnan().any(-1).any(-1).cpu(), sees) and torch.isfinite(out[new:]).all()
         assert torch.isfinite(out[:new][~sees]).all()
+
+
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1, (1 << 30) - 1])
+@pytest.mark.parametrize("n,lens,news", [(1, [3, 70], [8, 1]), (1, [3, 70], [1, 1]), (8, [3, 70], [60, 60])])
+def test_windows_longer_than_any_sequence(dcc, window, n, lens, news):
+    """Nothing is hidden, also from a batch with rows before position zero."""
+    g = torch.Generator().manual_seed(24)
+    cache, _, _ = make_cache(dcc, g, n, lens, 1, 128, 64, "bf16")
+    q = torch.randn(sum(news), 8, 128, generator=g).bfloat16().cuda()
+    outs = []
+    for w in (0, window):
+        outs.append([torch.full_like(q, 7.0) for _ in range(n)])
+        cache.attention([q] * n, outs[-1], batch(news), max_new=max(news), workspace=cache.attention_workspace(8), window=w)
+    assert dcc.dcc_local_check() == dcc.DCC_OK
+    assert outs[0][0].any() and all(torch.equal(a, b) for a, b in zip(*outs))
