@@ -13,7 +13,8 @@
 // the one operand that is rounded (11 bits; 22 in pages where a mask begins or
 // ends); its scale follows the running maximum of s_j and of the steps (R
 // below: l, O and all sums are in units of 2^R), so it neither overflows nor
-// falls into the subnormals unless it is 2^-28 of the largest seen.  Codes
+// falls into the subnormals unless it is 2^-28 of the largest that a row of the
+// tile has seen.  Codes
 // enter O as n - 8, about the middle of their range, so that what is rounded
 // is no larger than V itself.
 //
@@ -245,7 +246,8 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
   constexpr float kCenter = 8.0f;
   constexpr uint32_t kBias = 0xd480d480u;  // fp16 -72 = -(64 + kCenter), twice
   constexpr int kMinExp = -60;  // steps below 2^-60 count as that: 2^(14 + 60) a key still sums in fp32
-  constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr uint32_t kLoFloor = 80u << 7;
   extern __shared__ __align__(128) char dec_smem[];
   __shared__ __align__(8) uint64_t bars[W][S];
   __shared__ long long s_sum[W];
@@ -562,16 +564,20 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
     }
     // the largest step of V (its exponent) and the running maximum; what was
     // summed so far is rescaled where they grew
-    uint32_t top = 0;
+    uint32_t top = 0;  // by halves: step, lo
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         const int key = 2 * lane + h;
-        uint32_t s = (vpar - kg * NG)[key * NG + gr] & 0x7fffu;
-        if (s >= kInf || (MASKED && key0 + key > tile_end)) s = 0;
-        top = max(top, s);
+        uint32_t w = (vpar - kg * NG)[key * NG + gr] & (kBf16 ? 0x7fff7fffu : 0x7fffu);
+        const bool finite = kBf16 ? ((w + 0x00800080u) & 0x80008000u) == 0u : w < 0x7c00u;
+        if (!finite || (MASKED && key0 + key > tile_end)) w = 0;
+        top = kBf16 ? __vmaxu2(top, w) : max(top, w);
       }
+    // a bf16 lo far above all steps (constant groups) counts as 2^-80 of itself:
+    // p lo stays below 2^95, and 2^30 of them still sum in fp32
+    if (kBf16) top = max(top & 0xffffu, max(top >> 16, kLoFloor) - kLoFloor);
     top = __reduce_max_sync(0xffffffffu, top);
     const int ex_new = max(ex, (__float_as_int(Half16<T>::widen((uint16_t)top)) >> 23) - 127);
     bool grew = ex_new > ex;

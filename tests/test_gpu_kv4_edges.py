@@ -131,3 +131,23 @@ def test_windows_longer_than_any_sequence(dcc, window, n, lens, news):
         cache.attention([q] * n, outs[-1], batch(news), max_new=max(news), workspace=cache.attention_workspace(8), window=w)
     assert dcc.dcc_local_check() == dcc.DCC_OK
     assert outs[0][0].any() and all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,value", [("bf16", 1e20), ("bf16", -1e16), ("bf16", 3e30), ("bf16", 1e-30), ("fp16", 60000.0)])
+@pytest.mark.parametrize("dim,group", [(128, 64), (64, 32)])
+def test_constant_groups_of_v(dcc, form, dtype, value, dim, group):
+    """Groups whose step is zero, the same in every key: V itself comes out; beside them ordinary ones."""
+    n, new, kernel = FORMS[form]
+    g = torch.Generator().manual_seed(25)
+    m = 200
+    for constant in (dim, dim - group):  # all groups, or all but one
+        cache, _, table = make_cache(dcc, g, n, [m, m], 1, dim, group, dtype)
+        k = torch.randn(2 * m, 1, dim, generator=g).to(TD[dtype])
+        v = torch.randn(2 * m, 1, dim, generator=g).to(TD[dtype])
+        v[..., :constant] = value
+        cache.append([k.cuda()] * n, [v.cuda()] * n, batch([m, m]))
+        q = torch.randn(2 * new, 8, dim, generator=g).to(TD[dtype])
+        out = run(dcc, cache, table, q, [m, m], [new, new], n, 8, group, dtype, kernel)
+        exact = torch.tensor(value).to(TD[dtype]).double().item()
+        assert ((out[0][..., :constant].double() / exact - 1).abs() <= 2 * R.U[dtype]).all()
