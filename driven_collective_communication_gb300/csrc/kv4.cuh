@@ -119,10 +119,15 @@ __device__ __forceinline__ int kv4_seq_of(const int32_t* start, int seqs, int ro
 
 }  // namespace dcc
 
+namespace dcc {
+struct LocalDev;
+}
 namespace dcc_host {
-// Status words (two) of the calls that use no communicator, on the current device
+// Status words of the calls that use no communicator, on the current device
 // (ops_status.cu); null after a CUDA error.
 unsigned long long* local_status();
+// What the kernels of one such call wait with, given the status words.
+dcc::LocalDev local_dev(unsigned long long* status);
 // Checks a cache descriptor and makes its device view, without any CUDA call;
 // kv4_ready adds what a launch needs (ops_status.cu).
 int kv4_view(const dcc_kv4_t* kv, bool need_refs, dcc::Kv4Dev* out);

@@ -116,11 +116,7 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
     a.wide = (int)wide;
     const long long grid = (wide + narrow) * segments;
     if (grid > 0x7fffffffll) return DCC_ERR_INVALID_ARG;
-    dcc::DevComm dc{};
-    dc.n = kv->n_ranks;
-    dc.skip_signal_rank = -1;
-    dc.timeout_ns = a.timeout_ns;
-    dc.status = d.status + 1;
+    dcc::LocalDev dc = dcc_host::local_dev(d.status);
     void* args[] = {&d, &a, &dc};
     return dcc_host::launch(k.fn, (int)grid, k.threads, false, args, st, k.smem, true);
   }

@@ -148,7 +148,7 @@ constexpr float kTopK = 0x1p15f;  // larger groups of K do not fit fp16
 constexpr float kTopV = 0x1p11f;  // the smallest P that fp16 holds, times this, is 2^-12 of a V of 2^-8
 
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, const __grid_constant__ AttnArgs a, DevComm dc) {
+__global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, const __grid_constant__ AttnArgs a, LocalDev dc) {
   using Shape = PromptShape<D, G>;
   constexpr bool FP16 = std::is_same<T, __half>::value;
   constexpr int NG = D / G, BLK = Shape::block, R = kPromptRing, JW = D / 32;
@@ -168,10 +168,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   auto rawe = [&](int s) { return bars + 8u * (uint32_t)(R + s); };
   auto ready = [&](int s) { return bars + 8u * (uint32_t)(2 * R + 16 + s); };
   auto two = [&](int kind, int i) { return bars + 8u * (uint32_t)(2 * R + 2 * kind + i); };
+  const uint32_t last = bars + 8u * (uint32_t)(3 * R + 16);  // the products in flight when a wait gave up
   enum { kFull = 0, kFree, vFull, vFree, sFull, pFull, pvDone, qFull };  // the last: one for both
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    mma_mbar_init(last, 1);
     for (int i = 0; i < R; ++i) {
       mma_mbar_init(rawf(i), 1);
       mma_mbar_init(rawe(i), 4);
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   auto range = [&](int j) { return FP16 ? 0u : (uint32_t)*reinterpret_cast<const volatile uint16_t*>(s_range[j & 7]); };
   auto wide_v = [&](int j, int h) { return (range(j) & (2u << 8 * h)) != 0; };
   const int len = min(kv.len[seq], pos_hi + 1);  // keys that some row may see
-  auto wait = [&](uint32_t bar, int phase) { return mma_mbar_wait(bar, (uint32_t)phase & 1u, dc, rank, head); };
+  auto wait = [&](uint32_t bar, int phase) { return local_wait(bar, (uint32_t)phase & 1u, dc, rank, head); };
 
   if (warp == 0) {  // ---- loads
     int ids = -1, ids_at = -(1 << 30), unfinished = 0;
@@ -254,9 +256,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       }
       ++unfinished;
     }
-    // (a copy in flight when a wait gave up ends before the CTA does: its
-    // barrier is waited for below, with the same limit)
-    for (int p = max(0, unfinished - R); p < unfinished; ++p) wait(rawf(p % R), p / R);
+    // a copy in flight when a wait gave up ends before the CTA does
+    for (int p = max(0, unfinished - R); p < unfinished; ++p) local_drain(rawf(p % R), (uint32_t)(p / R) & 1u);
   } else if (warp == 1) {  // ---- MMAs
     if (lane == 0) {
       const uint32_t id = (1u << 4) | ((uint32_t)(128 >> 4) << 24);  // fp16 operands; bf16: bits 7 and 10
@@ -305,6 +306,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           tc_commit(two(pvDone, g));
           if (j + 1 < steps) scores(g, j + 1);
         }
+      if (!ok) {
+        tc_commit(last);
+        local_drain(last, 0);
+      }
     }
     __syncwarp();
   } else if (warp < 6) {  // ---- unpack

@@ -151,7 +151,7 @@ Plan plan(const Room& r, bool pair, int n, int ntile, int rows, int k) {
   return p;
 }
 
-int run_mma(const dcc::LinArgs& l, bool fp16, dcc::DevComm& dc, cudaStream_t s) {
+int run_mma(const dcc::LinArgs& l, bool fp16, dcc::LocalDev& dc, cudaStream_t s) {
   Room r;
   int rc = room(&r);
   if (rc != DCC_OK) return rc;
@@ -188,7 +188,7 @@ int run_mma(const dcc::LinArgs& l, bool fp16, dcc::DevComm& dc, cudaStream_t s) 
   return launch(p.fn, (int)grid, p.threads, false, args, s, p.smem, true, p.ks > 1 ? p.ks : 0);
 }
 
-int run_big(const dcc::LinArgs& l, bool fp16, dcc::DevComm& dc, cudaStream_t s) {
+int run_big(const dcc::LinArgs& l, bool fp16, dcc::LocalDev& dc, cudaStream_t s) {
   Room r;
   int rc = room(&r);
   if (rc != DCC_OK) return rc;
@@ -256,13 +256,9 @@ extern "C" int dcc_linear(int n_ranks, void* const* weight, void* const* x, void
   a.rows = (int)rows;
   a.k = (int)k;
   a.act = (int)act;
-  dcc::DevComm dc{};
-  dc.n = n_ranks;
-  dc.skip_signal_rank = -1;
-  dc.timeout_ns = 2000000000ull;
-  dc.status = dcc_host::local_status();
-  if (!dc.status) return DCC_ERR_CUDA;
-  ++dc.status;  // the word of waits that gave up
+  unsigned long long* status = dcc_host::local_status();
+  if (!status) return DCC_ERR_CUDA;
+  dcc::LocalDev dc = dcc_host::local_dev(status);
   cudaStream_t st = static_cast<cudaStream_t>(s);
   return tokens <= (size_t)dcc::kMmaMaxTokens ? run_mma(a, t == DCC_FP16, dc, st) : run_big(a, t == DCC_FP16, dc, st);
 }

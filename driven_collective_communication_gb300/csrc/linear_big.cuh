@@ -21,6 +21,8 @@
 //   warps 2..5               epilogue: lane = row, so the 32 lanes of a warp
 //                             read residuals and write results of 32
 //                             neighbouring rows of a token.
+// Waits run to their limit whatever another wait did (one wave, so that bounds
+// the kernel): what the other CTA of a pair had in flight is then long done.
 #pragma once
 #include "linear_mma.cuh"
 
@@ -82,7 +84,7 @@ __device__ __forceinline__ void big_store16(const uint32_t* v, float bias, const
 }
 
 __global__ void __launch_bounds__(kBigThreads, 1)
-    k_linear_big(const __grid_constant__ LinMaps maps, DevComm dc, const __grid_constant__ LinBigArgs a) {
+    k_linear_big(const __grid_constant__ LinMaps maps, LocalDev dc, const __grid_constant__ LinBigArgs a) {
   extern __shared__ unsigned char big_raw[];
   __shared__ uint32_t tmem_slot;
   constexpr int S = kBigStages;
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kBigThreads, 1)
       place(w, &rank, &row, &tok);
       for (int kb = 0; kb < kpb; ++kb, ++it) {
         const int s = it % S;
-        if (it >= S && !mma_mbar_wait(empty(s), (uint32_t)((it / S - 1) & 1), dc, rank, (int)cta)) {
+        if (it >= S && !local_wait<false>(empty(s), (uint32_t)((it / S - 1) & 1), dc, rank, (int)cta)) {
           ok = false;
           break;
         }
@@ -150,11 +152,11 @@ __global__ void __launch_bounds__(kBigThreads, 1)
     bool ok = true;
     for (int w = first; w < tiles && ok; w += stride, ++i) {
       const int b = i & 1;
-      if (i >= 2 && !mma_mbar_wait(acce(b), (uint32_t)((i / 2 - 1) & 1), dc, 0, 0)) break;
+      if (i >= 2 && !local_wait<false>(acce(b), (uint32_t)((i / 2 - 1) & 1), dc, 0, 0)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       for (int kb = 0; kb < kpb; ++kb, ++it) {
         const int s = it % S;
-        if (!mma_mbar_wait(full(s), (uint32_t)((it / S) & 1), dc, 0, 0)) {
+        if (!local_wait<false>(full(s), (uint32_t)((it / S) & 1), dc, 0, 0)) {
           ok = false;
           break;
         }
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(kBigThreads, 1)
         const uint16_t v = static_cast<const uint16_t*>(a.l.bias[rank])[row];
         bias = fp16 ? Half16<__half>::widen(v) : Half16<__nv_bfloat16>::widen(v);
       }
-      if (!mma_mbar_wait(accf(b), (uint32_t)((i / 2) & 1), dc, rank, (int)cta)) break;
+      if (!local_wait<false>(accf(b), (uint32_t)((i / 2) & 1), dc, rank, (int)cta)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       for (int c0 = 0; c0 < N; c0 += 16) {
         uint32_t v[16];

@@ -59,7 +59,7 @@ __device__ __forceinline__ uint4 lin_finish8(float* v, const uint4* bias, const 
 // inbox (see mma_epilogue in fused_mma.cuh, whose buffers and barriers these
 // are).  part and inbox reuse the stage buffers.
 template <int KSC, int THREADS>
-__device__ __forceinline__ void lin_epilogue(const DevComm& dc, const LinMmaArgs& a, uint32_t tmem, float* part,
+__device__ __forceinline__ void lin_epilogue(const LocalDev& dc, const LinMmaArgs& a, uint32_t tmem, float* part,
                                              uint32_t inbar, unsigned split, int rank, int m0, bool acc_ok) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, row = quad * 32 + lane;
   const int R = a.rounds, W = a.ntile / R, T = W / KSC;
@@ -104,7 +104,10 @@ __device__ __forceinline__ void lin_epilogue(const DevComm& dc, const LinMmaArgs
         }
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
-      ok = mma_mbar_wait(inbar, (uint32_t)(r & 1), dc, rank, (int)split) && ok;
+      if (!local_wait(inbar, (uint32_t)(r & 1), dc, rank, (int)split)) {
+        local_drain(inbar, (uint32_t)(r & 1));
+        ok = false;
+      }
     } else {
       __syncthreads();
     }
@@ -136,7 +139,7 @@ __device__ __forceinline__ void lin_epilogue(const DevComm& dc, const LinMmaArgs
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == kMmaPairThreads ? 2 : 1)
-    k_linear_mma(const __grid_constant__ LinMaps maps, DevComm dc, const __grid_constant__ LinMmaArgs a) {
+    k_linear_mma(const __grid_constant__ LinMaps maps, LocalDev dc, const __grid_constant__ LinMmaArgs a) {
   extern __shared__ unsigned char lin_raw[];
   __shared__ uint32_t tmem_slot;
   const uint32_t raw_u32 = smem_addr_u32(lin_raw);
@@ -179,19 +182,22 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMmaPairThreads ? 2 : 1)
   if (warp == 0 && lane == 0) {  // TMA producer
     const uint32_t tx = st_bytes - (uint32_t)(kMmaBM - a.bm) * (kMmaBK * 2);  // the weight box has bm rows
     const uint64_t pol_w = l2_evict_first(), pol_x = l2_evict_last();
-    for (int i = 0; i < nk; ++i) {
+    int i = 0;
+    for (; i < nk; ++i) {
       const int s = i % S;
-      if (i >= S && !mma_mbar_wait(empty(s), (uint32_t)(((i / S) - 1) & 1), dc, rank, (int)split)) break;
+      if (i >= S && !local_wait(empty(s), (uint32_t)(((i / S) - 1) & 1), dc, rank, (int)split)) break;
       const uint32_t sa = base + (uint32_t)s * st_bytes;
       mma_mbar_expect(full(s), tx);
       tma_load_2d_hint(sa, &maps.w[rank], (b0 + i) * kMmaBK, m0, full(s), pol_w);
       tma_load_2d_hint(sa + a_bytes, &maps.x[rank], (b0 + i) * kMmaBK, 0, full(s), pol_x);
     }
+    // none is in flight when the stages are used again, whoever gave up
+    for (int j = i > S ? i - S : 0; j < i; ++j) local_drain(full(j % S), (uint32_t)((j / S) & 1));
   } else if (warp == 1 && lane == 0) {  // MMA issuer
     const uint32_t idesc = mma_instr_desc(NTILE, a.fp16 != 0);
     for (int i = 0; i < nk; ++i) {
       const int s = i % S;
-      if (!mma_mbar_wait(full(s), (uint32_t)((i / S) & 1), dc, rank, (int)split)) break;
+      if (!local_wait(full(s), (uint32_t)((i / S) & 1), dc, rank, (int)split)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t sa = base + (uint32_t)s * st_bytes, sb = sa + a_bytes;
 #pragma unroll
@@ -210,7 +216,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMmaPairThreads ? 2 : 1)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(accf) : "memory");
   }
   __syncwarp();
-  const bool acc_ok = nk > 0 && mma_mbar_wait(accf, 0, dc, rank, (int)split);
+  const bool acc_ok = nk > 0 && local_wait(accf, 0, dc, rank, (int)split);
+  if (!acc_ok) local_drain(accf, 0);
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   float* part = reinterpret_cast<float*>(gbase);  // reuses the stage buffers (all loads consumed)
   if (mma_round_fits(NTILE, S, 1, KS, a.rounds)) {  // the host's plan always does

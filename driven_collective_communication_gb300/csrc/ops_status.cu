@@ -3,15 +3,17 @@
 // descriptor.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "kv4.cuh"
+#include "tcgen05.cuh"
 
 namespace {
-// Two words per device: numbers out of range, and waits that gave up (a wait
-// of the linear layer gives up at once when the second is set).  The address
-// comes from cudaGetSymbolAddress.
-static __device__ unsigned long long g_local_status[2];
+// Words per device: the first number out of range, the first wait that gave up,
+// the tag of the last call in which one did (LocalDev).  The address comes from
+// cudaGetSymbolAddress.
+static __device__ unsigned long long g_local_status[3];
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 unsigned long long* g_addr[kMaxDevices];
@@ -35,6 +37,11 @@ unsigned long long* local_status() {
     g_addr[dev] = static_cast<unsigned long long*>(p);
   }
   return g_addr[dev];
+}
+
+dcc::LocalDev local_dev(unsigned long long* status) {
+  static std::atomic<unsigned long long> calls{0};
+  return {2000000000ull, ++calls, status + 1};
 }
 
 int kv4_view(const dcc_kv4_t* kv, bool need_refs, dcc::Kv4Dev* out) {
@@ -94,7 +101,7 @@ int dcc_kv4_block_bytes(int head_dim, int group, size_t* bytes) {
 int dcc_local_check(dcc_stream_t s) {
   unsigned long long* p = dcc_host::local_status();
   if (!p) return DCC_ERR_CUDA;
-  unsigned long long st[2] = {0, 0};
+  unsigned long long st[3] = {0, 0, 0};
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(s)) != cudaSuccess ||
       cudaMemcpy(st, p, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) {
     cudaGetLastError();

@@ -1,9 +1,47 @@
-// tcgen05.cuh -- tensor-memory accesses, fences and commits in PTX, shared by
-// the kernels of the linear layer and of the attention.
+// tcgen05.cuh -- tensor-memory accesses, fences and commits in PTX, and bounded
+// waits, shared by the kernels of the linear layer and of the attention.
 #pragma once
 #include <cstdint>
 
+#include "fused_mma.cuh"
+
 namespace dcc {
+
+// What a call without a communicator gives its kernels to wait with: the
+// record of the first wait that gave up (any call's, until it is read), and
+// beside it the tag of the last call that did, which ends this call's other
+// waits early where it is their own.
+struct LocalDev {
+  unsigned long long timeout_ns, tag;
+  unsigned long long* status;  // [0] the record, [1] the tag
+};
+// Bounded wait on a phase.  EARLY: gives up as well when another wait of the
+// same call has.
+template <bool EARLY = true>
+__device__ __forceinline__ bool local_wait(uint32_t bar, uint32_t parity, const LocalDev& c, int rank, int blk) {
+  if (mma_mbar_try(bar, parity)) return true;
+  const unsigned long long t0 = global_timer_ns();
+  for (unsigned it = 1;; ++it) {
+    if (mma_mbar_try(bar, parity)) return true;
+    if ((it & 15u) == 0) {
+      if (EARLY && ld_relaxed_gpu(c.status + 1) == c.tag) return false;
+      if (global_timer_ns() - t0 > c.timeout_ns) {
+        atomicCAS(c.status, 0ull, pack_status(kStatusTimeout, rank, rank, blk));
+        atomicExch(c.status + 1, c.tag);
+        return false;
+      }
+    }
+  }
+}
+// After a wait that gave up: lets this CTA's own copies or products in flight
+// end, as long as a wait may last, whatever others recorded.  (At once where
+// the phase is over.)
+__device__ __forceinline__ void local_drain(uint32_t bar, uint32_t parity) {
+  if (mma_mbar_try(bar, parity)) return;
+  const unsigned long long t0 = global_timer_ns();
+  while (!mma_mbar_try(bar, parity) && global_timer_ns() - t0 < 2000000000ull) {
+  }
+}
 
 // 32 lanes (a warp's quarter of the 128) x 16 or 32 columns
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v) {

@@ -674,9 +674,12 @@ int dcc_linear(int n_ranks, void* const* weight, void* const* x, void* const* bi
 /* Synchronise the stream and report what the calls of this section recorded
  * on the current device since the last check: DCC_OK, DCC_ERR_BOUNDS (a
  * sequence or page number out of range; the access was skipped) or
- * DCC_ERR_TIMEOUT (a wait inside a kernel gave up; its outputs and those of
- * calls since are not complete, and attention workspaces want zeroing again).
- * Clears the record. */
+ * DCC_ERR_TIMEOUT (a wait inside a kernel gave up; that call's outputs are not
+ * complete, a captured graph that holds the call wants a check before it runs
+ * again, and attention workspaces want zeroing).  Clears the record.  There is
+ * one record a device, for all streams and threads: a check says what any of
+ * them recorded, so a program that calls from several has one place that
+ * checks, after it has waited for all of them. */
 int dcc_local_check(dcc_stream_t s);
 
 #ifdef __cplusplus
