@@ -30,6 +30,7 @@ const void* linear_kernel(int which);
 const void* kv4_row_kernel(bool fp16, bool read, int dim, int group, bool several);
 const void* kv4_attention_kernel(bool fp16, int dim, int group, int which);
 const void* kv4_pages_kernel(int i);
+const void* local_take_kernel();
 }  // namespace dcc
 
 namespace {
@@ -373,8 +374,8 @@ bool visit_kernels(F&& visit) {
     if (!v(dcc::linear_kernel(i))) return false;
   for (int i = 0; i < 5; ++i)
     if (!v(dcc::kv4_pages_kernel(i))) return false;
-  return v(dcc::ring_barrier_kernel()) && v(dcc::ring_barrier_cluster_kernel()) && v(dcc::channel_put_kernel()) &&
-         v(dcc::channel_get_kernel());
+  return v(dcc::local_take_kernel()) && v(dcc::ring_barrier_kernel()) && v(dcc::ring_barrier_cluster_kernel()) &&
+         v(dcc::channel_put_kernel()) && v(dcc::channel_get_kernel());
 }
 
 }  // namespace

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "comm.h"
 #include "kv4.cuh"
 #include "tcgen05.cuh"
 
@@ -13,11 +14,19 @@ namespace {
 // Words per device: the first number out of range, the first wait that gave up,
 // the tag of the last call in which one did (LocalDev).  The address comes from
 // cudaGetSymbolAddress.
-static __device__ unsigned long long g_local_status[3];
+static __device__ unsigned long long g_local_status[6];  // and what the last check took of them
 constexpr int kMaxDevices = 64;
-std::mutex g_mu;
+std::mutex g_mu, g_check_mu;
 unsigned long long* g_addr[kMaxDevices];
+
+// Takes the record and leaves none, one word at a time in one step each: what a
+// kernel on another stream records meanwhile is either taken or left.
+__global__ void k_local_take(unsigned long long* status) { status[3 + threadIdx.x] = atomicExch(status + threadIdx.x, 0ull); }
 }  // namespace
+
+namespace dcc {
+const void* local_take_kernel() { return (const void*)&k_local_take; }
+}  // namespace dcc
 
 namespace dcc_host {
 
@@ -102,16 +111,21 @@ int dcc_local_check(dcc_stream_t s) {
   unsigned long long* p = dcc_host::local_status();
   if (!p) return DCC_ERR_CUDA;
   unsigned long long st[3] = {0, 0, 0};
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(s)) != cudaSuccess ||
-      cudaMemcpy(st, p, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) {
+  cudaStream_t stream = static_cast<cudaStream_t>(s);
+  if (cudaStreamSynchronize(stream) != cudaSuccess) {
+    cudaGetLastError();
+    return DCC_ERR_CUDA;
+  }
+  std::lock_guard<std::mutex> lock(g_check_mu);  // what was taken lies in one place
+  void* args[] = {&p};
+  const int rc = dcc_host::launch(dcc::local_take_kernel(), 1, 3, false, args, stream);
+  if (rc != DCC_OK) return rc;
+  if (cudaMemcpyAsync(st, p + 3, sizeof st, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess) {
     cudaGetLastError();
     return DCC_ERR_CUDA;
   }
   if (st[0] == 0 && st[1] == 0) return DCC_OK;
-  if (cudaMemset(p, 0, sizeof st) != cudaSuccess) {
-    cudaGetLastError();
-    return DCC_ERR_CUDA;
-  }
   return (st[1] & 0xffull) == dcc::kStatusTimeout ? DCC_ERR_TIMEOUT : DCC_ERR_BOUNDS;
 }
 

@@ -2,6 +2,7 @@
 written from the host here (no wait is made to run out): a failure that another
 call left in it changes nothing for the calls after, and is reported once."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -79,3 +80,36 @@ def test_the_record_is_reported_once(dcc):
         write_record(dcc, *words)
         assert dcc.dcc_local_check() == code
         assert dcc.dcc_local_check() == dcc.DCC_OK
+
+
+def test_failures_of_two_streams_are_all_reported(dcc):
+    """Two threads, a stream each: calls that fail, and a check after each.  No
+    failure may go unreported: one thread's check finds its own unless the other
+    thread's has reported something since the call."""
+    cache, _, _ = make_cache(dcc, torch.Generator().manual_seed(3), 1, [70], 1, 128, 64, "bf16")
+    cache.table[0, 1] = -1
+    x = torch.randn(70, 1, 128).bfloat16().cuda()
+    start = batch([70])
+    torch.cuda.synchronize()
+    reports, lost, turns = [0, 0], [], 300
+
+    def work(me):
+        stream = torch.cuda.Stream()
+        for i in range(turns):
+            before = reports[1 - me]
+            cache.append([x], [x], start, stream=stream)
+            code = dcc.dcc_local_check(stream)
+            if code == dcc.DCC_ERR_BOUNDS:
+                reports[me] += 1
+            elif reports[1 - me] == before and done[1 - me]:
+                lost.append((me, i, code))  # nobody else is left who could have taken it
+        done[me] = True
+
+    done = [False, False]
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not lost and sum(reports) > 0
+    assert dcc.dcc_local_check() == dcc.DCC_OK
