@@ -132,4 +132,13 @@ dcc::LocalDev local_dev(unsigned long long* status);
 // kv4_ready adds what a launch needs (ops_status.cu).
 int kv4_view(const dcc_kv4_t* kv, bool need_refs, dcc::Kv4Dev* out);
 int kv4_ready(dcc::Kv4Dev* d);
+// A buffer of a call; one that is written overlaps no other.
+struct Extent {
+  const void* p;
+  size_t bytes;
+  bool written;
+};
+bool disjoint(const Extent* e, int n);
+// Whether rows of `width` bytes, `stride` apart (both alike), meet: slices of one buffer may interleave.
+bool rows_overlap(const void* a, const void* b, size_t rows, size_t stride, size_t width);
 }  // namespace dcc_host

@@ -73,6 +73,12 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
                   dcc_host::overlaps(lse[r], lb, out[p], ob) || (p < r && dcc_host::overlaps(lse[r], lb, lse[p], lb))))
         return DCC_ERR_INVALID_ARG;
     }
+    // the small buffers of the call, against what it writes (and the workspace against all)
+    const size_t table = (size_t)kv->seqs * kv->max_pages * 4, seqs = (size_t)kv->seqs * 4;
+    const dcc_host::Extent e[] = {{workspace, need, true},   {out[r], ob, true},       {lse ? lse[r] : nullptr, lb, true},
+                                  {q[r], qb, false},         {kv->pool[r], pool, false}, {kv->table, table, false},
+                                  {kv->len, seqs, false},    {start, seqs + 4, false}};
+    if (!dcc_host::disjoint(e, 8)) return DCC_ERR_INVALID_ARG;
     a.q[r] = q[r];
     a.out[r] = out[r];
     a.lse[r] = lse ? lse[r] : nullptr;

@@ -282,12 +282,19 @@ int rows_call(bool read, const dcc_kv4_t* kv, int layer, void* const* k, void* c
   const size_t bytes = ((tokens - 1) * stride + width) * 2;
   const size_t pool = (size_t)kv->layers * kv->pages * width / kv->head_dim *
                       dcc::kv4_block_bytes(kv->head_dim, kv->group);
-  for (int r = 0; r < kv->n_ranks; ++r) {
+  for (int r = 0; r < kv->n_ranks; ++r)
     if (!k[r] || !v[r]) return DCC_ERR_INVALID_ARG;
+  for (int r = 0; r < kv->n_ranks; ++r) {
     if ((reinterpret_cast<uintptr_t>(k[r]) | reinterpret_cast<uintptr_t>(v[r])) & 15u) return DCC_ERR_MISALIGNED;
     for (int p = 0; p < kv->n_ranks; ++p)
       if (dcc_host::overlaps(k[r], bytes, kv->pool[p], pool) || dcc_host::overlaps(v[r], bytes, kv->pool[p], pool))
         return DCC_ERR_INVALID_ARG;
+    for (int p = 0; read && p < kv->n_ranks; ++p) {  // outputs
+      if (dcc_host::rows_overlap(k[r], v[p], tokens, stride * 2, width * 2) ||
+          (p < r && (dcc_host::rows_overlap(k[r], k[p], tokens, stride * 2, width * 2) ||
+                     dcc_host::rows_overlap(v[r], v[p], tokens, stride * 2, width * 2))))
+        return DCC_ERR_INVALID_ARG;
+    }
     a.k[r] = k[r];
     a.v[r] = v[r];
   }

@@ -19,6 +19,8 @@
 // the GPU holds) stride over (copy, rank, layer, chunk), 16 bytes a thread and
 // several loads in flight; it is bound by memory (GB300: 0.98 GB read and
 // written in 164 us with the books, 5.9 TB/s, 88 % of a plain copy's rate).
+#include <initializer_list>
+
 #include "comm.h"
 #include "kv4.cuh"
 
@@ -472,6 +474,25 @@ int copy_launch(const dcc_kv4_t* kv, dcc::Kv4Dev& d, dcc::CopyArgs& a, cudaStrea
   return launch(fn, sms * per_sm, dcc::kCopyThreads, false, args, s, 0, true);
 }
 
+// What a page call reads and writes lies apart: the cache's books, the pools, the
+// workspace, info and `more` (at most 4 of the call's own).
+bool books_apart(const dcc_kv4_t* kv, const void* ws, const int32_t* info,
+                 std::initializer_list<dcc_host::Extent> more) {
+  const size_t pool = (size_t)kv->layers * kv->pages * kv->kv_heads * dcc::kv4_block_bytes(kv->head_dim, kv->group);
+  dcc_host::Extent e[9 + DCC_MAX_RANKS] = {{kv->table, (size_t)kv->seqs * kv->max_pages * 4, true},
+                                           {kv->len, (size_t)kv->seqs * 4, true},
+                                           {kv->refs, (size_t)kv->pages * 4, true},
+                                           {ws, ws_bytes(kv), true},
+                                           {info, 16, true}};
+  int n = 5;
+  for (const dcc_host::Extent& x : more) e[n++] = x;
+  if (!dcc_host::disjoint(e, n)) return false;
+  for (int r = 0; r < kv->n_ranks; ++r)
+    for (int i = 0; i < n; ++i)
+      if (e[i].p && dcc_host::overlaps(e[i].p, e[i].bytes, kv->pool[r], pool)) return false;
+  return true;
+}
+
 // Kernel `which` for one CTA, which + 1 for a cluster, by the numbers to go through.
 int launch_book(int which, long long numbers, void** args, cudaStream_t s) {
   const bool one = numbers <= dcc::kBookOneCta;
@@ -488,6 +509,7 @@ int book_call(const dcc_kv4_t* kv, int mode, const int32_t* src, const int32_t* 
   if (count > (size_t)kv->seqs) return DCC_ERR_INVALID_ARG;
   if ((count && !dst) || (mode == dcc::kBookFork && count && !src)) return DCC_ERR_INVALID_ARG;
   if (odd_word(src) || odd_word(dst) || odd_word(info)) return DCC_ERR_MISALIGNED;
+  if (!books_apart(kv, ws, info, {{src, count * 4, false}, {dst, count * 4, false}})) return DCC_ERR_INVALID_ARG;
   a.src = src;
   a.dst = dst;
   a.count = (int)count;
@@ -556,6 +578,13 @@ int dcc_kv4_compact(const dcc_kv4_t* kv, int32_t* new_table, int32_t* new_refs, 
   if (rc != DCC_OK) return rc;
   if (!new_table || !new_refs || !remap) return DCC_ERR_INVALID_ARG;
   if (odd_word(new_table) || odd_word(new_refs) || odd_word(remap) || odd_word(info)) return DCC_ERR_MISALIGNED;
+  // the new table and counts may be the cache's own
+  const size_t table_bytes = (size_t)kv->seqs * kv->max_pages * 4, pages_bytes = (size_t)kv->pages * 4;
+  if (!books_apart(kv, workspace, info,
+                   {{new_table == kv->table ? nullptr : new_table, table_bytes, true},
+                    {new_refs == kv->refs ? nullptr : new_refs, pages_bytes, true},
+                    {remap, pages_bytes, true}}))
+    return DCC_ERR_INVALID_ARG;
   a.new_table = new_table;
   a.new_refs = new_refs;
   a.remap = remap;

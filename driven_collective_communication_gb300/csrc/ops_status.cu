@@ -96,6 +96,21 @@ int kv4_ready(dcc::Kv4Dev* d) {
   return d->status ? DCC_OK : DCC_ERR_CUDA;
 }
 
+bool disjoint(const Extent* e, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((e[i].written || e[j].written) && e[i].p && e[j].p && overlaps(e[i].p, e[i].bytes, e[j].p, e[j].bytes))
+        return false;
+  return true;
+}
+
+bool rows_overlap(const void* a, const void* b, size_t rows, size_t stride, size_t width) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b), d = x < y ? y - x : x - y;
+  if (rows <= 1) return rows == 1 && d < width;
+  const uintptr_t i = d / stride, m = d % stride;  // row j of one lies m past row j + i of the other
+  return (m < width && i < rows) || (stride - m < width && i + 1 < rows);
+}
+
 }  // namespace dcc_host
 
 extern "C" {

@@ -577,8 +577,7 @@ def dcc_kv4_attention(kv, layer, q, out, start, max_new, workspace, lse=None, sc
         raise ValueError("out and lse have dense rows")
     return _check(_lib.dcc_kv4_attention(kv.ref, layer, q.ptrs, out.ptrs, lse.ptrs if lse else None, heads, tokens,
                                          q.stride, _index(start, kv.seqs + 1, "start"), max_new,
-                                         kv.head_dim ** -0.5 if scale is None else scale, window,
-                                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                         kv.head_dim ** -0.5 if scale is None else scale, window, *_ws(workspace),
                                          _stream(stream)), "dcc_kv4_attention")
 
 
@@ -589,6 +588,8 @@ def dcc_kv4_pages_workspace(kv):
 
 
 def _ws(workspace):
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous CUDA tensor")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

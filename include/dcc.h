@@ -548,6 +548,8 @@ int dcc_kernel_binary_version(int* version);
 /* pointer per rank.  A failure seen on the device (a page number outside    */
 /* the pool, a wait that gave up) is recorded and skipped; dcc_local_check   */
 /* reports it.                                                               */
+/* A buffer that a call writes overlaps none of its others (INVALID_ARG);    */
+/* what may coincide is said at the call.                                    */
 /* ------------------------------------------------------------------------ */
 
 #define DCC_KV4_PAGE 64 /* tokens per page of a 4-bit cache */

@@ -67,3 +67,27 @@ def test_linear(dcc):
             dcc.dcc_linear(*args, **{"bias": b, **kw})
     with pytest.raises((ValueError, KeyError)):
         dcc.dcc_linear(w, x, y, bias=b, act="swish")
+
+
+class Cache:
+    """What the calls read of a cache before they marshal it."""
+    kv_heads, head_dim, seqs, pages, max_pages, n, torch_dtype, ref = 1, 64, 2, 4, 2, 1, torch.bfloat16, None
+
+
+def test_workspaces_are_dense_and_on_the_device(dcc):
+    i32 = dev(torch.zeros(8, dtype=torch.int32))
+    q, out = [bf16(2, 4, 64)], [bf16(2, 4, 64)]
+    for ws in (torch.zeros(64, dtype=torch.uint8), dev(torch.zeros(64, 2, dtype=torch.uint8)[:, 0])):
+        for call in (lambda: dcc.dcc_kv4_attention(Cache, 0, q, out, i32, 1, ws), lambda: dcc.dcc_kv4_reserve(Cache, i32, ws),
+                     lambda: dcc.dcc_kv4_free(Cache, i32[:1], ws), lambda: dcc.dcc_kv4_fork(Cache, i32[:1], i32[1:2], ws),
+                     lambda: dcc.dcc_kv4_compact(Cache, i32, i32, i32, ws)):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
+
+
+def test_index_tensors(dcc):
+    ws = dev(torch.zeros(64, dtype=torch.uint8))
+    for bad in (torch.zeros(8, dtype=torch.int32), dev(torch.zeros(8, dtype=torch.int64)),
+                dev(torch.zeros(16, dtype=torch.int32)[::2]), dev(torch.zeros(1, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="int32"):
+            dcc.dcc_kv4_reserve(Cache, bad, ws)
