@@ -9,25 +9,6 @@ AttnKernel attn_kernel(bool fp16, int dim, int group, int which) {
 const void* kv4_attention_kernel(bool fp16, int dim, int group, int which) { return attn_kernel(fp16, dim, group, which).fn; }
 }  // namespace dcc
 
-namespace {
-// Whether the prompt kernel runs.  It keeps the tensor cores busy but does not
-// split a segment's keys over CTAs; the streaming kernel spreads any work
-// evenly but goes over the cache once per row tile.  Per key, on GB300: a
-// wave of the prompt kernel takes 0.017 us, a pass of the streaming kernel
-// over one segment 5.6e-5 us, a 300th; with few pages its latency shows and it
-// is a 100th.  (`segments`: ranks x kv heads x sequences.)  Measured,
-// streaming / prompt, us, 8 heads per kv head of 128 channels: 8 segments of
-// 8192 keys, 64 tokens 121 / 154, 128 tokens 224 / 154; 1 segment of 60,000
-// keys, 128 tokens 200 / 1027; 128 segments of up to 4096 keys, 4 tokens 68 /
-// 75, 8 tokens 115 / 75, 128 tokens 1876 / 235; 8 segments of 700 keys x 4
-// heads, 64 tokens 29.8 / 29.5, 128 tokens 43 / 30.
-bool prompt_runs(long long segments, long long rows, int dim, int max_pages, int sms) {
-  const long long tile = dim == 64 ? 24 : 16, passes = (rows + tile - 1) / tile;
-  const long long ctas = segments * ((rows + dcc::kPromptRows - 1) / dcc::kPromptRows), waves = (ctas + sms - 1) / sms;
-  return rows > 16 && segments * passes > (max_pages <= 32 ? 100 : 300) * waves;
-}
-}  // namespace
-
 extern "C" {
 
 int dcc_kv4_attention_workspace(const dcc_kv4_t* kv, int q_heads, size_t* bytes) {
@@ -104,35 +85,21 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
     return DCC_ERR_CUDA;
   }
   const bool fp16 = kv->dtype == DCC_FP16;
-  const long long rows = (long long)max_new * a.share;
   cudaStream_t st = static_cast<cudaStream_t>(s);
-  if (prompt_runs((long long)kv->n_ranks * kv->kv_heads * kv->seqs, rows, kv->head_dim, kv->max_pages, sms)) {
+  const long long heads = (long long)kv->n_ranks * kv->kv_heads;
+  const dcc::AttnPlan p = dcc::attn_plan(heads, kv->seqs, kv->max_pages, kv->head_dim, a.share, (long long)tokens, max_new, sms);
+  if (p.prompt) {
     const dcc::AttnKernel k = dcc::attn_kernel(fp16, kv->head_dim, kv->group, dcc::kAttnPrompt);
     if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
-    // whole waves of 256-row tiles; what is left in 128-row tiles if they fit one wave
-    const long long segments = (long long)kv->n_ranks * kv->kv_heads * kv->seqs;
-    long long wide = (rows + dcc::kPromptRows - 1) / dcc::kPromptRows, narrow = 0;
-    const long long whole = segments * wide / sms * sms / segments;
-    const long long left = (rows - whole * dcc::kPromptRows + 127) / 128;
-    if (whole < wide && segments * left <= sms) {
-      wide = whole;
-      narrow = left;
-    }
-    if (wide > (1 << 24)) return DCC_ERR_INVALID_ARG;
-    a.wide = (int)wide;
-    const long long grid = (wide + narrow) * segments;
+    if (p.wide > (1 << 24)) return DCC_ERR_INVALID_ARG;
+    a.wide = (int)p.wide;
+    const long long grid = (p.wide + p.narrow) * heads * kv->seqs;
     if (grid > 0x7fffffffll) return DCC_ERR_INVALID_ARG;
     dcc::LocalDev dc = dcc_host::local_dev(d.status);
     void* args[] = {&d, &a, &dc};
     return dcc_host::launch(k.fn, (int)grid, k.threads, false, args, st, k.smem, true);
   }
-  // Row tiles: as few passes over the cache as the registers allow, then the
-  // fewest rows that make that many.
-  const int most = kv->head_dim == 64 ? 3 : 2, passes = ((int)rows + 8 * most - 1) / (8 * most);
-  const long long most_units = (long long)kv->n_ranks * kv->kv_heads * kv->seqs * kv->max_pages;
-  const bool small = rows <= 8 && most_units <= (long long)sms * dcc::kDecSmallWarps;
-  const dcc::AttnKernel k = dcc::attn_kernel(fp16, kv->head_dim, kv->group,
-                                             small ? dcc::kAttnSmall : ((int)rows + 8 * passes - 1) / (8 * passes));
+  const dcc::AttnKernel k = dcc::attn_kernel(fp16, kv->head_dim, kv->group, p.small ? dcc::kAttnSmall : p.tiles);
   if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
   void* args[] = {&d, &a};
   return dcc_host::launch(k.fn, sms < dcc::kDecMaxCtas ? sms : dcc::kDecMaxCtas, k.threads, false, args, st, k.smem,

@@ -64,6 +64,7 @@
 
 #include "bulk.cuh"
 #include "kv4.cuh"
+#include "kv4_plan.h"
 
 namespace dcc {
 
@@ -81,7 +82,7 @@ struct AttnArgs {
 };
 
 constexpr int kDecMaxCtas = 160;
-constexpr int kDecMaxWarps = 12, kDecSmallWarps = 4;
+constexpr int kDecMaxWarps = 12;
 // floats of a partial: m and l per row, then rows of O, padded so that the
 // fragments' stores fall into different banks
 __host__ __device__ constexpr int dec_slot(int rows, int dim) { return rows * (dim + 6); }

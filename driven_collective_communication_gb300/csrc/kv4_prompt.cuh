@@ -65,7 +65,6 @@
 namespace dcc {
 
 constexpr int kPromptThreads = 512;
-constexpr int kPromptRows = 256;  // per CTA: two tiles of 128
 constexpr int kPromptRing = 3;    // pages in flight
 
 template <int D, int G>
