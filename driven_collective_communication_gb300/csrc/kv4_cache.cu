@@ -7,10 +7,10 @@
 // halfway between two codes goes where the mathematics sends it.
 //
 // Both kernels ought to be bound by memory: 2 bytes an element on the dense
-// side, 1/2 + 4/G in the cache.  Measured on GB300, 12,400 rows x 2 heads x 128
-// channels x 8 ranks, fp16, G = 32 (136 MB each way): append 59 us (2.3 TB/s,
-// bound by its instructions, some 20 a value), read 32 us (4.2 TB/s, the
-// integer pipe).  D/8 lanes take one (token, head): 16-byte accesses to
+// side, 1/2 + 4/G in the cache.  Measured on GB300, 12,718 rows x 2 heads x 128
+// channels x 8 ranks, fp16, G = 32 (137 MB each way): append 59 us (2.3 TB/s),
+// read 32 us (4.2 TB/s).  Both now spend their time on instructions, 33 a value
+// appended and 17 read, at 77 % of the issue slots: one value at a time.  D/8 lanes take one (token, head): 16-byte accesses to
 // the dense rows, two tokens of a 128-wide head per warp; a group's minimum
 // and maximum are three shuffles.  A lane's eight K codes are one word of the
 // row; its eight V codes fall into the row's eight chunks, so the row is put

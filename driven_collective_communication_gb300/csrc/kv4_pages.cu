@@ -12,13 +12,13 @@
 // their workspace words -- the scan of the counts is the only long part, and
 // eight SMs read them eight times as fast as one, without a launch per phase.
 // It is bound by latency, and a cluster's barrier with its fence costs more
-// than a CTA's: a fork of 64 beams out of 128 with its copies takes 21 us on
-// GB300 with one CTA, 27 with the cluster.  It writes the list of page copies to
+// than a CTA's: a fork of 64 beams out of 128 with its copies takes 19 us on
+// GB300 with one CTA (a host that issues slowly: up to 25), 27 with the cluster.  It writes the list of page copies to
 // the workspace.  The second kernel copies:
 // the number of copies is only known on the device, so its CTAs (as many as
 // the GPU holds) stride over (copy, rank, layer, chunk), 16 bytes a thread and
 // several loads in flight; it is bound by memory (GB300: 0.98 GB read and
-// written in 164 us with the books, 5.9 TB/s, 88 % of a plain copy's rate).
+// written in 162 us with the books, 6.0 TB/s, 89 % of a plain copy's rate).
 #include <initializer_list>
 
 #include "comm.h"

@@ -26,14 +26,21 @@
 // in ordinary caches, so their forms are short rather than fast.
 //
 // Measured on GB300, 2048 new tokens on 8192 keys, 8 ranks x 8 query heads x 128
-// channels: fp16 530 us, 0.92 PFLOP/s; bf16 551 us, 0.88 PFLOP/s, 46 % of a
-// library product's rate (the MMAs alone: 326 us; bf16 tiles: 521 us).  What
-// bounds it is shared memory (the S products read 128 bytes a clock, all there
-// is, and the unpacking warps' accesses and every barrier queue behind them) and
-// the instructions of P and the unpacking.  Tried without gain: separate warps
-// for K and V, a row of scores held in registers, P handed over in halves, an
-// MMA warp that polls both tiles, rings of K's and V's codes apart (a deeper
-// prefetch: 542 us where this took 523).
+// channels: fp16 534 us, 0.91 PFLOP/s; bf16 551 us, 0.88 PFLOP/s, 46 % of a
+// library product's rate (the MMAs alone: 326 us; bf16 tiles: 521 us).  No unit is
+// near its rate: tensor pipe 39 %, issue slots 48 %, integer pipe 37 %, exponentials
+// 20 %, shared memory 21 % for the warps and 27 % for the MMAs' operands.  The warps
+// wait for tensor memory and for one another: a step is a chain of hand-overs
+// (unpack, S, P, O) with two row tiles in turn to cover it.  Tried without gain:
+// separate warps for K and V, a row of scores held in registers, P handed over in
+// halves, an MMA warp that polls both tiles, rings of K's and V's codes apart (a
+// deeper prefetch: 542 us where this took 523).
+//
+// What it rounds, each to fp16 (2^-12 of the value): K, V and P, where the streaming
+// kernel rounds p * step alone.  The errors average over the keys a row sees only as
+// fast as the output itself does, so an fp16 output is off by up to 4.1e-4 in its
+// 2-norm where its own rounding is 2.1e-4; bf16 outputs show their own rounding only.
+// Values of V beyond 2^100 (bf16) may overflow the sums.
 //
 // Roles (512 threads): warp 0 loads pages (one bulk copy each, three in
 // flight); warp 1 issues the MMAs; warps 2..5 unpack; warps 6..9 and 10..13
@@ -56,7 +63,7 @@
 // get NaN and the others nothing.  A value past the type's largest (by an ulp,
 // where the step was rounded up) counts as the largest: as an infinity it would
 // reach the rows that do not see the key, whose P is 0.  (Looking for such
-// groups in the fp16 cache costs 523 -> 530 us.)
+// groups in the fp16 cache cost 523 -> 530 us.)
 #pragma once
 #include "fused_mma.cuh"
 #include "kv4_decode.cuh"

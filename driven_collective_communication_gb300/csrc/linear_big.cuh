@@ -11,9 +11,11 @@
 // of one weight tile side by side (the weights then come from memory once),
 // and the accumulator is doubled in tensor memory, so the epilogue of one tile
 // runs under the products of the next.  Measured on GB300, 8 ranks, 2048 tokens x
-// 3584 rows x 8192, bias and GELU: 530-600 us by the clock that the power limit
-// leaves, 1.6-1.8 PFLOP/s (a library product alone: 1.9 in a burst, 1.7
-// sustained).  Roles (192 threads):
+// 3584 rows x 8192, bias and GELU: 590-610 us by the clock that the power limit
+// leaves, 1.6 PFLOP/s (a library product alone: 1.9 in a burst, 1.7 sustained); the
+// tensor pipe is active 81 % of the time.  All of K goes into one accumulator, whose
+// adds truncate: some more results fall an ulp of their type off than with K split.
+// Roles (192 threads):
 //   warp 0, one thread       TMA into this CTA's stage; the bytes of both CTAs
 //                             complete on the leader's full barrier;
 //   warp 1, one thread       (leader) tcgen05.mma 256 x N x 16; commits free

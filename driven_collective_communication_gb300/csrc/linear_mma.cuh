@@ -10,9 +10,9 @@
 // enough CTAs stream when the rows alone are few, and join their partial tiles
 // through distributed shared memory, in split order.  Then bias, activation,
 // residual and the one rounding follow in registers.  Measured on GB300, 8
-// ranks, K = 8192: 1 token x 1024 rows 22.6 us (134 MB, 5.9 TB/s, 88 % of a plain
-// copy's rate), 64 tokens x 3584 rows with bias, GELU and residual 78 us (478 MB,
-// 6.1 TB/s, 90 %).  Roles per CTA (128
+// ranks, K = 8192: 1 token x 1024 rows 23.1 us (134 MB, 5.8 TB/s, 86 % of a plain
+// copy's rate), 64 tokens x 3584 rows with bias, GELU and residual 81.5 us (478 MB,
+// 5.9 TB/s, 87 %).  Roles per CTA (128
 // threads, two CTAs to an SM, or 256):
 //   warp 0, one thread   TMA: per 64 channels, the rows x 64 tile of W and the
 //                         tokens x 64 tile of X (128-byte swizzled, K-major)

@@ -603,8 +603,11 @@ int dcc_kv4_read(const dcc_kv4_t* kv, int layer, void* const* k, void* const* v,
  * elements apart (a multiple of 8), out rows dense; lse NULL, or lse[r]:
  * tokens * q_heads floats.  max_new: an upper bound of start[s+1] - start[s]
  * (rows past it are left as they are).  q_heads a multiple of kv_heads, at
- * most 128 query heads per kv head.  Scores, softmax and sums in fp32; the
- * probabilities enter the second product rounded to 16 bits.
+ * most 128 query heads per kv head.  Scores, softmax and sums in fp32.  What
+ * enters the products in 16 bits: with few rows per sequence step * p (11 bits;
+ * the codes and q are exact), with many K, V and p (fp16, also of a bf16 cache;
+ * bf16 V and p in pages where a group's largest |V| is not in 2^-8 .. 2^11).
+ * K or V of a bf16 cache beyond 2^96 may overflow the fp32 sums.
  * workspace: dcc_kv4_attention_workspace bytes, 16-byte aligned, filled with
  * zeros once before its first use (calls leave its counters at zero); calls
  * that may run at the same time need one each. */
