@@ -479,11 +479,11 @@ int copy_launch(const dcc_kv4_t* kv, dcc::Kv4Dev& d, dcc::CopyArgs& a, cudaStrea
 bool books_apart(const dcc_kv4_t* kv, const void* ws, const int32_t* info,
                  std::initializer_list<dcc_host::Extent> more) {
   const size_t pool = (size_t)kv->layers * kv->pages * kv->kv_heads * dcc::kv4_block_bytes(kv->head_dim, kv->group);
-  dcc_host::Extent e[9 + DCC_MAX_RANKS] = {{kv->table, (size_t)kv->seqs * kv->max_pages * 4, true},
-                                           {kv->len, (size_t)kv->seqs * 4, true},
-                                           {kv->refs, (size_t)kv->pages * 4, true},
-                                           {ws, ws_bytes(kv), true},
-                                           {info, 16, true}};
+  dcc_host::Extent e[9] = {{kv->table, (size_t)kv->seqs * kv->max_pages * 4, true},
+                           {kv->len, (size_t)kv->seqs * 4, true},
+                           {kv->refs, (size_t)kv->pages * 4, true},
+                           {ws, ws_bytes(kv), true},
+                           {info, 16, true}};
   int n = 5;
   for (const dcc_host::Extent& x : more) e[n++] = x;
   if (!dcc_host::disjoint(e, n)) return false;

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMmaPairThreads ? 2 : 1)
       tma_load_2d_hint(sa, &maps.w[rank], (b0 + i) * kMmaBK, m0, full(s), pol_w);
       tma_load_2d_hint(sa + a_bytes, &maps.x[rank], (b0 + i) * kMmaBK, 0, full(s), pol_x);
     }
-    // none is in flight when the stages are used again, whoever gave up
+    // none is in flight when the CTA leaves, whoever gave up
     for (int j = i > S ? i - S : 0; j < i; ++j) local_drain(full(j % S), (uint32_t)((j / S) & 1));
   } else if (warp == 1 && lane == 0) {  // MMA issuer
     const uint32_t idesc = mma_instr_desc(NTILE, a.fp16 != 0);
