@@ -10,13 +10,14 @@
 // everything that carries lo is fp32.  The codes are exact.  So is Q: a row is
 // scaled by a power of two that brings its largest channel to 2^14, which
 // keeps all bits of a bf16 or fp16 channel down to 2^-28 of it.  p * step is
-// the one operand that is rounded (11 bits; 22 in pages where a mask begins or
-// ends); its scale follows the running maximum of s_j and of the steps (R
-// below: l, O and all sums are in units of 2^R), so it neither overflows nor
-// falls into the subnormals unless it is 2^-28 of the largest that a row of the
-// tile has seen.  Codes
-// enter O as n - 8, about the middle of their range, so that what is rounded
-// is no larger than V itself.
+// the one operand that is rounded, to fp16's 11 bits; its scale follows the
+// running maximum of s_j and of the steps (R below: l, O and all sums are in
+// units of 2^R), so it neither overflows nor falls into the subnormals unless it
+// is 2^-28 of the largest seen.  In pages where a mask begins or ends it is two
+// bf16 numbers, 16 bits: there a row may see a handful of keys, whose errors do
+// not average, beside keys of any size that only other rows see.  Codes enter O
+// as n - 8, about the middle of their range, so that what is rounded is about
+// half of the group's range at most.
 //
 // Bound by reading the cache (0.56 bytes a channel at G = 64) if the
 // instructions that unpack it stay below the memory's time, above all the
@@ -25,8 +26,8 @@
 // makes two codes an operand register, after a shift for three nibbles of
 // four (the left one runs on the multiply pipe).  The 64 comes off the scores
 // as the accumulators' initial value (-64 sum q), and off O, with the 8, by a
-// product of the same rounded p * step with a constant -72 before each product
-// with codes: nothing is subtracted or converted per code.  (Taken off in the
+// product of the same rounded p * step with a constant -72 (bf16: 128 + n and -136)
+// before each product with codes: nothing is subtracted or converted per code.  (Taken off in the
 // end, through one row of ones, it would cost fewer products, but the
 // accumulators then carry 72 sum p * step all along, and the tensor core
 // truncates its sums: over 131k keys the result lost 3 bits.  Bare nibbles are
@@ -53,9 +54,9 @@
 // do not depend on timing.
 //
 // Measured on GB300, bf16, 8 ranks x 1 kv head x 8 query heads x 128 channels, G
-// = 64, one token each: 64 sequences of up to 8192 keys 91 us (326 MB, 3.6 TB/s,
-// 53 % of a plain copy's rate); one of 777 keys 13 us.  fp16, 2 kv heads x 4, G =
-// 32, one sequence of 131,109 keys: 89 us (336 MB, 3.8 TB/s).  The loads alone
+// = 64, one token each: 64 sequences of up to 8192 keys 92 us (326 MB, 3.5 TB/s,
+// 52 % of a plain copy's rate); one of 777 keys 13 us.  fp16, 2 kv heads x 4, G =
+// 32, one sequence of 131,109 keys: 90 us (336 MB, 3.7 TB/s).  The loads alone
 // take 74 and 63 us (65 and 79 % of the copy's rate), loads and scores 82 and 69: of
 // the rest about 10 us are the start (plan, page numbers, first pages) and 10 the
 // joins and uneven ends, and the loop issues 2.6 of 4 instructions a clock.  Calls
@@ -132,6 +133,21 @@ __device__ __forceinline__ void mma_16816_from(float* d, uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }  // -126 <= k <= 127
+// the same with bf16 operands
+__device__ __forceinline__ void mma_16816_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// nibbles P and P + 4 of w as two bf16 numbers 128 + n
+template <int P>
+__device__ __forceinline__ uint32_t code_pair_bf16(uint32_t w) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * P)), "r"(0x000f000fu), "r"(0x43004300u));
+  return r;
+}
 // nibbles P and P + 4 of w as two fp16 numbers 64 + n
 template <int P>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
@@ -249,10 +265,11 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
   constexpr int W = Shape::warps, S = Shape::stages, BLK = Shape::block, THREADS = W * 32;
   constexpr int NG = D / G, ROWS = 8 * RT, JW = D / 32, MT = D / 16, SLOT = dec_slot(ROWS, D);
   constexpr float kCenter = 8.0f;
-  constexpr uint32_t kBias = 0xd480d480u;  // fp16 -72 = -(64 + kCenter), twice
+  constexpr uint32_t kBias = 0xd480d480u;      // fp16 -72 = -(64 + kCenter), twice
+  constexpr uint32_t kBiasWide = 0xc308c308u;  // bf16 -136 = -(128 + kCenter)
   constexpr int kMinExp = -60;  // steps below 2^-60 count as that: 2^(14 + 60) a key still sums in fp32
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr uint32_t kLoFloor = 80u << 7;
+  constexpr uint32_t kFloor = 80u << 7;
   extern __shared__ __align__(128) char dec_smem[];
   __shared__ __align__(8) uint64_t bars[W][S];
   __shared__ long long s_sum[W];
@@ -567,23 +584,38 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
           }
       }
     }
-    // the largest step of V (its exponent) and the running maximum; what was
-    // summed so far is rescaled where they grew
-    uint32_t top = 0;  // by halves: step, lo
+    // The largest step of V (its exponent) and the running maximum; what was summed
+    // so far is rescaled where they grew.  In masked pages, where p * step has
+    // bf16's range, the smallest that a key has at most: keys that only some rows
+    // see may be any size, and their scale is not the others'.
+    uint32_t top = 0, low = 0x7fffu;  // by halves: step, lo
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      const int key = 2 * lane + h;
+      uint32_t one = MASKED ? 0u : top;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        const int key = 2 * lane + h;
         uint32_t w = (vpar - kg * NG)[key * NG + gr] & (kBf16 ? 0x7fff7fffu : 0x7fffu);
         const bool finite = kBf16 ? ((w + 0x00800080u) & 0x80008000u) == 0u : w < 0x7c00u;
         if (!finite || (MASKED && key0 + key > tile_end)) w = 0;
-        top = kBf16 ? __vmaxu2(top, w) : max(top, w);
+        one = kBf16 ? __vmaxu2(one, w) : max(one, w);
       }
-    // a bf16 lo far above all steps (constant groups) counts as 2^-80 of itself:
-    // p lo stays below 2^95, and 2^30 of them still sum in fp32
-    if (kBf16) top = max(top & 0xffffu, max(top >> 16, kLoFloor) - kLoFloor);
+      if (MASKED && (one & 0x7fffu)) low = min(low, one & 0x7fffu);
+      if (MASKED) one = kBf16 ? __vmaxu2(top, one) : 0u;
+      top = one;
+    }
+    // A bf16 lo far above all steps (constant groups), and such a step in a masked
+    // page, count as 2^-80 of themselves: p times either stays below 2^95, and
+    // 2^25 of them still sum in fp32.
+    if (kBf16) {
+      const uint32_t far = max(max(MASKED ? top & 0xffffu : 0u, top >> 16), kFloor) - kFloor;
+      top = MASKED ? far : max(top & 0xffffu, far);
+    }
     top = __reduce_max_sync(0xffffffffu, top);
+    if (MASKED) {
+      low = __reduce_min_sync(0xffffffffu, low);
+      if (low < 0x7fffu) top = max(top, low);
+    }
     const int ex_new = max(ex, (__float_as_int(Half16<T>::widen((uint16_t)top)) >> 23) - 127);
     bool grew = ex_new > ex;
     float alpha[RT][2], ref[RT][2];
@@ -624,8 +656,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {  // 16 keys each
-      // P^T fragments: p * step, and in masked pages what its rounding left (a
-      // row that sees a handful of keys has no other errors to average it with)
+      // P^T fragments: p * step, and in masked pages what its rounding left
       uint32_t bp[RT][NG][2], bq[RT][NG][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -655,11 +686,12 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
               if (MASKED && p[b] == 0.0f) q[b] = c = 0.0f;  // tokens that are not there may hold anything
               pmid[x][gr][b] = fmaf(p[b], c, pmid[x][gr][b]);
             }
-            const uint32_t w = half2_bits(q[0], q[1]);
+            using Wide = Half16<__nv_bfloat16>;
+            const uint32_t w = MASKED ? Wide::narrow2(q[0], q[1]) : half2_bits(q[0], q[1]);
             bp[x][gr][h] = transpose8(w);
             if (MASKED) {
-              const float2 f = Half16<__half>::widen2(w);
-              bq[x][gr][h] = transpose8(half2_bits(q[0] - f.x, q[1] - f.y));
+              const float2 f = Wide::widen2(w);
+              bq[x][gr][h] = transpose8(Wide::narrow2(q[0] - f.x, q[1] - f.y));
             }
           }
         }
@@ -684,19 +716,31 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
         const int w = q4 >> 1;
         const uint32_t x0 = __byte_perm(v[0][0][w], v[0][1][w], (q4 & 1) ? 0x7632 : 0x5410);
         const uint32_t x1 = __byte_perm(v[1][0][w], v[1][1][w], (q4 & 1) ? 0x7632 : 0x5410);
-        const uint32_t f0[4] = {code_pair<0>(x0), code_pair<1>(x0), code_pair<0>(x1), code_pair<1>(x1)};
-        const uint32_t f1[4] = {code_pair<2>(x0), code_pair<3>(x0), code_pair<2>(x1), code_pair<3>(x1)};
+        if constexpr (MASKED) {
+          const uint32_t f0[4] = {code_pair_bf16<0>(x0), code_pair_bf16<1>(x0), code_pair_bf16<0>(x1), code_pair_bf16<1>(x1)};
+          const uint32_t f1[4] = {code_pair_bf16<2>(x0), code_pair_bf16<3>(x0), code_pair_bf16<2>(x1), code_pair_bf16<3>(x1)};
 #pragma unroll
-        for (int x = 0; x < RT; ++x) {
-          const int g0 = 32 * q4 / G;
-          auto both = [&](const uint32_t* b) {
+          for (int x = 0; x < RT; ++x) {
+            auto both = [&](const uint32_t* b) {
+              mma_16816_bf16(o[x][2 * q4], kBiasWide, kBiasWide, kBiasWide, kBiasWide, b[0], b[1]);
+              mma_16816_bf16(o[x][2 * q4 + 1], kBiasWide, kBiasWide, kBiasWide, kBiasWide, b[0], b[1]);
+              mma_16816_bf16(o[x][2 * q4], f0[0], f0[1], f0[2], f0[3], b[0], b[1]);
+              mma_16816_bf16(o[x][2 * q4 + 1], f1[0], f1[1], f1[2], f1[3], b[0], b[1]);
+            };
+            both(bp[x][32 * q4 / G]);
+            both(bq[x][32 * q4 / G]);
+          }
+        } else {
+          const uint32_t f0[4] = {code_pair<0>(x0), code_pair<1>(x0), code_pair<0>(x1), code_pair<1>(x1)};
+          const uint32_t f1[4] = {code_pair<2>(x0), code_pair<3>(x0), code_pair<2>(x1), code_pair<3>(x1)};
+#pragma unroll
+          for (int x = 0; x < RT; ++x) {
+            const uint32_t* b = bp[x][32 * q4 / G];
             mma_16816(o[x][2 * q4], kBias, kBias, kBias, kBias, b[0], b[1]);
             mma_16816(o[x][2 * q4 + 1], kBias, kBias, kBias, kBias, b[0], b[1]);
             mma_16816(o[x][2 * q4], f0[0], f0[1], f0[2], f0[3], b[0], b[1]);
             mma_16816(o[x][2 * q4 + 1], f1[0], f1[1], f1[2], f1[3], b[0], b[1]);
-          };
-          both(bp[x][g0]);
-          if (MASKED) both(bq[x][g0]);
+          }
         }
       }
     }

@@ -151,3 +151,31 @@ def test_constant_groups_of_v(dcc, form, dtype, value, dim, group):
         out = run(dcc, cache, table, q, [m, m], [new, new], n, 8, group, dtype, kernel)
         exact = torch.tensor(value).to(TD[dtype]).double().item()
         assert ((out[0][..., :constant].double() / exact - 1).abs() <= 2 * R.U[dtype]).all()
+
+
+@pytest.mark.parametrize("form,news", [("one token", [1, 1]), ("streaming", [3, 5]), ("streaming", [40, 7]), ("prompt", [60, 61])])
+@pytest.mark.parametrize("dtype,small,large", [("bf16", 1.0, 1e12), ("bf16", 1e-20, 1e8), ("fp16", 2.0 ** -18, 6e4)])
+@pytest.mark.parametrize("dim,group", [(128, 64), (64, 32), (128, 32)])
+@pytest.mark.parametrize("window", [0, 21])
+def test_rows_do_not_lose_bits_to_keys_they_do_not_see(dcc, form, news, dtype, small, large, dim, group, window):
+    """V of every fifth of the newest tokens is larger than the rest by more than
+    a product's 16 bits can span: rows before such a token, or past its window,
+    are as exact as without it."""
+    n, _, kernel = FORMS[form]
+    g = torch.Generator().manual_seed(26)
+    m = 200
+    cache, _, table = make_cache(dcc, g, n, [m, m], 1, dim, group, dtype)
+    k = torch.randn(2 * m, 1, dim, generator=g).to(TD[dtype])
+    v = torch.randn(2 * m, 1, dim, generator=g) * small
+    huge = [(s, at) for s, t in enumerate(news) for at in range(m - t + 1, m, 5)]
+    for s, at in huge:
+        v[s * m + at] *= large / small / 4
+    cache.append([k.cuda()] * n, [v.clamp(-6e4, 6e4).to(TD[dtype]).cuda() if dtype == "fp16" else v.to(TD[dtype]).cuda()] * n,
+                 batch([m, m]))
+    q = torch.randn(sum(news), 8, dim, generator=g).to(TD[dtype])
+
+    def rows(s, pos):  # those that see none of them
+        w = window or m
+        return torch.stack([((at > pos) | (at <= pos - w)) for t, at in huge if t == s] +
+                           [torch.ones_like(pos, dtype=torch.bool)]).all(0)
+    run(dcc, cache, table, q, [m, m], news, n, 8, group, dtype, kernel, window=window, rows=rows)
