@@ -54,7 +54,7 @@
 // do not depend on timing.
 //
 // Measured on GB300, bf16, 8 ranks x 1 kv head x 8 query heads x 128 channels, G
-// = 64, one token each: 64 sequences of up to 8192 keys 92 us (326 MB, 3.5 TB/s,
+// = 64, one token each: 64 sequences of up to 8192 keys 93 us (326 MB, 3.5 TB/s,
 // 52 % of a plain copy's rate); one of 777 keys 13 us.  fp16, 2 kv heads x 4, G =
 // 32, one sequence of 131,109 keys: 90 us (336 MB, 3.7 TB/s).  The loads alone
 // take 74 and 63 us (65 and 79 % of the copy's rate), loads and scores 82 and 69: of
@@ -62,7 +62,7 @@
 // joins and uneven ends, and the loop issues 2.6 of 4 instructions a clock.  Calls
 // of few pages a warp are another matter: 16 sequences x 5 drafted tokens in a window
 // of 1024 keys, 64 channels, 47 us for 19 MB; the warps have three or four pages each
-// and spend 39 % of their cycles waiting for instructions, the unrolled code being
+// and spend 40 % of their cycles waiting for instructions, the unrolled code being
 // fetched for the first time.
 #pragma once
 #include <type_traits>
