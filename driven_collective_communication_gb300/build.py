@@ -41,10 +41,10 @@ SOURCES = ["dcc_host.cu", "sync_kernels.cu", "coll_allgather.cu",
            "coll_int32.cu", "coll_fp32.cu", "coll_fp16.cu", "coll_bf16.cu", "noalloc.cu",
            "proxy.cu", "coll_fused_bulk.cu", "coll_max.cu", "coll_min.cu", "coll_fused_mma.cu",
            "ops_status.cu", "kv4_cache.cu", "kv4_pages.cu", "kv4_attention.cu",
-           "kv4_attention_bf16.cu", "kv4_attention_fp16.cu", "linear.cu"]
+           "kv4_attention_bf16.cu", "kv4_attention_fp16.cu", "kv4_seen_bf16.cu", "kv4_seen_fp16.cu", "logprobs.cu", "linear.cu"]
 # Sources without data accesses that DCC_CHECK_BOUNDS checks (their kernels check
 # what they read from tables by themselves): one object serves both builds.
-SHARED = [s for s in SOURCES if s.startswith(("kv4_", "linear", "ops_"))]
+SHARED = [s for s in SOURCES if s.startswith(("kv4_", "linear", "logprobs", "ops_"))]
 
 
 def nvcc():

@@ -28,7 +28,8 @@
 namespace dcc {  // kernels of the calls without a communicator, for visit_kernels
 const void* linear_kernel(int which);
 const void* kv4_row_kernel(bool fp16, bool read, int dim, int group, bool several);
-const void* kv4_attention_kernel(bool fp16, int dim, int group, int which);
+const void* kv4_attention_kernel(bool fp16, bool seen, int dim, int group, int which);
+const void* logprobs_kernel(int which);
 const void* kv4_pages_kernel(int i);
 const void* local_take_kernel();
 }  // namespace dcc
@@ -364,16 +365,21 @@ bool visit_kernels(F&& visit) {
     for (int dim = 64; dim <= 128; dim += 64)
       for (int group = 32; group <= 64; group += 32)
         if (!v(dcc::kv4_row_kernel(fp16, false, dim, group, false)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group, false)) ||
-            !v(dcc::kv4_row_kernel(fp16, false, dim, group, true)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group, true)) ||
-            !v(dcc::kv4_attention_kernel(fp16, dim, group, 1)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 2)) ||
-            !v(dcc::kv4_attention_kernel(fp16, dim, group, 3)) || !v(dcc::kv4_attention_kernel(fp16, dim, group, 0)) ||
-            !v(dcc::kv4_attention_kernel(fp16, dim, group, 4)))
+            !v(dcc::kv4_row_kernel(fp16, false, dim, group, true)) || !v(dcc::kv4_row_kernel(fp16, true, dim, group, true)))
           return false;
+    for (int dim = 64; dim <= 128; dim += 64)
+      for (int group = 32; group <= 64; group += 32)
+        for (int which = 0; which < 5; ++which)
+          if (!v(dcc::kv4_attention_kernel(fp16, false, dim, group, which)) ||
+              !v(dcc::kv4_attention_kernel(fp16, true, dim, group, which)))
+            return false;
   }
   for (int i = 0; i < 3; ++i)
     if (!v(dcc::linear_kernel(i))) return false;
-  for (int i = 0; i < 5; ++i)
+  for (int i = 0; i < 12; ++i)
     if (!v(dcc::kv4_pages_kernel(i))) return false;
+  for (int i = 0; i < 6; ++i)
+    if (!v(dcc::logprobs_kernel(i))) return false;
   return v(dcc::local_take_kernel()) && v(dcc::ring_barrier_kernel()) && v(dcc::ring_barrier_cluster_kernel()) &&
          v(dcc::channel_put_kernel()) && v(dcc::channel_get_kernel());
 }

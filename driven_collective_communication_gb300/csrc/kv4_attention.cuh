@@ -1,5 +1,6 @@
 // kv4_attention.cuh -- the attention's kernels by type, head size and group; the
-// two types compile in a unit each (kv4_attention_bf16.cu, kv4_attention_fp16.cu).
+// two types compile in a unit each (kv4_attention_bf16.cu, kv4_attention_fp16.cu),
+// and so do those for rows with sets of seen keys of their own (kv4_seen_*.cu).
 #pragma once
 #include "kv4_prompt.cuh"
 
@@ -15,14 +16,16 @@ struct AttnKernel {
 constexpr int kAttnPrompt = 0, kAttnSmall = 4;
 AttnKernel attn_kernel_bf16(int dim, int group, int which);
 AttnKernel attn_kernel_fp16(int dim, int group, int which);
+AttnKernel attn_seen_kernel_bf16(int dim, int group, int which);
+AttnKernel attn_seen_kernel_fp16(int dim, int group, int which);
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool SEEN>
 AttnKernel attn_kernel_of(int which) {
   auto decode = [](auto tiles, auto small) {
     constexpr int RT = decltype(tiles)::value;
     constexpr bool SMALL = decltype(small)::value;
     using S = DecShape<D, G, RT, SMALL>;
-    return AttnKernel{(const void*)&k_kv4_decode<T, D, G, RT, SMALL>, S::warps * 32, S::smem};
+    return AttnKernel{(const void*)&k_kv4_decode<T, D, G, RT, SMALL, SEEN>, S::warps * 32, S::smem};
   };
   using No = std::false_type;
   switch (which) {
@@ -35,10 +38,10 @@ AttnKernel attn_kernel_of(int which) {
     if (which == 3) return decode(std::integral_constant<int, 3>{}, No{});
   return decode(std::integral_constant<int, 2>{}, No{});
 }
-template <typename T>
+template <typename T, bool SEEN = false>
 AttnKernel attn_kernel_for(int dim, int group, int which) {
-  if (dim == 128) return group == 64 ? attn_kernel_of<T, 128, 64>(which) : attn_kernel_of<T, 128, 32>(which);
-  return group == 64 ? attn_kernel_of<T, 64, 64>(which) : attn_kernel_of<T, 64, 32>(which);
+  if (dim == 128) return group == 64 ? attn_kernel_of<T, 128, 64, SEEN>(which) : attn_kernel_of<T, 128, 32, SEEN>(which);
+  return group == 64 ? attn_kernel_of<T, 64, 64, SEEN>(which) : attn_kernel_of<T, 64, 32, SEEN>(which);
 }
 
 }  // namespace dcc

@@ -82,10 +82,15 @@ struct AttnArgs {
   size_t q_stride;
   int tokens, layer, q_heads, share, max_new, window;
   int wide;  // prompt kernel: tiles of 256 rows per segment, before those of 128
+  // rows with sets of seen keys of their own (SEEN, below)
+  int sinks;             // first tokens that a window does not hide
+  int words;             // of a row of mask
+  const uint32_t* mask;  // a tree's: drafted token j of the sequence is seen where bit j is set; null: causal rows
   float scale;
   unsigned long long timeout_ns;
 };
 
+constexpr int kTreeWords = DCC_TREE_MAX / 32;  // of a row's mask
 constexpr int kDecMaxCtas = 160;
 constexpr int kDecMaxWarps = 12;
 // floats of a partial: m and l per row, then rows of O, padded so that the
@@ -164,27 +169,79 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t w) {
 }
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) { return Half16<__half>::narrow2(a, b); }
 
+// ---- SEEN: rows that do not see one run of keys each.  A row sees the keys lo ..
+// hi, the sinks up to hi and, of a tree, the drafted tokens of its mask; hi is
+// its own position, or in a tree the last one of the context.
+
+// bits 0 .. n - 1 of a word
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+struct SeenRow {
+  int hi, lo;      // hi < 0: nothing
+  int pos0, news;  // of the sequence: where its drafted tokens begin, and how many there are
+  const uint32_t* mask;
+};
+__device__ __forceinline__ uint32_t seen_mask_word(const SeenRow& r, int words, int i) {
+  return i >= 0 && i < words ? r.mask[i] & bits_below(r.news - 32 * i) : 0u;
+}
+// Of the keys k0 .. k0 + 31, those that the row sees.
+__device__ __forceinline__ uint32_t seen_word(const SeenRow& r, const AttnArgs& a, int k0) {
+  uint32_t w = bits_below(r.hi + 1 - k0) & (~bits_below(r.lo - k0) | bits_below(a.sinks - k0));
+  const int d = k0 - r.pos0;
+  if (r.mask && d > -32 && d < r.news)
+    w |= __funnelshift_r(seen_mask_word(r, a.words, d >> 5), seen_mask_word(r, a.words, (d >> 5) + 1), (uint32_t)d & 31u);
+  return w;
+}
+// Row of new token `tok` of a sequence: token `at` of the batch.
+__device__ __forceinline__ SeenRow seen_row(const AttnArgs& a, int pos0, int news, int tok, int at) {
+  SeenRow r = {pos0 + tok, 0, pos0, news, nullptr};
+  int own = tok + 1;  // new tokens that it sees: the window is over these and the context
+  if (a.mask) {
+    r.mask = a.mask + (size_t)at * a.words;
+    r.hi = pos0 - 1;
+    if (a.window > 0) {
+      own = 0;
+      for (int i = 0; i < a.words && 32 * i < news; ++i) own += __popc(seen_mask_word(r, a.words, i));
+    }
+  }
+  if (a.window > 0) r.lo = pos0 + own - a.window;
+  return r;
+}
+
 // One sequence's part of the line of units.
 struct DecSeq {
   int begin, rows, pos0, page0, pages, tiles;  // rows: new tokens * share; tiles * pages units per (rank, head)
   bool empty;
+  // SEEN: the first `kept` of the pages hold the sinks and are pages 0 .. of the
+  // row, the others go on at page0 + kept; and the new tokens
+  int kept, news;
 };
+// the table's slot of a sequence's page, both counted from page0
+__device__ __forceinline__ int dec_slot_of(const DecSeq& q, int slot) { return slot - q.page0 < q.kept ? slot - q.page0 : slot; }
+template <bool SEEN>
 __device__ __forceinline__ DecSeq dec_seq(const Kv4Dev& kv, const AttnArgs& a, int s, int tile_rows) {
   DecSeq q;
+  q.kept = q.news = 0;
   const int b = max(0, a.start[s]), e = min(a.tokens, a.start[s + 1]), len = kv.len[s];
   const int news = max(0, e - b);
   q.begin = b;
   q.pos0 = len - news;
   q.rows = min(news, a.max_new) * a.share;
   q.tiles = (q.rows + tile_rows - 1) / tile_rows;
-  const int first = a.window > 0 ? max(0, q.pos0 - a.window + 1) : 0;
+  // (a row of a tree may see none of the drafted tokens)
+  const int first = a.window > 0 ? max(0, q.pos0 - a.window + (SEEN && a.mask ? 0 : 1)) : 0;
   q.page0 = first / kKv4Page;
+  if (SEEN) {
+    q.news = news;
+    q.kept = min((min(a.sinks, len) + kKv4Page - 1) / kKv4Page, q.page0);
+    if (q.kept == q.page0) q.kept = 0, q.page0 = 0;  // no gap
+    q.page0 -= q.kept;
+  }
   // one page past the row at most: it is reported there
   q.pages = len > 0 ? min((len - 1) / kKv4Page, kv.max_pages) - q.page0 + 1 : 0;
   q.empty = q.pages <= 0;
   if (q.empty) {
     q.pages = 1;
-    q.page0 = 0;
+    q.page0 = q.kept = 0;
   }
   if (q.rows == 0) q.pages = q.tiles = 0;
   return q;
@@ -258,7 +315,7 @@ __device__ __forceinline__ void dec_join(const AttnArgs& a, int e, int n, At at,
   }
 }
 
-template <typename T, int D, int G, int RT, bool SMALL>
+template <typename T, int D, int G, int RT, bool SMALL, bool SEEN>
 __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShape<D, G, RT, SMALL>::ctas)
     k_kv4_decode(Kv4Dev kv, AttnArgs a) {
   using Shape = DecShape<D, G, RT, SMALL>;
@@ -316,7 +373,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
   for (int s0 = 0; s0 < kv.seqs; s0 += THREADS) {
     const int s = s0 + (int)threadIdx.x;
     DecSeq q = {};
-    if (s < kv.seqs) q = dec_seq(kv, a, s, ROWS);
+    if (s < kv.seqs) q = dec_seq<SEEN>(kv, a, s, ROWS);
     long long total;
     const long long first = scan((long long)q.pages * q.tiles, &total);
     if (s0 == 0) {
@@ -338,7 +395,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
     long long first = first0;
     if (s0 > 0 || kv.seqs > THREADS) {
       q = DecSeq{};
-      if (s < kv.seqs) q = dec_seq(kv, a, s, ROWS);
+      if (s < kv.seqs) q = dec_seq<SEEN>(kv, a, s, ROWS);
       long long total;
       first = before + scan((long long)q.pages * q.tiles, &total);
       before += total;
@@ -376,7 +433,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
       seg = 0;
       do {
         ++s;
-        if (s < kv.seqs) q = dec_seq(kv, a, s, ROWS);
+        if (s < kv.seqs) q = dec_seq<SEEN>(kv, a, s, ROWS);
       } while (s < kv.seqs && q.pages == 0);
     }
     put(c, s, seg, q);
@@ -395,6 +452,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
     ld_base = q.empty ? nullptr : kv4_block(kv, rank, a.layer, 0, rh - rank * kv.heads, BLK);
   };
   uint32_t missing = 0;  // stages that hold no page
+  auto page_at = [&](int slot) { return kv4_page(kv, ldc.s, SEEN ? dec_slot_of(ldc.q, slot) : slot); };
   auto issue = [&](int st) {
     if (ld_slot == ld_end) {
       const int s = ldc.s;
@@ -406,11 +464,11 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
     if (ld_base) {
       if (ids_at < 0 || ld_slot - ids_at >= 32) {
         ids_at = ld_slot;
-        ids = ids_at + lane < ld_end ? kv4_page(kv, ldc.s, ids_at + lane) : -1;
+        ids = ids_at + lane < ld_end ? page_at(ids_at + lane) : -1;
       }
       if (ld_slot < ids_at) {  // the next segment of the same sequence starts over
         ids_at = ld_slot;
-        ids = ids_at + lane < ld_end ? kv4_page(kv, ldc.s, ids_at + lane) : -1;
+        ids = ids_at + lane < ld_end ? page_at(ids_at + lane) : -1;
       }
       page = __shfl_sync(0xffffffffu, ids, ld_slot - ids_at);
     }
@@ -441,6 +499,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
   float qsum[RT][NG][2], mx[RT][2], l[RT][2], pmid[RT][NG][2], cs[RT][2];
   float o[RT][MT][4];
   int ex = kMinExp, lim_hi[RT][2], lim_lo[RT][2], tile_hi = 0, tile_lo = 0, tile_end = 0;
+  int row_at[RT][2];  // SEEN: the rows' tokens of the batch
   auto open = [&]() {
     const DecSeq sq = cuc.q;
     const int rh = cuc.seg / sq.tiles, tile = cuc.seg - rh * sq.tiles, rank = rh / kv.heads, head = rh - rank * kv.heads;
@@ -451,7 +510,12 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
       const bool in = row < sq.rows;
       const T* q = static_cast<const T*>(a.q[rank]) + (size_t)(sq.begin + tok) * a.q_stride +
                    (size_t)(head * a.share + row - tok * a.share) * D;
-      const int hi = in ? sq.pos0 + tok : -1, lo = a.window > 0 ? sq.pos0 + tok - a.window + 1 : 0;
+      int hi = in ? sq.pos0 + tok : -1, lo = a.window > 0 ? sq.pos0 + tok - a.window + 1 : 0;
+      if (SEEN && a.mask) {
+        const SeenRow r = seen_row(a, sq.pos0, in ? sq.news : 0, tok, sq.begin + tok);
+        hi = in ? r.hi : -1;
+        lo = in ? r.lo : -(1 << 30);  // (not among the tile's largest)
+      }
       uint4 v[JW];
       float big = 0.0f;
 #pragma unroll
@@ -501,6 +565,7 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
         cs[x][b] = __shfl_sync(0xffffffffu, c, src);
         lim_hi[x][b] = __shfl_sync(0xffffffffu, hi, src);
         lim_lo[x][b] = __shfl_sync(0xffffffffu, lo, src);
+        if (SEEN) row_at[x][b] = __shfl_sync(0xffffffffu, in ? sq.begin + tok : -1, src);
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           qsum[x][gr][b] = __shfl_sync(0xffffffffu, qs[gr], src);
@@ -520,6 +585,16 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
     tile_hi = sq.pos0 + tile * ROWS / a.share;
     tile_end = sq.pos0 + last / a.share;
     tile_lo = a.window > 0 ? tile_end - a.window + 1 : 0;
+    if (SEEN && a.mask) {
+      tile_hi = sq.pos0 - 1;
+      tile_end = sq.pos0 + sq.news - 1;
+      if (a.window > 0) {
+        tile_lo = lim_lo[0][0];
+#pragma unroll
+        for (int x = 0; x < RT; ++x) tile_lo = max(tile_lo, max(lim_lo[x][0], lim_lo[x][1]));
+        tile_lo = __reduce_max_sync(0xffffffffu, tile_lo);
+      }
+    }
   };
 
   // One page.  MASKED: some row does not see some key of it.
@@ -533,6 +608,19 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
     const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D)) + kg * NG;
     const uint32_t* vpar = par + kKv4Page * NG;
     float sc[4][RT][4];
+    uint32_t vis[RT][2][2];  // SEEN: the page's keys that the rows see
+    if constexpr (MASKED && SEEN) {
+#pragma unroll
+      for (int x = 0; x < RT; ++x)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const bool tree = a.mask && row_at[x][b] >= 0;
+          const SeenRow r = {lim_hi[x][b], lim_lo[x][b], cuc.q.pos0, cuc.q.news,
+                             tree ? a.mask + (size_t)row_at[x][b] * a.words : nullptr};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) vis[x][b][i] = seen_word(r, a, key0 + 32 * i) >> kg;
+        }
+    }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {  // 16 keys each
       uint32_t w[2][JW];
@@ -576,7 +664,9 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
             for (int gr = 1; gr < NG; ++gr) s = fmaf(sl[gr].y, qsum[x][gr][b], s);
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) s = fmaf(sl[gr].x, acc[x][gr][2 * h + b], s);
-            if (MASKED) {
+            if (MASKED && SEEN) {
+              if (!((vis[x][b][n >> 1] >> (16 * (n & 1) + 8 * h)) & 1u)) s = -INFINITY;
+            } else if (MASKED) {
               const int pos = key0 + 16 * n + 8 * h + kg;
               if (pos > lim_hi[x][b] || pos < lim_lo[x][b]) s = -INFINITY;
             }
@@ -814,6 +904,8 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
     long long seg_begin;  // first unit of the open segment
     int left;             // its units still to come
     int key0;             // first key of its next page
+    int slot = 0;         // SEEN: that page, counted from the sequence's page0
+    auto slot_key = [&]() { return dec_slot_of(cuc.q, slot) * kKv4Page; };
     {
       const int j = s_page[warp];
       const DecSeq q = ldc.q;
@@ -822,6 +914,10 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
       seg_begin = u0 - j;
       left = q.pages - j;
       key0 = (q.page0 + j) * kKv4Page;
+      if (SEEN) {
+        slot = q.page0 + j;
+        key0 = slot_key();
+      }
     }
     int issued = 0;
     for (; issued < S && issued < count; ++issued) issue(issued);
@@ -839,7 +935,8 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
       }
       if (!((missing >> st) & 1u)) {
         const char* blk = ring + (size_t)st * BLK;
-        if (key0 + kKv4Page - 1 > tile_hi || key0 < tile_lo) page_pass(std::true_type{}, blk, key0);
+        if (key0 + kKv4Page - 1 > tile_hi || (key0 < tile_lo && !(SEEN && key0 + kKv4Page <= a.sinks)))
+          page_pass(std::true_type{}, blk, key0);
         else page_pass(std::false_type{}, blk, key0);
       }
       __syncwarp();  // every lane has read the stage
@@ -848,6 +945,10 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
         ++issued;
       }
       key0 += kKv4Page;
+      if (SEEN) {
+        ++slot;
+        key0 = slot_key();
+      }
       const bool ends = --left == 0;
       if (ends || i + 1 == count) {  // the segment, or the range, ends
         settle();
@@ -873,6 +974,10 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
           next_segment(cuc);
           left = cuc.q.pages;
           key0 = cuc.q.page0 * kKv4Page;
+          if (SEEN) {
+            slot = cuc.q.page0;
+            key0 = slot_key();
+          }
           fresh = true;
         }
       }

@@ -1,5 +1,5 @@
 // kv4_pages.cu -- the pages of the 4-bit cache: giving them out, sharing,
-// copying, compacting and freeing them.
+// copying, compacting and freeing them, and keeping accepted drafted tokens.
 //
 // All bookkeeping is whole numbers in device memory, and the outcome does not
 // depend on timing: free pages are taken lowest first and requests are served
@@ -421,6 +421,173 @@ __global__ void __launch_bounds__(kCopyThreads) k_kv4_copy(Kv4Dev kv, CopyArgs a
   }
 }
 
+// ---- keep: of the drafted tokens of each sequence, the accepted ones move to the
+// front, in all layers and ranks, and the rest is given up.
+//
+// The moves first: a warp for each (sequence, rank, layer, kv head), which looks
+// the path over for itself (a few words), so that no launch comes before the
+// moves.  A row is D/16 vectors of codes and 2 D/G words of parameters, one lane
+// each, several rows at a time.  The path ascends, so a row's place is never
+// past it: a batch of rows is read before any of it is written, and what later
+// batches read lies behind all that was written.  The books follow in a second
+// kernel, which reads what the first one decided.
+struct KeepArgs {
+  const int32_t* start;
+  const int32_t* path;
+  const int32_t* count;
+  int32_t* info;
+  int tokens;
+  PagesWs ws;  // mark[s]: tokens kept, -1: left as it is; pre[s]: tokens moved
+};
+struct KeepSeq {
+  int begin, news, pos0, len, kept, stay;  // stay: accepted tokens in front that are in place already
+  bool ok;
+};
+// One warp's look at a sequence: all lanes call, and get the same.
+__device__ __forceinline__ KeepSeq keep_seq(const Kv4Dev& kv, const KeepArgs& a, int s) {
+  const int lane = threadIdx.x & 31;
+  KeepSeq q;
+  q.begin = max(0, a.start[s]);
+  q.news = max(0, min(a.tokens, a.start[s + 1]) - q.begin);
+  q.len = kv.len[s];
+  q.kept = a.count[s];
+  q.pos0 = q.len - q.news;
+  q.stay = q.kept;
+  q.ok = q.pos0 >= 0 && q.kept >= 0 && q.kept <= q.news && (q.len + kKv4Page - 1) / kKv4Page <= kv.max_pages;
+  if (!q.ok) return q;
+  for (int i0 = 0; i0 < q.kept; i0 += 32) {
+    const int i = i0 + lane, x = i < q.kept ? a.path[q.begin + i] : 0;
+    const int last = i > 0 && i < q.kept ? a.path[q.begin + i - 1] : -1;
+    if (__any_sync(0xffffffffu, i < q.kept && (x <= last || x >= q.news))) {
+      q.ok = false;
+      return q;
+    }
+    const unsigned moves = __ballot_sync(0xffffffffu, i < q.kept && x != i);
+    if (moves && q.stay == q.kept) q.stay = i0 + __ffs(moves) - 1;
+  }
+  if (q.stay < q.kept) {  // pages that are read or written are the pool's, those that are written nobody else's
+    const int first = (q.pos0 + q.stay) / kKv4Page, written = (q.pos0 + q.kept - 1) / kKv4Page;
+    for (int j0 = first; j0 <= (q.len - 1) / kKv4Page; j0 += 32) {
+      const int j = j0 + lane;
+      const bool in = j <= (q.len - 1) / kKv4Page;
+      const int p = in ? kv4_page(kv, s, j) : 0;
+      if (__any_sync(0xffffffffu, in && (p < 0 || (j <= written && ld_count(kv.refs + p) != 1)))) {
+        q.ok = false;
+        return q;
+      }
+    }
+  }
+  return q;
+}
+
+constexpr int kKeepThreads = 256;
+template <int D, int G>
+__global__ void __launch_bounds__(kKeepThreads) k_kv4_keep_move(Kv4Dev kv, KeepArgs a) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kBatch = 2;  // lanes of a row, rows at once, vectors a lane has in flight
+  constexpr int NG = D / G, BLK = kv4_block_bytes(D, G), kHalf = kLanes / 2;
+  pdl_prologue();
+  const int lane = threadIdx.x & 31, v = lane % kLanes, sub = lane / kLanes;
+  const int nh = kv.n * kv.layers * kv.heads;
+  const long long units = (long long)kv.seqs * nh, step = (long long)gridDim.x * (kKeepThreads / 32);
+  for (long long u = (long long)blockIdx.x * (kKeepThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
+    const int s = (int)(u / nh), rest = (int)(u % nh);
+    const KeepSeq q = keep_seq(kv, a, s);
+    if (rest == 0 && lane == 0) {
+      a.ws.mark[s] = q.ok ? q.kept : -1;
+      a.ws.pre[s] = q.ok ? q.kept - q.stay : 0;
+    }
+    if (!q.ok) continue;
+    const int head = rest % kv.heads, layer = rest / kv.heads % kv.layers, rank = rest / kv.heads / kv.layers;
+    for (int i0 = q.stay; i0 < q.kept; i0 += kRows * kBatch) {
+      uint4 codes[kBatch];
+      uint32_t param[kBatch];
+      char* to[kBatch];
+      int tok[kBatch], from[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = i0 + b * kRows + sub;
+        to[b] = nullptr;
+        if (i >= q.kept) continue;
+        const int x = q.pos0 + a.path[q.begin + i], y = q.pos0 + i;
+        from[b] = x % kKv4Page;
+        tok[b] = y % kKv4Page;
+        const int32_t* row = kv.table + (size_t)s * kv.max_pages;
+        const char* src = kv4_block(kv, rank, layer, row[x / kKv4Page], head, BLK);
+        to[b] = kv4_block(kv, rank, layer, row[y / kKv4Page], head, BLK);
+        codes[b] = *reinterpret_cast<const uint4*>(src + (v >= kHalf) * kv4_codes_bytes(D) + from[b] * (D / 2) + v % kHalf * 16);
+        if (v < 2 * NG)
+          param[b] = reinterpret_cast<const uint32_t*>(src + 2 * kv4_codes_bytes(D) +
+                                                       (v >= NG) * kv4_params_bytes(D, G))[from[b] * NG + v % NG];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (!to[b]) continue;
+        // at D = 128, V's chunks lie by bit 2 of the token: a vector is two neighbouring ones
+        const int swap = D == 128 && v >= kHalf ? ((from[b] ^ tok[b]) >> 2 & 1) * 2 : 0;
+        *reinterpret_cast<uint4*>(to[b] + (v >= kHalf) * kv4_codes_bytes(D) + tok[b] * (D / 2) + (v % kHalf ^ swap) * 16) = codes[b];
+        if (v < 2 * NG)
+          reinterpret_cast<uint32_t*>(to[b] + 2 * kv4_codes_bytes(D) +
+                                      (v >= NG) * kv4_params_bytes(D, G))[tok[b] * NG + v % NG] = param[b];
+      }
+      __syncwarp();
+    }
+  }
+}
+
+template <int CTAS>
+__global__ void __launch_bounds__(kBookThreads) k_kv4_keep_book(Kv4Dev kv, KeepArgs a) {
+  __shared__ int smem[32];
+  pdl_prologue();
+  const int cta = (int)blockIdx.x, tid = cta * kBookThreads + (int)threadIdx.x, lane = threadIdx.x & 31;
+  constexpr int kAll = CTAS * kBookThreads;
+  const PagesWs ws = a.ws;
+  for (int i = tid; i < kWsWords; i += kAll) ws.w[i] = 0;
+  book_sync<CTAS>();
+  int fails = 0, moved = 0;
+  for (int s = tid >> 5; s < kv.seqs; s += kAll / 32) {
+    const int kept = ws.mark[s], len = kv.len[s];
+    const int news = max(0, min(a.tokens, a.start[s + 1]) - max(0, a.start[s]));
+    __syncwarp();  // every lane has read the length
+    if (kept < 0) {
+      fails += lane == 0;
+      continue;
+    }
+    const int now = len - news + kept;
+    int32_t* row = kv.table + (size_t)s * kv.max_pages;
+    for (int j = (now + kKv4Page - 1) / kKv4Page + lane; j < (len + kKv4Page - 1) / kKv4Page; j += 32) {
+      const int p = row[j];
+      if (p >= 0 && p < kv.pages) atomicSub(kv.refs + p, 1);
+      else book_bad(kv, s);
+      row[j] = -1;
+    }
+    if (lane == 0) {
+      kv.len[s] = now;
+      moved += ws.pre[s];
+    }
+  }
+  if (!a.info) return;
+  if (fails) atomicAdd(&ws.w[kWsFails], fails);
+  if (moved) atomicAdd(&ws.w[kWsFreed], moved);
+  book_sync<CTAS>();
+  const Span my = my_pages<CTAS>(kv.pages, cta);
+  int mine = 0;
+  for (int p = my.b + (int)threadIdx.x; p < my.e; p += kBookThreads) mine += ld_count(kv.refs + p) == 0;
+  mine = cta_sum(mine, smem);
+  if (threadIdx.x == 0) atomicAdd(&ws.w[kWsTotal], mine);
+  book_sync<CTAS>();
+  if (tid == 0) {
+    a.info[0] = __ldcg(ws.w + kWsTotal);
+    a.info[1] = __ldcg(ws.w + kWsFails);
+    a.info[2] = __ldcg(ws.w + kWsFreed);
+  }
+}
+
+const void* keep_move_kernel(int dim, int group) {
+  if (dim == 128) return group == 64 ? (const void*)&k_kv4_keep_move<128, 64> : (const void*)&k_kv4_keep_move<128, 32>;
+  return group == 64 ? (const void*)&k_kv4_keep_move<64, 64> : (const void*)&k_kv4_keep_move<64, 32>;
+}
+
 const void* kv4_pages_kernel(int i) {
   switch (i) {
     case 0: return (const void*)&k_kv4_book<1>;
@@ -428,6 +595,12 @@ const void* kv4_pages_kernel(int i) {
     case 2: return (const void*)&k_kv4_compact_book<1>;
     case 3: return (const void*)&k_kv4_compact_book<kBookCtas>;
     case 4: return (const void*)&k_kv4_copy;
+    case 5: return (const void*)&k_kv4_keep_book<1>;
+    case 6: return (const void*)&k_kv4_keep_book<kBookCtas>;
+    case 7: return keep_move_kernel(64, 32);
+    case 8: return keep_move_kernel(64, 64);
+    case 9: return keep_move_kernel(128, 32);
+    case 10: return keep_move_kernel(128, 64);
     default: return nullptr;
   }
 }
@@ -553,6 +726,42 @@ int dcc_kv4_fork(const dcc_kv4_t* kv, const int32_t* src, const int32_t* dst, si
                  void* workspace, size_t workspace_bytes, dcc_stream_t s) {
   return book_call(kv, dcc::kBookFork, src, dst, count, info, workspace, workspace_bytes,
                    static_cast<cudaStream_t>(s));
+}
+
+int dcc_kv4_keep(const dcc_kv4_t* kv, const int32_t* start, const int32_t* path, size_t tokens, const int32_t* count,
+                 int32_t* info, void* workspace, size_t workspace_bytes, dcc_stream_t s) {
+  dcc::Kv4Dev d{};
+  dcc::KeepArgs a{};
+  int rc = page_view(kv, true, workspace, workspace_bytes, &d, &a.ws);
+  if (rc != DCC_OK) return rc;
+  if (!start || !count || (tokens && !path) || tokens > (size_t)1 << 26) return DCC_ERR_INVALID_ARG;
+  if (odd_word(start) || odd_word(path) || odd_word(count) || odd_word(info)) return DCC_ERR_MISALIGNED;
+  const size_t seqs = (size_t)kv->seqs * 4;
+  if (!books_apart(kv, workspace, info, {{start, seqs + 4, false}, {path, tokens * 4, false}, {count, seqs, false}}))
+    return DCC_ERR_INVALID_ARG;
+  a.start = start;
+  a.path = path;
+  a.count = count;
+  a.info = info;
+  a.tokens = (int)tokens;
+  if ((rc = dcc_host::kv4_ready(&d)) != DCC_OK) return rc;
+  const void* fn = dcc::keep_move_kernel(kv->head_dim, kv->group);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return DCC_ERR_CUDA;
+  }
+  const int per_sm = dcc_host::max_active_per_sm(fn, dcc::kKeepThreads);
+  if (per_sm < 1) return DCC_ERR_LAUNCH;
+  constexpr long long kWarps = dcc::kKeepThreads / 32;
+  const long long units = (long long)kv->seqs * kv->n_ranks * kv->layers * kv->kv_heads, ctas = (units + kWarps - 1) / kWarps;
+  const int grid = (int)(ctas < (long long)sms * per_sm ? ctas : (long long)sms * per_sm);
+  void* args[] = {&d, &a};
+  cudaStream_t st = static_cast<cudaStream_t>(s);
+  rc = launch(fn, grid, dcc::kKeepThreads, false, args, st, 0, true);
+  if (rc != DCC_OK) return rc;
+  return launch_book(5, kv->pages, args, st);
 }
 
 int dcc_kv4_copy(const dcc_kv4_t* kv, const int32_t* src, const int32_t* dst, size_t count, dcc_stream_t s) {

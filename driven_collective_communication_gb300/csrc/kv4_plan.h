@@ -33,6 +33,15 @@ struct AttnPlan {
   bool small;
 };
 
+// Row tiles of the streaming kernel: as few passes over the cache as the registers
+// allow, then the fewest rows that make that many.
+inline void stream_plan(AttnPlan* p, long long n_heads, long long seqs, long long max_pages, int dim, long long rows,
+                        long long sms) {
+  const long long most = dim == 64 ? 3 : 2, times = (rows + 8 * most - 1) / (8 * most);
+  p->tiles = (int)((rows + 8 * times - 1) / (8 * times));
+  p->small = rows <= 8 && n_heads * seqs * max_pages <= sms * kDecSmallWarps;
+}
+
 inline AttnPlan attn_plan(long long n_heads /* ranks x kv heads */, long long seqs, long long max_pages, int dim,
                           long long share, long long tokens, long long max_new, long long sms) {
   AttnPlan p = {};
@@ -55,11 +64,7 @@ inline AttnPlan attn_plan(long long n_heads /* ranks x kv heads */, long long se
     p.wide = wide;
     return p;
   }
-  // Row tiles: as few passes over the cache as the registers allow, then the
-  // fewest rows that make that many.
-  const long long most = dim == 64 ? 3 : 2, times = (rows + 8 * most - 1) / (8 * most);
-  p.tiles = (int)((rows + 8 * times - 1) / (8 * times));
-  p.small = rows <= 8 && n_heads * seqs * max_pages <= sms * kDecSmallWarps;
+  stream_plan(&p, n_heads, seqs, max_pages, dim, rows, sms);
   return p;
 }
 

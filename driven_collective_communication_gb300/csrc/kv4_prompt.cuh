@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   const int nh = kv.n * kv.heads, per = nh * kv.seqs;
   const int turn = (int)blockIdx.x / per, rest = (int)blockIdx.x % per, seq = rest / nh, rh = rest % nh;
   const int rank = rh / kv.heads, head = rh % kv.heads;
-  const DecSeq q = dec_seq(kv, a, seq, kPromptRows);
+  const DecSeq q = dec_seq<false>(kv, a, seq, kPromptRows);
   // a.wide tiles of 256 rows from the last row down, then tiles of 128
   const int past = min(turn, a.wide), row_hi = q.rows - kPromptRows * past - 128 * (turn - past);
   if (row_hi <= 0) return;

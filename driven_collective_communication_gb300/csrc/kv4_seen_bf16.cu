@@ -1,0 +1,7 @@
+// kv4_seen_bf16.cu -- the attention's kernels over bf16 caches for rows with sets of
+// seen keys of their own: trees of drafted tokens, windows with sinks.
+#include "kv4_attention.cuh"
+
+namespace dcc {
+AttnKernel attn_seen_kernel_bf16(int dim, int group, int which) { return attn_kernel_for<__nv_bfloat16, true>(dim, group, which); }
+}  // namespace dcc

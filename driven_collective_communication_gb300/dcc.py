@@ -56,6 +56,8 @@ ALGO_CODES = {"auto": DCC_ALGO_AUTO, "one_shot": DCC_ALGO_ONE_SHOT, "two_shot": 
               "two_shot_scratch": DCC_ALGO_TWO_SHOT_SCRATCH, "two_shot_bulk": DCC_ALGO_TWO_SHOT_BULK,
               "one_shot_ll": DCC_ALGO_ONE_SHOT_LL}
 DCC_KV4_PAGE = 64
+DCC_TREE_MAX = 1024
+DCC_TOP_MAX = 64
 ACT_CODES = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 KIND_CODES = {"input": DCC_BUF_INPUT, "output": DCC_BUF_OUTPUT, "scratch": DCC_BUF_SCRATCH}
 
@@ -125,13 +127,18 @@ _SIGS = {
     "dcc_kv4_read": [_KV, _i, _PP, _PP, _sz, _sz, _vp, _vp],
     "dcc_kv4_attention": [_KV, _i, _PP, _PP, _PP, _i, _sz, _sz, _vp, _i, _f32, _i, _vp, _sz, _vp],
     "dcc_kv4_attention_workspace": [_KV, _i, ctypes.POINTER(_sz)],
+    "dcc_kv4_attention_sinks": [_KV, _i, _PP, _PP, _PP, _i, _sz, _sz, _vp, _i, _f32, _i, _i, _vp, _sz, _vp],
+    "dcc_kv4_attention_tree": [_KV, _i, _PP, _PP, _PP, _i, _sz, _sz, _vp, _i, _vp, _i, _f32, _i, _i, _vp, _sz, _vp],
     "dcc_kv4_pages_workspace": [_KV, ctypes.POINTER(_sz)],
     "dcc_kv4_reserve": [_KV, _vp, _vp, _vp, _sz, _vp],
     "dcc_kv4_free": [_KV, _vp, _sz, _vp, _vp, _sz, _vp],
     "dcc_kv4_fork": [_KV, _vp, _vp, _sz, _vp, _vp, _sz, _vp],
+    "dcc_kv4_keep": [_KV, _vp, _vp, _sz, _vp, _vp, _vp, _sz, _vp],
     "dcc_kv4_copy": [_KV, _vp, _vp, _sz, _vp],
     "dcc_kv4_compact": [_KV, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
     "dcc_linear": [_i, _PP, _PP, _PP, _PP, _PP, _sz, _sz, _sz, _i, _i, _vp],
+    "dcc_token_logprobs": [_i, _PP, _sz, _sz, _sz, _sz, _vp, _f32, _i, _vp, _vp, _vp, _vp, _vp, _sz, _i, _vp],
+    "dcc_token_logprobs_workspace": [_i, _sz, _sz, _i, ctypes.POINTER(_sz)],
     "dcc_local_check": [_vp],
 }
 for _name, _args in _SIGS.items():
@@ -564,9 +571,7 @@ def dcc_kv4_attention_workspace(kv, q_heads):
     return out.value
 
 
-def dcc_kv4_attention(kv, layer, q, out, start, max_new, workspace, lse=None, scale=None, window=0, stream=None):
-    """Causal attention of the batch's rows over the cache (see dcc.h).  scale
-    None: 1 / sqrt(head_dim)."""
+def _attention_args(kv, q, out, lse):
     q, out, lse = _ranks(q), _ranks(out), _ranks(lse)
     tokens, heads = q.shape[0], q.shape[1]
     _same(q, (tokens, heads, kv.head_dim), kv.torch_dtype, kv.n, "q")
@@ -575,10 +580,38 @@ def dcc_kv4_attention(kv, layer, q, out, start, max_new, workspace, lse=None, sc
         _same(lse, (tokens, heads), torch.float32, kv.n, "lse")
     if not out.dense or (lse is not None and not lse.dense):
         raise ValueError("out and lse have dense rows")
-    return _check(_lib.dcc_kv4_attention(kv.ref, layer, q.ptrs, out.ptrs, lse.ptrs if lse else None, heads, tokens,
-                                         q.stride, _index(start, kv.seqs + 1, "start"), max_new,
+    return q.ptrs, out.ptrs, lse.ptrs if lse else None, heads, tokens, q.stride
+
+
+def dcc_kv4_attention(kv, layer, q, out, start, max_new, workspace, lse=None, scale=None, window=0, stream=None):
+    """Causal attention of the batch's rows over the cache (see dcc.h).  scale
+    None: 1 / sqrt(head_dim)."""
+    return _check(_lib.dcc_kv4_attention(kv.ref, layer, *_attention_args(kv, q, out, lse),
+                                         _index(start, kv.seqs + 1, "start"), max_new,
                                          kv.head_dim ** -0.5 if scale is None else scale, window, *_ws(workspace),
                                          _stream(stream)), "dcc_kv4_attention")
+
+
+def dcc_kv4_attention_sinks(kv, layer, q, out, start, max_new, window, sinks, workspace, lse=None, scale=None,
+                            stream=None):
+    """Causal attention with a window whose first `sinks` tokens stay visible."""
+    return _check(_lib.dcc_kv4_attention_sinks(kv.ref, layer, *_attention_args(kv, q, out, lse),
+                                               _index(start, kv.seqs + 1, "start"), max_new,
+                                               kv.head_dim ** -0.5 if scale is None else scale, window, sinks,
+                                               *_ws(workspace), _stream(stream)), "dcc_kv4_attention_sinks")
+
+
+def dcc_kv4_attention_tree(kv, layer, q, out, start, mask, max_new, workspace, lse=None, scale=None, window=0, sinks=0,
+                           stream=None):
+    """Attention of drafted tokens that see the context and what their masks name:
+    mask int32 (tokens, words), bit j of a row's words for drafted token j."""
+    args = _attention_args(kv, q, out, lse)
+    if mask.dim() != 2 or mask.shape[0] != args[4]:
+        raise ValueError("mask: (tokens, words)")
+    return _check(_lib.dcc_kv4_attention_tree(kv.ref, layer, *args, _index(start, kv.seqs + 1, "start"), max_new,
+                                              _index(mask, 0, "mask"), mask.shape[1],
+                                              kv.head_dim ** -0.5 if scale is None else scale, window, sinks,
+                                              *_ws(workspace), _stream(stream)), "dcc_kv4_attention_tree")
 
 
 def dcc_kv4_pages_workspace(kv):
@@ -613,6 +646,13 @@ def dcc_kv4_fork(kv, src, dst, workspace, info=None, stream=None):
                                     *_ws(workspace), _stream(stream)), "dcc_kv4_fork")
 
 
+def dcc_kv4_keep(kv, start, path, count, workspace, info=None, stream=None):
+    """Keep count[s] of each sequence's drafted tokens, those that path names."""
+    return _check(_lib.dcc_kv4_keep(kv.ref, _index(start, kv.seqs + 1, "start"), _index(path, 0, "path"), path.numel(),
+                                    _index(count, kv.seqs, "count"), _info(info), *_ws(workspace), _stream(stream)),
+                  "dcc_kv4_keep")
+
+
 def dcc_kv4_copy(kv, src, dst, stream=None):
     n = dst.numel()
     return _check(_lib.dcc_kv4_copy(kv.ref, _index(src, n, "src"), _index(dst, n, "dst"), n, _stream(stream)),
@@ -623,6 +663,46 @@ def dcc_kv4_compact(kv, new_table, new_refs, remap, workspace, info=None, stream
     return _check(_lib.dcc_kv4_compact(kv.ref, _index(new_table, kv.seqs * kv.max_pages, "new_table"),
                                        _index(new_refs, kv.pages, "new_refs"), _index(remap, kv.pages, "remap"),
                                        _info(info), *_ws(workspace), _stream(stream)), "dcc_kv4_compact")
+
+
+def dcc_token_logprobs_workspace(n_ranks, tokens, columns, top):
+    out = _sz()
+    _check(_lib.dcc_token_logprobs_workspace(n_ranks, tokens, columns, top, ctypes.byref(out)),
+           "dcc_token_logprobs_workspace")
+    return out.value
+
+
+def token_logprobs_workspace(n_ranks, tokens, columns, top, device="cuda"):
+    """A workspace for dcc_token_logprobs (zeroed once; one per concurrent call)."""
+    return torch.zeros(dcc_token_logprobs_workspace(n_ranks, tokens, columns, top), dtype=torch.uint8, device=device)
+
+
+def _vector(t, dtype, shape, what):
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError("%s: a contiguous %s CUDA tensor of shape %s" % (what, dtype, tuple(shape)))
+    return t.data_ptr()
+
+
+def dcc_token_logprobs(logits, target, logprob, workspace, entropy=None, top_ids=None, top_logprobs=None, vocab=None,
+                       scale=1.0, stream=None):
+    """Log probabilities of the target tokens under vocabulary-parallel logits
+    (one (tokens, columns) tensor a rank), entropy and the most likely tokens
+    (top_ids int32 and top_logprobs, (tokens, top)).  vocab None: all columns."""
+    logits = _ranks(logits)
+    if len(logits.shape) != 2:
+        raise ValueError("logits: (tokens, columns) a rank")
+    tokens, columns = logits.shape
+    top = 0 if top_ids is None else top_ids.shape[-1]
+    ids, lps = (_vector(top_ids, torch.int32, (tokens, top), "top_ids"),
+                _vector(top_logprobs, torch.float32, (tokens, top), "top_logprobs")) if top else (None, None)
+    return _check(_lib.dcc_token_logprobs(len(logits), logits.ptrs, tokens, columns, logits.stride,
+                                          columns * len(logits) if vocab is None else vocab,
+                                          _vector(target, torch.int32, (tokens,), "target"), scale, top,
+                                          _vector(logprob, torch.float32, (tokens,), "logprob"),
+                                          _vector(entropy, torch.float32, (tokens,), "entropy"), ids, lps,
+                                          *_ws(workspace), _dtype(logits.dtype), _stream(stream)), "dcc_token_logprobs")
 
 
 def prepare_allreduce(comm, send, recv, count, dtype, algo="auto", stream=None):
@@ -775,6 +855,17 @@ class Kv4Cache:
 
     def attention(self, q, out, start, max_new, workspace, lse=None, scale=None, window=0, layer=0, stream=None):
         dcc_kv4_attention(self, layer, q, out, start, max_new, workspace, lse, scale, window, stream)
+
+    def attention_sinks(self, q, out, start, max_new, workspace, window, sinks, lse=None, scale=None, layer=0,
+                        stream=None):
+        dcc_kv4_attention_sinks(self, layer, q, out, start, max_new, window, sinks, workspace, lse, scale, stream)
+
+    def attention_tree(self, q, out, start, mask, max_new, workspace, lse=None, scale=None, window=0, sinks=0, layer=0,
+                       stream=None):
+        dcc_kv4_attention_tree(self, layer, q, out, start, mask, max_new, workspace, lse, scale, window, sinks, stream)
+
+    def keep(self, start, path, count, workspace, info=None, stream=None):
+        dcc_kv4_keep(self, start, path, count, workspace, info, stream)
 
     def reserve(self, add, workspace, info=None, stream=None):
         dcc_kv4_reserve(self, add, workspace, info, stream)

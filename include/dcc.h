@@ -616,6 +616,32 @@ int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* cons
                       void* workspace, size_t workspace_bytes, dcc_stream_t s);
 int dcc_kv4_attention_workspace(const dcc_kv4_t* kv, int q_heads, size_t* bytes);
 
+/* The same with a window whose first tokens stay visible: a row at position x
+ * sees max(0, x - window + 1) .. x and the first min(sinks, x + 1) positions.
+ * Pages that no row sees are not read.  Window 0: all up to x. */
+int dcc_kv4_attention_sinks(const dcc_kv4_t* kv, int layer, void* const* q, void* const* out, float* const* lse,
+                            int q_heads, size_t tokens, size_t q_stride, const int32_t* start, int max_new, float scale,
+                            int window, int sinks, void* workspace, size_t workspace_bytes, dcc_stream_t s);
+
+/* The same for trees of drafted tokens: the batch's rows are their sequences'
+ * drafted tokens, appended to the cache in any order, and a row sees the
+ * context (the positions before the sequence's first drafted token) and the
+ * drafted tokens of its sequence that its mask names, usually its ancestors and
+ * itself: drafted token j where bit j mod 32 of mask[i * mask_words + j / 32] is
+ * set (device, tokens * mask_words words, the row's own token i of the batch).
+ * Bits past the sequence's drafted tokens say nothing.  mask_words * 32 is at
+ * least max_new (or tokens, where they are fewer), at most DCC_TREE_MAX; drafted
+ * tokens past 32 * mask_words are not seen.  With a window, a row that sees c
+ * drafted tokens sees the last max(0, window - c) positions of the context and
+ * its first `sinks`: what a sequential pass over its branch sees, for branches
+ * up to the window's length.  A row that sees nothing gives zeros and lse
+ * -infinity. */
+#define DCC_TREE_MAX 1024
+int dcc_kv4_attention_tree(const dcc_kv4_t* kv, int layer, void* const* q, void* const* out, float* const* lse,
+                           int q_heads, size_t tokens, size_t q_stride, const int32_t* start, int max_new,
+                           const uint32_t* mask, int mask_words, float scale, int window, int sinks, void* workspace,
+                           size_t workspace_bytes, dcc_stream_t s);
+
 /* Page calls: all state is on the device, the lowest free pages are given out
  * first, requests are served in order, so the outcome is the same every time.  Lists of sequences have at
  * most seqs entries, lists of pages at most pages.
@@ -647,6 +673,21 @@ int dcc_kv4_free(const dcc_kv4_t* kv, const int32_t* seqs, size_t count, int32_t
 int dcc_kv4_fork(const dcc_kv4_t* kv, const int32_t* src, const int32_t* dst, size_t count, int32_t* info,
                  void* workspace, size_t workspace_bytes, dcc_stream_t s);
 
+/* Keep the accepted ones of each sequence's drafted tokens, its last start[s+1]
+ * - start[s] (the batch of dcc_kv4_append): count[s] of them (device, seqs),
+ * path[start[s] + i] (device, tokens; i < count[s]), numbered from the first
+ * drafted one and ascending.  Token i of the path moves to place i among the
+ * drafted ones, in all layers and ranks; the others are dropped: the length
+ * shrinks, and a page that is no longer needed returns to the pool with its last
+ * owner.  What lies behind the new length in a page that stays is undefined.  A
+ * sequence is left as it is where count[s] is not in 0 .. its drafted tokens, the
+ * path does not ascend within them, it has more drafted tokens than tokens, or a
+ * row would move into a page that another sequence shares (a path that begins 0,
+ * 1, 2 .. moves nothing up to there).  info: free pages left, sequences left as
+ * they are, tokens moved. */
+int dcc_kv4_keep(const dcc_kv4_t* kv, const int32_t* start, const int32_t* path, size_t tokens, const int32_t* count,
+                 int32_t* info, void* workspace, size_t workspace_bytes, dcc_stream_t s);
+
 /* Copy page src[i] to page dst[i] (device lists, i < count) in all layers and
  * ranks.  No dst may be named twice or be some src. */
 int dcc_kv4_copy(const dcc_kv4_t* kv, const int32_t* src, const int32_t* dst, size_t count, dcc_stream_t s);
@@ -675,6 +716,28 @@ typedef enum { DCC_ACT_NONE = 0, DCC_ACT_RELU = 1, DCC_ACT_GELU = 2, DCC_ACT_GEL
  * from each other and from every other buffer. */
 int dcc_linear(int n_ranks, void* const* weight, void* const* x, void* const* bias, void* const* residual,
                void* const* y, size_t tokens, size_t rows, size_t k, dcc_act_t act, dcc_dtype_t t, dcc_stream_t s);
+
+/* Log probabilities of vocabulary-parallel logits (what a column-parallel output
+ * layer leaves on the ranks): rank r holds the logits of tokens r * columns .. of
+ * the vocabulary, `tokens` rows of `columns` elements, `stride` elements apart
+ * (any alignment of the element); columns from `vocab` on are padding.  With p =
+ * softmax(scale * logits) over the whole vocabulary, per row
+ *   logprob = ln p[target]         target (device, tokens) and logprob NULL, or both given;
+ *                                  a negative target: 0; one past the vocabulary: NaN, recorded
+ *   entropy = -sum p ln p          NULL: not wanted
+ *   top_ids, top_logprob           the `top` most likely tokens (0 .. DCC_TOP_MAX, at most vocab; 0: NULL), most
+ *                                  likely first, equal logits by token number; tokens * top each
+ * in fp32, the same on every run.  A logit of -infinity is a token that cannot
+ * come.  A row that holds a NaN or +infinity, or nothing but -infinity, gives NaN
+ * and ids -1.  scale above 0.  fp32 / fp16 / bf16.  workspace:
+ * dcc_token_logprobs_workspace bytes, 16-byte aligned, filled with zeros once
+ * before its first use (calls leave its counters at zero, whatever their sizes);
+ * calls that may run at the same time need one each. */
+#define DCC_TOP_MAX 64
+int dcc_token_logprobs(int n_ranks, const void* const* logits, size_t tokens, size_t columns, size_t stride, size_t vocab,
+                       const int32_t* target, float scale, int top, float* logprob, float* entropy, int32_t* top_ids,
+                       float* top_logprob, void* workspace, size_t workspace_bytes, dcc_dtype_t t, dcc_stream_t s);
+int dcc_token_logprobs_workspace(int n_ranks, size_t tokens, size_t columns, int top, size_t* bytes);
 
 /* Synchronise the stream and report what the calls of this section recorded
  * on the current device since the last check: DCC_OK, DCC_ERR_BOUNDS (a
