@@ -369,8 +369,8 @@ bool visit_kernels(F&& visit) {
           return false;
     for (int dim = 64; dim <= 128; dim += 64)
       for (int group = 32; group <= 64; group += 32)
-        for (int which = 0; which < 5; ++which)
-          if (!v(dcc::kv4_attention_kernel(fp16, false, dim, group, which)) ||
+        for (int which = 0; which < 6; ++which)
+          if ((which < 5 && !v(dcc::kv4_attention_kernel(fp16, false, dim, group, which))) ||
               !v(dcc::kv4_attention_kernel(fp16, true, dim, group, which)))
             return false;
   }

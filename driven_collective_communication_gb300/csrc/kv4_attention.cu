@@ -25,7 +25,8 @@ extern "C" {
 
 int dcc_kv4_attention_workspace(const dcc_kv4_t* kv, int q_heads, size_t* bytes) {
   if (!kv || !bytes || q_heads < 1 || kv->kv_heads < 1 || q_heads % kv->kv_heads) return DCC_ERR_INVALID_ARG;
-  *bytes = dcc::dec_ws_bytes();
+  const size_t seen = dcc::seen_ws_bytes(kv->head_dim), dec = dcc::dec_ws_bytes();
+  *bytes = seen > dec ? seen : dec;
   return DCC_OK;
 }
 
@@ -136,11 +137,21 @@ int attention_call(const dcc_kv4_t* kv, int layer, void* const* q, void* const* 
   cudaStream_t st = static_cast<cudaStream_t>(s);
   const long long heads = (long long)kv->n_ranks * kv->kv_heads;
   dcc::AttnPlan p = {};
-  if (seen) dcc::stream_plan(&p, heads, kv->seqs, kv->max_pages, kv->head_dim, (long long)max_new * a.share, sms);
+  if (seen) p = dcc::seen_plan(heads, kv->seqs, kv->max_pages, kv->head_dim, (long long)max_new * a.share, sms);
   else p = dcc::attn_plan(heads, kv->seqs, kv->max_pages, kv->head_dim, a.share, (long long)tokens, max_new, sms);
   if (p.prompt) {
     const dcc::AttnKernel k = dcc::attn_kernel(fp16, seen, kv->head_dim, kv->group, dcc::kAttnPrompt);
     if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;
+    if (seen) {
+      int ctas = sms < dcc::kDecMaxCtas ? sms : dcc::kDecMaxCtas;
+      dcc::LocalDev dc = dcc_host::local_dev(d.status);
+      void* args[] = {&d, &a, &dc};
+      rc = dcc_host::launch(k.fn, ctas, k.threads, false, args, st, k.smem, true);
+      if (rc != DCC_OK) return rc;
+      const dcc::AttnKernel j = dcc::attn_kernel(fp16, true, kv->head_dim, kv->group, dcc::kAttnJoin);
+      void* join[] = {&a, &ctas};
+      return dcc_host::launch(j.fn, 4 * ctas, j.threads, false, join, st, 0, true);
+    }
     if (p.wide > (1 << 24)) return DCC_ERR_INVALID_ARG;
     a.wide = (int)p.wide;
     const long long grid = (p.wide + p.narrow) * heads * kv->seqs;

@@ -12,8 +12,8 @@ struct AttnKernel {
   size_t smem;
 };
 // which: 1 to 3 row tiles of the streaming kernel (3: 64-wide heads only), its
-// small form, or the prompt kernel
-constexpr int kAttnPrompt = 0, kAttnSmall = 4;
+// small form, the prompt kernel, or what joins its parts (SEEN)
+constexpr int kAttnPrompt = 0, kAttnSmall = 4, kAttnJoin = 5;
 AttnKernel attn_kernel_bf16(int dim, int group, int which);
 AttnKernel attn_kernel_fp16(int dim, int group, int which);
 AttnKernel attn_seen_kernel_bf16(int dim, int group, int which);
@@ -29,7 +29,8 @@ AttnKernel attn_kernel_of(int which) {
   };
   using No = std::false_type;
   switch (which) {
-    case kAttnPrompt: return {(const void*)&k_kv4_prompt<T, D, G>, kPromptThreads, PromptShape<D, G>::smem};
+    case kAttnPrompt: return {(const void*)&k_kv4_prompt<T, D, G, SEEN>, kPromptThreads, PromptShape<D, G>::smem};
+    case kAttnJoin: return {(const void*)&k_kv4_seen_join<T, D>, kSeenJoinThreads, 0};
     case kAttnSmall: return decode(std::integral_constant<int, 1>{}, std::true_type{});
     case 1: return decode(std::integral_constant<int, 1>{}, No{});
     default: break;

@@ -42,6 +42,15 @@ inline void stream_plan(AttnPlan* p, long long n_heads, long long seqs, long lon
   p->small = rows <= 8 && n_heads * seqs * max_pages <= sms * kDecSmallWarps;
 }
 
+// Rows with sets of seen keys of their own: the prompt kernel splits such calls
+// evenly, so it takes all that need more than one pass of the streaming kernel.
+inline AttnPlan seen_plan(long long n_heads, long long seqs, long long max_pages, int dim, long long rows, long long sms) {
+  AttnPlan p = {};
+  p.prompt = rows > (dim == 64 ? 24 : 16);
+  if (!p.prompt) stream_plan(&p, n_heads, seqs, max_pages, dim, rows, sms);
+  return p;
+}
+
 inline AttnPlan attn_plan(long long n_heads /* ranks x kv heads */, long long seqs, long long max_pages, int dim,
                           long long share, long long tokens, long long max_new, long long sms) {
   AttnPlan p = {};
