@@ -150,7 +150,7 @@ int attention_call(const dcc_kv4_t* kv, int layer, void* const* q, void* const* 
       if (rc != DCC_OK) return rc;
       const dcc::AttnKernel j = dcc::attn_kernel(fp16, true, kv->head_dim, kv->group, dcc::kAttnJoin);
       void* join[] = {&a, &ctas};
-      return dcc_host::launch(j.fn, 4 * ctas, j.threads, false, join, st, 0, true);
+      return dcc_host::launch(j.fn, 3 * ctas, j.threads, false, join, st, 0, true);
     }
     if (p.wide > (1 << 24)) return DCC_ERR_INVALID_ARG;
     a.wide = (int)p.wide;

@@ -233,8 +233,10 @@ __device__ __forceinline__ bool seen_next(const Kv4Dev& kv, const AttnArgs& a, S
 struct SeenJoin {
   int parts, rank, head, row_lo, row_hi, begin, pad[2];
 };
+constexpr int kSeenRing = 4;  // pieces known at a time
 constexpr int kSeenJoinBytes = kDecMaxCtas * (int)sizeof(SeenJoin);
-// floats of a partial: reference and l of each row, then O
+// floats of a partial: reference and l of each row, then O, four channels of all rows
+// after the other (a warp holds 32 rows and writes whole lines)
 __host__ __device__ constexpr size_t seen_part(int dim) { return (size_t)kPromptRows * (dim + 2); }
 __host__ __device__ constexpr size_t seen_ws_bytes(int dim) {
   return 1024 + kSeenJoinBytes + 2 * kDecMaxCtas * seen_part(dim) * 4;
@@ -256,9 +258,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   // bf16 cache, by step and page: 1 where a key of K has its own scale, 2 where V stays bf16
   __shared__ __align__(2) uint8_t s_range[8][2];
   __shared__ int8_t s_exp[4][128];  // by step: K's powers of two
-  // SEEN: each warp walks along the pieces by itself; those that make P look one ahead
-  __shared__ SeenWalk s_walk[SEEN ? 16 : 1];
-  __shared__ PromptPiece s_piece[SEEN ? 24 : 1];
+  // SEEN: the pieces, found by the warp that loads, ahead of the others.  The last
+  // one is marked: row_hi 0.
+  __shared__ SeenWalk s_walk;
+  __shared__ PromptPiece s_piece[kSeenRing];
+  __shared__ __align__(8) uint64_t s_piece_bars[2 * kSeenRing];
+  auto piece_full = [&](int k) { return smem_addr_u32(&s_piece_bars[k % kSeenRing]); };
+  auto piece_free = [&](int k) { return smem_addr_u32(&s_piece_bars[kSeenRing + k % kSeenRing]); };
   const uint32_t base = (smem_addr_u32(prompt_raw) + 1023u) & ~1023u;
   const uint32_t sq = base, sk = sq + 2 * Shape::q_tile, sv = sk + 2 * Shape::kv_tile, raw = sv + 2 * Shape::kv_tile;
   unsigned char* raw_g_rw = prompt_raw + (raw - smem_addr_u32(prompt_raw));
@@ -289,6 +295,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       mma_mbar_init(two(pvDone, i), 1);
       mma_mbar_init(two(qFull, i), 4);
     }
+    if (SEEN)
+      for (int i = 0; i < kSeenRing; ++i) {
+        mma_mbar_init(piece_full(i), 1);
+        mma_mbar_init(piece_free(i), FP16 ? 13 : 15);  // one each from the warps that read it
+      }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
@@ -350,7 +361,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       if (mine && first * nh <= c0 && c0 < (first + mine) * nh) {
         const int steps = seen_tile_steps(a, dec_seq<true>(kv, a, s, kPromptRows));
         const long long in = c0 - first * nh;
-        for (int w = 0; w < 16; ++w) s_walk[w] = SeenWalk{c0, c1, units, C, s, (int)(in / steps), (int)(in % steps)};
+        s_walk = SeenWalk{c0, c1, units, C, s, (int)(in / steps), (int)(in % steps)};
       }
     }
   } else {
@@ -402,20 +413,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
     if constexpr (!SEEN) {
       return work(one, 0);
     } else {
-      for (int done = 0;;) {
-        bool more = true;
-        if (whole_warp) {
-          __syncwarp();
-          if (lane == 0) more = seen_next(kv, a, s_walk[warp], s_piece[warp]);
-          more = __shfl_sync(0xffffffffu, (int)more, 0) != 0;
-          __syncwarp();
-        } else {
-          more = seen_next(kv, a, s_walk[warp], s_piece[warp]);
-        }
-        if (!more) return true;
-        const PromptPiece& p = s_piece[warp];
+      for (int k = 0, done = 0;; ++k) {
+        if (!wait(piece_full(k), k / kSeenRing)) return false;
+        const PromptPiece& p = s_piece[k % kSeenRing];
+        if (p.row_hi == 0) return true;
         if (!work(p, done)) return false;
         done += p.j1 - p.j0;
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) mbar_arrive(piece_free(k));
       }
     }
   };
@@ -424,7 +429,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
 
   if (warp == 0) {  // ---- loads
     int unfinished = 0;
-    pieces(true, [&](const PromptPiece& pc, int before) {
+    auto load = [&](const PromptPiece& pc, int before) {
     int ids = -1, ids_at = -(1 << 30);
     const int ahead = 2 * (before - pc.j0);  // of the ring, against the tile's pages
     for (int v = 2 * pc.j0; v < 2 * pc.j1; ++v) {
@@ -449,7 +454,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       ++unfinished;
     }
     return true;
-    });
+    };
+    if constexpr (!SEEN) {
+      load(one, 0);
+    } else {
+      // Piece k + 1 is made known before piece k's pages are asked for.  A slot of the
+      // ring is free once piece k + 1 - kSeenRing has been worked off, whose pages
+      // have been loaded.
+      auto publish = [&](int k) {
+        if (k >= kSeenRing && !wait(piece_free(k), k / kSeenRing - 1)) return false;
+        if (lane == 0) {
+          PromptPiece& p = s_piece[k % kSeenRing];
+          if (!seen_next(kv, a, s_walk, p)) p.row_hi = 0;
+          mbar_arrive(piece_full(k));
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = publish(0);
+      for (int k = 0, before = 0; ok; ++k) {
+        const PromptPiece pc = s_piece[k % kSeenRing];
+        if (pc.row_hi == 0) break;
+        ok = publish(k + 1) && load(pc, before);
+        before += pc.j1 - pc.j0;
+      }
+    }
     // a copy in flight when a wait gave up ends before the CTA does
     for (int p = max(0, unfinished - R); p < unfinished; ++p) local_drain(rawf(p % R), (uint32_t)(p / R) & 1u);
   } else if (warp == 1) {  // ---- MMAs
@@ -793,39 +822,52 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
     // Q into its tile, channels in the codes' order, with the scale's sign; returns
     // what scores are multiplied with
     auto load_q = [&](const PromptPiece& pc) {
-      const int row = pc.row_lo + 128 * g + r;
-      const bool in = row < pc.row_hi;
-      const int tok = row / a.share, gh = row - tok * a.share;
-      float c = fabsf(a.scale) * 1.44269504088896341f;
-      const T* src = static_cast<const T*>(a.q[pc.rank]) + (size_t)(pc.begin + tok) * a.q_stride +
-                     (size_t)(pc.head * a.share + gh) * D;
-      const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-      const uint32_t dst = sq + (uint32_t)(g * Shape::q_tile) + (uint32_t)r * 128u;
-      float f = 1.0f;
-      if constexpr (!FP16) {  // a bf16 row as fp16: its largest value goes to 2^8 .. 2^9, exactly
-        uint32_t top = 0;
-#pragma unroll 4
-        for (int u = 0; u < D / 8; ++u) {
-          const uint4 v = in ? *reinterpret_cast<const uint4*>(src + 8 * u) : make_uint4(0, 0, 0, 0);
-          top = __vmaxu2(__vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu)),
-                         v.w & 0x7fff7fffu);
-        }
-        top = max(top & 0xffffu, top >> 16);
-        const int e = top ? max(-100, min(119, (int)(top >> 7) - 127 - 8)) : 0;
-        f = power2(-e);
-        c *= power2(e);
-      }
-      auto half = [&](uint32_t w) {  // two values
-        if constexpr (FP16) return w ^ flip;
-        const float2 x = param_floats(w);
-        return Half16<__half>::narrow2(x.x * f, x.y * f) ^ flip;
-      };
+      // Neighbouring lanes take a row's 16-byte units, so that a load touches a few
+      // lines rather than 32; all loads are in flight at once.
+      constexpr int UPR = D / 8, RPI = 32 / UPR;
+      const int row = pc.row_lo + 128 * g + r, tok = row / a.share, gh = row - tok * a.share;
+      const long long own = row < pc.row_hi
+                                ? (long long)((size_t)(pc.begin + tok) * a.q_stride + (size_t)(pc.head * a.share + gh) * D)
+                                : -1;
+      const T* src = static_cast<const T*>(a.q[pc.rank]);
+      const int u = lane % UPR, sub = lane / UPR;
+      uint4 v[UPR];
 #pragma unroll
-      for (int u = 0; u < D / 8; ++u) {
-        const uint4 v = in ? *reinterpret_cast<const uint4*>(src + 8 * u) : make_uint4(0, 0, 0, 0);
-        const uint4 o = make_uint4(half(__byte_perm(v.x, v.z, 0x5410)), half(__byte_perm(v.x, v.z, 0x7632)),
-                                   half(__byte_perm(v.y, v.w, 0x5410)), half(__byte_perm(v.y, v.w, 0x7632)));
-        sts128(dst + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (r & 7)) * 16), o);
+      for (int i = 0; i < UPR; ++i) {
+        const long long at = __shfl_sync(0xffffffffu, own, i * RPI + sub);
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (at >= 0)
+          asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                       : "l"(src + at + 8 * u));
+      }
+      float c = fabsf(a.scale) * 1.44269504088896341f;
+      const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+      for (int i = 0; i < UPR; ++i) {
+        float f = 1.0f;
+        if constexpr (!FP16) {  // a bf16 row as fp16: its largest value goes to 2^8 .. 2^9, exactly
+          uint32_t top = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                  __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+          top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+          for (int m = UPR / 2; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+          const int e = top ? max(-100, min(119, (int)(top >> 7) - 127 - 8)) : 0;
+          f = power2(-e);
+          const int mine = __shfl_sync(0xffffffffu, e, lane % RPI * UPR);
+          if (lane / RPI == i) c *= power2(mine);
+        }
+        auto half = [&](uint32_t w) {  // two values
+          if constexpr (FP16) return w ^ flip;
+          const float2 x = param_floats(w);
+          return Half16<__half>::narrow2(x.x * f, x.y * f) ^ flip;
+        };
+        const uint4 o = make_uint4(half(__byte_perm(v[i].x, v[i].z, 0x5410)), half(__byte_perm(v[i].x, v[i].z, 0x7632)),
+                                   half(__byte_perm(v[i].y, v[i].w, 0x5410)), half(__byte_perm(v[i].y, v[i].w, 0x7632)));
+        const int x = quad * 32 + i * RPI + sub;
+        sts128(sq + (uint32_t)(g * Shape::q_tile) + (uint32_t)x * 128u + (uint32_t)(u / 8) * 16384u +
+                   (uint32_t)(((u % 8) ^ (x & 7)) * 16),
+               o);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -997,7 +1039,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           part[at] = any || l != 0.0f ? ref : -INFINITY;  // (NaN is seen)
           part[kPromptRows + at] = l;
         }
-        float* dst = part + 2 * kPromptRows + (size_t)at * D;
+        float* dst = part + 2 * kPromptRows + 4 * at;
         if (some)
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 16) {
@@ -1007,11 +1049,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
             if (in && ok)
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<uint4*>(dst + c0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                *reinterpret_cast<uint4*>(dst + (size_t)(c0 + i) * kPromptRows) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         return ok;
       }
       const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
+      const bool wide_out = (reinterpret_cast<uintptr_t>(a.out[pc.rank]) & 31u) == 0;
       const size_t at = (size_t)(pc.begin + tok) * a.q_heads + pc.head * a.share + gh;
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 16) {
@@ -1025,8 +1068,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         }
         if (in && ok) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out[pc.rank]) + at * D + c0);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          if (SEEN && wide_out) {  // each store of a warp touches 32 lines: half as many
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                         "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+          } else {
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
         }
       }
       if (in && ok && a.lse[pc.rank])
@@ -1038,36 +1087,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
     } else {
       // the next piece's Q is loaded before this one's results are written
       SeenJoin join = {};
-      int before = 0, had = 0, at = 0;
-      float c = 0.0f, c_next = 0.0f;
-      auto fetch = [&](int to_slot) {
-        PromptPiece& p = s_piece[to_slot ? 10 + warp : warp];  // warps 6 .. 13: slots 16 .. 23 are their second ones
-        __syncwarp();
-        bool more = true;
-        if (lane == 0) more = seen_next(kv, a, s_walk[warp], p);
-        more = __shfl_sync(0xffffffffu, (int)more, 0) != 0;
-        __syncwarp();
-        if (more && mine(p)) c_next = load_q(p);
-        return more;
+      float c_next = 0.0f;
+      bool ok = true;
+      auto fetch = [&](int k) {
+        if (!(ok = wait(piece_full(k), k / kSeenRing))) return;
+        const PromptPiece& p = s_piece[k % kSeenRing];
+        if (p.row_hi > 0 && mine(p)) c_next = load_q(p);
       };
-      bool more = fetch(0);
-      while (more) {
-        const PromptPiece& pc = s_piece[at ? 10 + warp : warp];
+      fetch(0);
+      for (int k = 0, before = 0, had = 0; ok; ++k) {
+        const PromptPiece& pc = s_piece[k % kSeenRing];
+        if (pc.row_hi == 0) break;
         if (pc.parts) join = SeenJoin{pc.parts, pc.rank, pc.head, pc.row_lo, pc.row_hi, pc.begin, {0, 0}};
-        c = c_next;
-        bool fetched = false;
-        const bool rows = pc.row_hi - pc.row_lo > 128 * g;
-        bool ok = true;
-        if (rows)
-          ok = piece(pc, before, had, c, [&] {
-            more = fetch(at ^ 1);
-            fetched = true;
-          });
-        if (!ok) break;
-        if (!fetched) more = fetch(at ^ 1);
-        before += pc.j1 - pc.j0;
-        if (rows) had += pc.j1 - pc.j0;
-        at ^= 1;
+        const int steps = pc.j1 - pc.j0;
+        if (pc.row_hi - pc.row_lo > 128 * g) {
+          const bool done = piece(pc, before, had, c_next, [&] { fetch(k + 1); });
+          ok = ok && done;
+          had += steps;
+        } else {
+          fetch(k + 1);
+        }
+        before += steps;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_free(k));
       }
       if (warp == 6 && lane == 0) seen_joins(a)[blockIdx.x] = join;
     }
@@ -1077,15 +1119,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// Joins the parts of the tiles that were cut: a warp a row, D/4 lanes at a time.
-constexpr int kSeenJoinThreads = 256, kSeenJoinRows = kSeenJoinThreads / 32;
+// Joins the parts of the tiles that were cut.  A CTA takes 32 rows, a lane each, its
+// warps the channels; the results go through shared memory to whole lines.
+constexpr int kSeenJoinThreads = 256, kSeenJoinRows = 32;
 template <typename T, int D>
-__global__ void __launch_bounds__(kSeenJoinThreads) k_kv4_seen_join(const __grid_constant__ AttnArgs a, int ctas) {
-  constexpr int L = D / 4, GRP = 32 / L, kBatch = 8;
+__global__ void __launch_bounds__(kSeenJoinThreads, 3) k_kv4_seen_join(const __grid_constant__ AttnArgs a, int ctas) {
+  constexpr int W = kSeenJoinThreads / 32, PER = D / 4 / W, kBatch = 4;  // 16-byte units of a row a warp takes; parts in flight
   constexpr float kShift = 6.0f;
-  __shared__ int s_list[kDecMaxCtas], s_warp[kSeenJoinThreads / 32];
+  __shared__ int s_list[kDecMaxCtas], s_warp[W];
+  __shared__ uint2 s_out[kSeenJoinRows][D / 4 + 1];
   pdl_prologue();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / L, d4 = lane % L;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const SeenJoin* joins = seen_joins(a);
   // the tiles that were cut, in order: the same list in every CTA
   static_assert(kDecMaxCtas <= kSeenJoinThreads, "a thread each");
@@ -1095,7 +1139,7 @@ __global__ void __launch_bounds__(kSeenJoinThreads) k_kv4_seen_join(const __grid
   __syncthreads();
   int count = 0, before = 0;
 #pragma unroll
-  for (int w = 0; w < kSeenJoinThreads / 32; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) before += s_warp[w];
     count += s_warp[w];
   }
@@ -1103,65 +1147,69 @@ __global__ void __launch_bounds__(kSeenJoinThreads) k_kv4_seen_join(const __grid
   __syncthreads();
   constexpr int kChunks = kPromptRows / kSeenJoinRows;
   for (int item = blockIdx.x; item < count * kChunks; item += gridDim.x) {
-    const int cta = s_list[item / kChunks], row = item % kChunks * kSeenJoinRows + warp;
+    const int cta = s_list[item / kChunks], row0 = item % kChunks * kSeenJoinRows, row = row0 + lane;
     const SeenJoin j = joins[cta];
-    if (j.row_lo + row >= j.row_hi) continue;
+    if (j.row_lo + row0 >= j.row_hi) continue;
+    const bool in = j.row_lo + row < j.row_hi;
     auto part = [&](int i) { return seen_parts(a, D, cta + i, i == 0 ? 1 : 0); };
-    // the largest reference, then the weights, 32 parts at a time
-    float m = -INFINITY;
-    for (int i = lane; i < j.parts; i += 32) m = fmaxf(m, part(i)[row]);
+    float m = -INFINITY;  // the row's largest reference
+    for (int i0 = 0; i0 < j.parts; i0 += 8) {
+      float x[8];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      for (int i = 0; i < 8; ++i) x[i] = in && i0 + i < j.parts ? part(i0 + i)[row] : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, x[i]);
+    }
     const float mu = m == -INFINITY ? 0.0f : m;
     float l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = 0; i0 < j.parts; i0 += 32) {
-      const int i = i0 + lane;
-      float w = 0.0f;
-      if (i < j.parts) {
-        w = exp2_approx(part(i)[row] - mu);
-        if (part(i)[row] != -INFINITY) l = fmaf(w, part(i)[kPromptRows + row], l);
+    float4 o[PER];
+#pragma unroll
+    for (int x = 0; x < PER; ++x) o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < j.parts; i0 += kBatch) {
+      float f[kBatch], pl[kBatch];
+      float4 v[kBatch][PER];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const bool has = in && i0 + b < j.parts;
+        const float* p = part(has ? i0 + b : 0);
+        const float ref = has ? p[row] : -INFINITY;
+        const bool some = ref != -INFINITY;  // (nothing was written where no key was seen)
+        f[b] = some ? ref : -INFINITY;
+        pl[b] = some ? p[kPromptRows + row] : 0.0f;
+#pragma unroll
+        for (int x = 0; x < PER; ++x)
+          v[b][x] = some ? *reinterpret_cast<const float4*>(p + 2 * kPromptRows + 4 * ((size_t)(warp + W * x) * kPromptRows + row))
+                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
-      for (int b0 = 0; b0 < 32 && i0 + b0 < j.parts; b0 += kBatch * GRP) {
-        float4 v[kBatch];
-        float f[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int x = b0 + b * GRP + grp;
-          f[b] = __shfl_sync(0xffffffffu, w, x & 31);
-          const bool there = x < 32 && i0 + x < j.parts && f[b] != 0.0f;  // (nothing was written where no key was seen)
-          v[b] = there ? *reinterpret_cast<const float4*>(part(i0 + x) + 2 * kPromptRows + (size_t)row * D + 4 * d4)
-                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (!there) f[b] = 0.0f;
-        }
+      for (int b = 0; b < kBatch; ++b) {
+        const float w = exp2_approx(f[b] - mu);
+        l = fmaf(w, pl[b], l);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          o.x = fmaf(f[b], v[b].x, o.x);
-          o.y = fmaf(f[b], v[b].y, o.y);
-          o.z = fmaf(f[b], v[b].z, o.z);
-          o.w = fmaf(f[b], v[b].w, o.w);
+        for (int x = 0; x < PER; ++x) {
+          o[x].x = fmaf(w, v[b][x].x, o[x].x);
+          o[x].y = fmaf(w, v[b][x].y, o[x].y);
+          o[x].z = fmaf(w, v[b][x].z, o[x].z);
+          o[x].w = fmaf(w, v[b][x].w, o[x].w);
         }
       }
     }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    if (GRP == 2) {
-      o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
-      o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
-      o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
-      o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
-    }
-    const int tok = (j.row_lo + row) / a.share, h = j.head * a.share + (j.row_lo + row) % a.share;
-    const size_t at = (size_t)(j.begin + tok) * a.q_heads + h;
     const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
-    if (grp == 0) {
-      uint2 w;
-      w.x = Half16<T>::narrow2(o.x * inv, o.y * inv);
-      w.y = Half16<T>::narrow2(o.z * inv, o.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.out[j.rank]) + at * D + 4 * d4) = w;
+#pragma unroll
+    for (int x = 0; x < PER; ++x)
+      s_out[lane][warp + W * x] = make_uint2(Half16<T>::narrow2(o[x].x * inv, o[x].y * inv), Half16<T>::narrow2(o[x].z * inv, o[x].w * inv));
+    auto at = [&](int x) {
+      const int y = j.row_lo + row0 + x, tok = y / a.share;
+      return (size_t)(j.begin + tok) * a.q_heads + j.head * a.share + (y - tok * a.share);
+    };
+    if (warp == 0 && in && a.lse[j.rank]) a.lse[j.rank][at(lane)] = l == 0.0f ? -INFINITY : (mu - kShift + log2f(l)) * 0.69314718055994531f;
+    __syncthreads();
+    for (int e = threadIdx.x; e < kSeenJoinRows * (D / 4); e += kSeenJoinThreads) {
+      const int x = e / (D / 4), d4 = e % (D / 4);
+      if (j.row_lo + row0 + x < j.row_hi)
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out[j.rank]) + at(x) * D + 4 * d4) = s_out[x][d4];
     }
-    if (lane == 0 && a.lse[j.rank])
-      a.lse[j.rank][at] = l == 0.0f ? -INFINITY : (mu - kShift + log2f(l)) * 0.69314718055994531f;
+    __syncthreads();
   }
 }
 
