@@ -822,8 +822,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
     // Q into its tile, channels in the codes' order, with the scale's sign; returns
     // what scores are multiplied with
     auto load_q = [&](const PromptPiece& pc) {
-      // Neighbouring lanes take a row's 16-byte units, so that a load touches a few
-      // lines rather than 32; all loads are in flight at once.
+      // Straight into shared memory, all loads in flight, neighbouring lanes a row's
+      // 16-byte units (a few lines a load, not 32); then in place.  Loops stay loops:
+      // this runs once a piece, and its time is that of fetching its code.
       constexpr int UPR = D / 8, RPI = 32 / UPR;
       const int row = pc.row_lo + 128 * g + r, tok = row / a.share, gh = row - tok * a.share;
       const long long own = row < pc.row_hi
@@ -831,24 +832,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
                                 : -1;
       const T* src = static_cast<const T*>(a.q[pc.rank]);
       const int u = lane % UPR, sub = lane / UPR;
-      uint4 v[UPR];
-#pragma unroll
+      const uint32_t tile = sq + (uint32_t)(g * Shape::q_tile) + (uint32_t)(u / 8) * 16384u;
+      auto place = [&](int i) {
+        const int x = quad * 32 + i * RPI + sub;
+        return tile + (uint32_t)x * 128u + (uint32_t)(((u % 8) ^ (x & 7)) * 16);
+      };
+#pragma unroll 1
       for (int i = 0; i < UPR; ++i) {
         const long long at = __shfl_sync(0xffffffffu, own, i * RPI + sub);
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (at >= 0)
-          asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                       : "l"(src + at + 8 * u));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place(i)), "l"(src + (at < 0 ? 0 : at + 8 * u)),
+                     "r"(at < 0 ? 0 : 16)  // (rows that are not there: zeros)
+                     : "memory");
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       float c = fabsf(a.scale) * 1.44269504088896341f;
       const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < UPR; ++i) {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place(i)) : "memory");
         float f = 1.0f;
         if constexpr (!FP16) {  // a bf16 row as fp16: its largest value goes to 2^8 .. 2^9, exactly
-          uint32_t top = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
-                                  __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+          uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
           top = max(top & 0xffffu, top >> 16);
 #pragma unroll
           for (int m = UPR / 2; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
@@ -862,12 +867,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           const float2 x = param_floats(w);
           return Half16<__half>::narrow2(x.x * f, x.y * f) ^ flip;
         };
-        const uint4 o = make_uint4(half(__byte_perm(v[i].x, v[i].z, 0x5410)), half(__byte_perm(v[i].x, v[i].z, 0x7632)),
-                                   half(__byte_perm(v[i].y, v[i].w, 0x5410)), half(__byte_perm(v[i].y, v[i].w, 0x7632)));
-        const int x = quad * 32 + i * RPI + sub;
-        sts128(sq + (uint32_t)(g * Shape::q_tile) + (uint32_t)x * 128u + (uint32_t)(u / 8) * 16384u +
-                   (uint32_t)(((u % 8) ^ (x & 7)) * 16),
-               o);
+        sts128(place(i), make_uint4(half(__byte_perm(v.x, v.z, 0x5410)), half(__byte_perm(v.x, v.z, 0x7632)),
+                                    half(__byte_perm(v.y, v.w, 0x5410)), half(__byte_perm(v.y, v.w, 0x7632))));
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -893,6 +894,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         all_hi = first < pc.row_hi ? pc.pos0 - 1 : 0x7fffffff;
         all_lo = __reduce_max_sync(0xffffffffu, in ? lo : -(1 << 30));
       }
+      if (SEEN && c == 0.0f) c = 0x1p-140f;  // 0 times the hidden scores' infinity would be NaN
       float ref = 0.0f, l = 0.0f;
       bool any = false, ok = true;
       for (int jj = 0; jj < steps; ++jj) {
@@ -903,18 +905,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         const uint32_t absent = s_absent[j & 7];
         const uint32_t rg = range(j);
         // (a page's V in bf16, so P too: tested in the masked form only)
-        bool masked;
-        uint32_t vis[4] = {0, 0, 0, 0};  // SEEN: the keys that the row sees
+        bool masked, hides = false;
+        int key1 = 0;
         if constexpr (SEEN) {
-          const int key1 = slot_at(pc, 2 * (pc.j0 + jj) + 1) * kKv4Page;
+          key1 = slot_at(pc, 2 * (pc.j0 + jj) + 1) * kKv4Page;
           auto whole = [&](int k) { return k + kKv4Page - 1 <= all_hi && (k >= all_lo || k + kKv4Page <= a.sinks); };
-          masked = absent || !whole(key0) || !whole(key1) || (rg & 0x202u);
-          if (masked) {
-            const SeenRow x = {hi, lo, pc.pos0, pc.news, a.mask && in ? a.mask + (size_t)(pc.begin + tok) * a.words : nullptr};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              vis[i] = (absent >> (i >> 1)) & 1u ? 0u : seen_word(x, a, (i < 2 ? key0 : key1) + 32 * (i & 1));
-          }
+          hides = absent || !whole(key0) || !whole(key1);
+          masked = (rg & 0x202u) != 0;
         } else {
           masked = absent || key0 + 127 > all_hi || key0 < all_lo || (rg & 0x202u);
         }
@@ -930,23 +927,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           }
           tmem_st_wait();
         }
-        // of the 32 keys from c0 on, c0 = 0 or 64, or 32 more
-        auto word = [&](int c0, int more) { return c0 < 64 ? vis[more] : vis[2 + more]; };
-        auto seen = [&](uint32_t w, int c0, int i) {
-          if constexpr (SEEN) return ((w >> i) & 1u) != 0;
-          const int key = key0 + c0 + i;
-          return key <= hi && key >= lo && !((absent >> ((c0 + i) >> 6)) & 1u);
+        if (SEEN && hides) {
+          // Hidden scores become -infinity in tensor memory, so that one form of what
+          // follows serves all steps: two would not stay in the instruction cache.
+          const SeenRow x = {hi, lo, pc.pos0, pc.news, a.mask && in ? a.mask + (size_t)(pc.begin + tok) * a.words : nullptr};
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            const uint32_t w = (absent >> (c0 >> 6)) & 1u ? 0u : seen_word(x, a, (c0 < 64 ? key0 : key1) + (c0 & 32));
+            uint32_t v[32];
+            tmem_ld32(ts + (uint32_t)c0, v);
+            tmem_ld_wait32(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((w >> i) & 1u)) v[i] = 0xff800000u;
+            tmem_st16(ts + (uint32_t)c0, v);
+            tmem_st16(ts + (uint32_t)c0 + 16u, v + 16);
+          }
+          tmem_st_wait();
+        }
+        auto seen = [&](int i) {
+          if (SEEN) return true;
+          const int key = key0 + i;
+          return key <= hi && key >= lo && !((absent >> (i >> 6)) & 1u);
         };
         // Loops over 32 columns stay loops (the roles' code together must stay
         // in the instruction cache); the next columns load under the current.
         uint32_t s[2][32];
         float m0 = -INFINITY, m1 = -INFINITY;
         tmem_ld32(ts, s[0]);
-        auto top = [&](const uint32_t* v, int c0, uint32_t w) {
-          if (masked) {
+        auto top = [&](const uint32_t* v, int c0) {
+          if (!SEEN && masked) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (seen(w, c0, i)) m0 = fmaxf(m0, __uint_as_float(v[i]));
+              if (seen(c0 + i)) m0 = fmaxf(m0, __uint_as_float(v[i]));
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -959,10 +972,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         for (int c0 = 0; c0 < 128; c0 += 64) {
           tmem_ld_wait32(s[0]);
           tmem_ld32(ts + (uint32_t)c0 + 32u, s[1]);
-          top(s[0], c0, SEEN ? word(c0, 0) : 0u);
+          top(s[0], c0);
           tmem_ld_wait32(s[1]);
           tmem_ld32(ts + ((uint32_t)c0 + 64u) % 128u, s[0]);  // in the end the first columns again
-          top(s[1], c0 + 32, SEEN ? word(c0, 1) : 0u);
+          top(s[1], c0 + 32);
         }
         const float m = fmaxf(m0, m1), mc = m * c;
         const bool grows = m != -INFINITY && (!any || mc > ref + 8.0f);
@@ -991,15 +1004,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           const float2 x = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), cc, off);
           return make_float2(exp2_approx(x.x), exp2_approx(x.y));
         };
-        auto make = [&](const uint32_t* v, int c0, uint32_t vw) {
+        auto make = [&](const uint32_t* v, int c0) {
           uint32_t w[16];
           if (masked) {  // tested once, not per element
             const bool wide = (rg & (c0 < 64 ? 2u : 0x200u)) != 0;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float2 p = pair(v, i);
-              if (!seen(vw, c0, i)) p.x = 0.0f;
-              if (!seen(vw, c0, i + 1)) p.y = 0.0f;
+              if (!seen(c0 + i)) p.x = 0.0f;
+              if (!seen(c0 + i + 1)) p.y = 0.0f;
               sum = add2(sum, p);
               w[i / 2] = wide ? Half16<T>::narrow2(p.x, p.y) : Half16<__half>::narrow2(p.x, p.y);
             }
@@ -1017,10 +1030,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         for (int c0 = 0; c0 < 128; c0 += 64) {
           tmem_ld_wait32(s[0]);
           tmem_ld32(ts + (uint32_t)c0 + 32u, s[1]);
-          make(s[0], c0, SEEN ? word(c0, 0) : 0u);
+          make(s[0], c0);
           tmem_ld_wait32(s[1]);
           if (c0 == 0) tmem_ld32(ts + 64u, s[0]);
-          make(s[1], c0 + 32, SEEN ? word(c0, 1) : 0u);
+          make(s[1], c0 + 32);
         }
         l += sum.x + sum.y;
         tmem_st_wait();
@@ -1056,7 +1069,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
       const bool wide_out = (reinterpret_cast<uintptr_t>(a.out[pc.rank]) & 31u) == 0;
       const size_t at = (size_t)(pc.begin + tok) * a.q_heads + pc.head * a.share + gh;
-#pragma unroll
+#pragma unroll(SEEN ? 1 : D / 16)
       for (int c0 = 0; c0 < D; c0 += 16) {
         uint32_t v[16], w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (some) {
