@@ -2,7 +2,7 @@
 // two types compile in a unit each (kv4_attention_bf16.cu, kv4_attention_fp16.cu),
 // and so do those for rows with sets of seen keys of their own (kv4_seen_*.cu).
 #pragma once
-#include "kv4_prompt.cuh"
+#include "kv4_seen.cuh"
 
 namespace dcc {
 
@@ -29,8 +29,12 @@ AttnKernel attn_kernel_of(int which) {
   };
   using No = std::false_type;
   switch (which) {
-    case kAttnPrompt: return {(const void*)&k_kv4_prompt<T, D, G, SEEN>, kPromptThreads, PromptShape<D, G>::smem};
-    case kAttnJoin: return {(const void*)&k_kv4_seen_join<T, D>, kSeenJoinThreads, 0};
+    case kAttnPrompt:
+      if constexpr (SEEN) return {(const void*)&k_kv4_seen<T, D, G>, kPromptThreads, PromptShape<D, G>::smem};
+      else return {(const void*)&k_kv4_prompt<T, D, G>, kPromptThreads, PromptShape<D, G>::smem};
+    case kAttnJoin:
+      if constexpr (SEEN) return {(const void*)&k_kv4_seen_join<T, D>, kSeenJoinThreads, 0};
+      else return {};
     case kAttnSmall: return decode(std::integral_constant<int, 1>{}, std::true_type{});
     case 1: return decode(std::integral_constant<int, 1>{}, No{});
     default: break;

@@ -153,100 +153,7 @@ __device__ __forceinline__ float power2(int e) { return __int_as_float((127 + e)
 constexpr float kTopK = 0x1p15f;  // larger groups of K do not fit fp16
 constexpr float kTopV = 0x1p11f;  // the smallest P that fp16 holds, times this, is 2^-12 of a V of 2^-8
 
-// What a CTA works on: up to 256 rows of one (sequence, rank, kv head) and some of
-// the steps over their keys -- all of them, or with SEEN what its share holds.
-struct PromptPiece {
-  int seq, rank, head, begin, pos0, news;  // (begin .. news: the sequence's rows, DecSeq)
-  int row_lo, row_hi;
-  int page0, kept, pages;                  // the tile's pages, as in DecSeq
-  int len;                                 // keys from here on are seen by no row
-  int j0, j1;                              // steps j0 .. j1 - 1
-  int slot;                                // SEEN: where its partial goes; -1: it is whole
-  int parts;                               // the CTAs that hold a part of the tile, where this is the first of several
-};
-
-// ---- SEEN: an even split.  The steps of all tiles (of 256 rows; by sequence, rank,
-// kv head) form one line, of which every CTA takes an equal run; a tile that is
-// cut leaves partials (reference, l, O), joined by a second kernel.  Each tile
-// of a sequence counts the same number of steps: exact in a tree, where all rows
-// see the whole context, and at most one too many with a window, unless the
-// sequence is shorter than that.
-__device__ __forceinline__ int seen_tile_steps(const AttnArgs& a, const DecSeq& q) {
-  long long pages = q.pages;
-  if (!a.mask) {
-    const long long keys = (long long)a.window + (kPromptRows - 2 + a.share) / a.share;  // from the first row's first one
-    const long long most = (keys + kKv4Page - 2) / kKv4Page + 1 + (a.sinks + kKv4Page - 1) / kKv4Page;
-    if (most < pages) pages = most;
-  }
-  return (int)((pages + 1) / 2);
-}
-struct SeenWalk {
-  long long u, end;  // the next step of the line, and the end of the CTA's run
-  long long units;   // of the line
-  int ctas;
-  int s, seg, j;     // the sequence, its tile (rank and head slowest), the step within
-};
-// The next piece of a run (one thread).
-__device__ __forceinline__ bool seen_next(const Kv4Dev& kv, const AttnArgs& a, SeenWalk& w, PromptPiece& p) {
-  if (w.u >= w.end) return false;
-  const int nh = kv.n * kv.heads;
-  DecSeq q = dec_seq<true>(kv, a, w.s, kPromptRows);
-  while (w.seg >= nh * q.tiles) {  // on to the next sequence that has rows
-    q = dec_seq<true>(kv, a, ++w.s, kPromptRows);
-    w.seg = 0;
-  }
-  const int rh = w.seg / q.tiles, tile = w.seg - rh * q.tiles, steps = seen_tile_steps(a, q);
-  p.seq = w.s;
-  p.rank = rh / kv.heads;
-  p.head = rh - p.rank * kv.heads;
-  p.begin = q.begin;
-  p.pos0 = q.pos0;
-  p.news = q.news;
-  p.row_lo = tile * kPromptRows;
-  p.row_hi = min(q.rows, p.row_lo + kPromptRows);
-  p.page0 = q.page0;
-  p.kept = q.kept;
-  p.pages = q.empty ? 0 : q.pages;
-  p.len = kv.len[w.s];
-  if (!a.mask) {
-    const int pos_lo = q.pos0 + p.row_lo / a.share, pos_hi = q.pos0 + (p.row_hi - 1) / a.share;
-    p.page0 = max(0, pos_lo - a.window + 1) / kKv4Page;
-    p.kept = min((a.sinks + kKv4Page - 1) / kKv4Page, p.page0);
-    if (p.kept == p.page0) p.kept = 0, p.page0 = 0;
-    p.page0 -= p.kept;
-    p.pages = pos_hi < 0 ? 0 : min(pos_hi / kKv4Page, kv.max_pages) - p.page0 + 1;
-    p.len = min(p.len, pos_hi + 1);
-  }
-  const int take = (int)min((long long)(steps - w.j), w.end - w.u), real = (p.pages + 1) / 2;
-  p.j0 = min(w.j, real);
-  p.j1 = min(w.j + take, real);
-  p.slot = take == steps ? -1 : w.j > 0 ? 0 : 1;
-  p.parts = 0;
-  if (p.slot == 1)  // the CTA with the tile's last step
-    p.parts = (int)(((w.u + steps) * w.ctas - 1) / w.units) - (int)(((w.u + 1) * w.ctas - 1) / w.units) + 1;
-  w.u += take;
-  w.j = 0;
-  ++w.seg;
-  return true;
-}
-// what a call's workspace holds after the streaming kernel's counters
-struct SeenJoin {
-  int parts, rank, head, row_lo, row_hi, begin, pad[2];
-};
-constexpr int kSeenRing = 4;  // pieces known at a time
-constexpr int kSeenJoinBytes = kDecMaxCtas * (int)sizeof(SeenJoin);
-// floats of a partial: reference and l of each row, then O, four channels of all rows
-// after the other (a warp holds 32 rows and writes whole lines)
-__host__ __device__ constexpr size_t seen_part(int dim) { return (size_t)kPromptRows * (dim + 2); }
-__host__ __device__ constexpr size_t seen_ws_bytes(int dim) {
-  return 1024 + kSeenJoinBytes + 2 * kDecMaxCtas * seen_part(dim) * 4;
-}
-__device__ __forceinline__ SeenJoin* seen_joins(const AttnArgs& a) { return reinterpret_cast<SeenJoin*>(a.ws + 1024); }
-__device__ __forceinline__ float* seen_parts(const AttnArgs& a, int dim, int cta, int slot) {
-  return reinterpret_cast<float*>(a.ws + 1024 + kSeenJoinBytes) + (2 * (size_t)cta + slot) * seen_part(dim);
-}
-
-template <typename T, int D, int G, bool SEEN>
+template <typename T, int D, int G>
 __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, const __grid_constant__ AttnArgs a, LocalDev dc) {
   using Shape = PromptShape<D, G>;
   constexpr bool FP16 = std::is_same<T, __half>::value;
@@ -258,13 +165,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   // bf16 cache, by step and page: 1 where a key of K has its own scale, 2 where V stays bf16
   __shared__ __align__(2) uint8_t s_range[8][2];
   __shared__ int8_t s_exp[4][128];  // by step: K's powers of two
-  // SEEN: the pieces, found by the warp that loads, ahead of the others.  The last
-  // one is marked: row_hi 0.
-  __shared__ SeenWalk s_walk;
-  __shared__ PromptPiece s_piece[kSeenRing];
-  __shared__ __align__(8) uint64_t s_piece_bars[2 * kSeenRing];
-  auto piece_full = [&](int k) { return smem_addr_u32(&s_piece_bars[k % kSeenRing]); };
-  auto piece_free = [&](int k) { return smem_addr_u32(&s_piece_bars[kSeenRing + k % kSeenRing]); };
   const uint32_t base = (smem_addr_u32(prompt_raw) + 1023u) & ~1023u;
   const uint32_t sq = base, sk = sq + 2 * Shape::q_tile, sv = sk + 2 * Shape::kv_tile, raw = sv + 2 * Shape::kv_tile;
   unsigned char* raw_g_rw = prompt_raw + (raw - smem_addr_u32(prompt_raw));
@@ -295,76 +195,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       mma_mbar_init(two(pvDone, i), 1);
       mma_mbar_init(two(qFull, i), 4);
     }
-    if (SEEN)
-      for (int i = 0; i < kSeenRing; ++i) {
-        mma_mbar_init(piece_full(i), 1);
-        mma_mbar_init(piece_free(i), FP16 ? 13 : 15);  // one each from the warps that read it
-      }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
 
-  PromptPiece one = {};  // the only piece
-  if constexpr (SEEN) {
-    __shared__ long long s_sum[kPromptThreads / 32];
-    const int nh = kv.n * kv.heads, cta = (int)blockIdx.x;
-    auto steps_of = [&](int s) {
-      if (s >= kv.seqs) return 0ll;
-      const DecSeq q = dec_seq<true>(kv, a, s, kPromptRows);
-      return q.tiles > 0 ? (long long)q.tiles * seen_tile_steps(a, q) : 0ll;
-    };
-    auto scan = [&](long long mine, long long* total) {  // exclusive, over the CTA
-      long long x = mine;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, m);
-        if (lane >= m) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_sum[warp] = x;
-      __syncthreads();
-      long long first = x - mine;
-      *total = 0;
-      for (int w = 0; w < kPromptThreads / 32; ++w) {
-        if (w < warp) first += s_sum[w];
-        *total += s_sum[w];
-      }
-      return first;
-    };
-    long long units = 0, first0 = 0, mine0 = 0;
-    for (int s0 = 0; s0 < kv.seqs; s0 += kPromptThreads) {
-      const long long mine = steps_of(s0 + (int)threadIdx.x);
-      long long total;
-      const long long first = scan(mine, &total);
-      if (s0 == 0) first0 = first, mine0 = mine;
-      units += total;
-    }
-    units *= nh;
-    const int C = units < (long long)gridDim.x ? (int)units : (int)gridDim.x;
-    if (cta >= C) {
-      if (threadIdx.x == 0) seen_joins(a)[cta].parts = 0;
-      return;
-    }
-    const long long c0 = units * cta / C, c1 = units * (cta + 1) / C;
-    long long before = 0;
-    for (int s0 = 0; s0 < kv.seqs && before * nh <= c0; s0 += kPromptThreads) {
-      const int s = s0 + (int)threadIdx.x;
-      long long mine = mine0, first = first0;
-      if (kv.seqs > kPromptThreads) {
-        mine = steps_of(s);
-        long long total;
-        first = before + scan(mine, &total);
-        before += total;
-      } else {
-        before = units;
-      }
-      if (mine && first * nh <= c0 && c0 < (first + mine) * nh) {
-        const int steps = seen_tile_steps(a, dec_seq<true>(kv, a, s, kPromptRows));
-        const long long in = c0 - first * nh;
-        s_walk = SeenWalk{c0, c1, units, C, s, (int)(in / steps), (int)(in % steps)};
-      }
-    }
-  } else {
   // ---- this CTA's rows; the last tiles (the most keys) come first
   const int nh = kv.n * kv.heads, per = nh * kv.seqs;
   const int turn = (int)blockIdx.x / per, rest = (int)blockIdx.x % per, seq = rest / nh, rh = rest % nh;
@@ -380,6 +214,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   // one page past the row at most: it is reported there
   const int pages = pos_hi < 0 ? 0 : min(pos_hi / kKv4Page, kv.max_pages) - page0 + 1;
   const int steps = (pages + 1) / 2;
+  const int nt = row_hi - row_lo > 128 ? 2 : 1;
   if (steps <= 0) {  // nothing to see
     for (int i = threadIdx.x; i < (row_hi - row_lo) * (D / 8); i += kPromptThreads) {
       const int row = row_lo + i / (D / 8);
@@ -388,8 +223,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       if (i % (D / 8) == 0 && a.lse[rank]) a.lse[rank][at] = -INFINITY;
     }
     return;
-  }
-  one = PromptPiece{seq, rank, head, q.begin, q.pos0, 0, row_lo, row_hi, page0, 0, pages, min(kv.len[seq], pos_hi + 1), 0, steps, -1, 0};
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr_u32(&tmem_slot)),
@@ -404,42 +237,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
   const uint32_t tmem = tmem_slot;  // S / P of the two row tiles, then O: 128 columns each
   auto range = [&](int j) { return FP16 ? 0u : (uint32_t)*reinterpret_cast<const volatile uint16_t*>(s_range[j & 7]); };
   auto wide_v = [&](int j, int h) { return (range(j) & (2u << 8 * h)) != 0; };
-  auto wait = [&](uint32_t bar, int phase) {
-    return local_wait(bar, (uint32_t)phase & 1u, dc, SEEN ? 0 : one.rank, SEEN ? (int)blockIdx.x : one.head);
-  };
-  // Calls `work` for every piece with the steps before it, until one returns false
-  // (one thread, or a whole warp).
-  auto pieces = [&](bool whole_warp, auto&& work) {
-    if constexpr (!SEEN) {
-      return work(one, 0);
-    } else {
-      for (int k = 0, done = 0;; ++k) {
-        if (!wait(piece_full(k), k / kSeenRing)) return false;
-        const PromptPiece& p = s_piece[k % kSeenRing];
-        if (p.row_hi == 0) return true;
-        if (!work(p, done)) return false;
-        done += p.j1 - p.j0;
-        if (whole_warp) __syncwarp();
-        if (!whole_warp || lane == 0) mbar_arrive(piece_free(k));
-      }
-    }
-  };
-  // the table's slot of a tile's page
-  auto slot_at = [&](const PromptPiece& p, int v) { return SEEN && v < p.kept ? v : p.page0 + v; };
+  const int len = min(kv.len[seq], pos_hi + 1);  // keys that some row may see
+  auto wait = [&](uint32_t bar, int phase) { return local_wait(bar, (uint32_t)phase & 1u, dc, rank, head); };
 
   if (warp == 0) {  // ---- loads
-    int unfinished = 0;
-    auto load = [&](const PromptPiece& pc, int before) {
-    int ids = -1, ids_at = -(1 << 30);
-    const int ahead = 2 * (before - pc.j0);  // of the ring, against the tile's pages
-    for (int v = 2 * pc.j0; v < 2 * pc.j1; ++v) {
-      const int p = v + ahead;
-      if (v - ids_at >= 32) {
-        ids_at = v;
-        ids = v + lane < pc.pages ? kv4_page(kv, pc.seq, slot_at(pc, v + lane)) : -1;
+    int ids = -1, ids_at = -(1 << 30), unfinished = 0;
+    for (int p = 0; p < 2 * steps; ++p) {
+      if (p - ids_at >= 32) {
+        ids_at = p;
+        ids = p + lane < pages ? kv4_page(kv, seq, page0 + p + lane) : -1;
       }
-      const int page = __shfl_sync(0xffffffffu, ids, v - ids_at), slot = p % R;
-      if (p >= R && !wait(rawe(slot), p / R - 1)) return false;
+      const int page = __shfl_sync(0xffffffffu, ids, p - ids_at), slot = p % R;
+      if (p >= R && !wait(rawe(slot), p / R - 1)) break;
       if (lane == 0) {
         uint32_t& absent = s_absent[(p / 2) & 7];
         absent = (p & 1 ? absent : 0u) | (page < 0 ? 1u << (p & 1) : 0u);
@@ -448,36 +257,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           asm volatile(
               "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                   raw + (uint32_t)(slot * BLK)),
-              "l"(kv4_block(kv, pc.rank, a.layer, page, pc.head, BLK)), "r"((uint32_t)BLK), "r"(rawf(slot))
+              "l"(kv4_block(kv, rank, a.layer, page, head, BLK)), "r"((uint32_t)BLK), "r"(rawf(slot))
               : "memory");
       }
       ++unfinished;
-    }
-    return true;
-    };
-    if constexpr (!SEEN) {
-      load(one, 0);
-    } else {
-      // Piece k + 1 is made known before piece k's pages are asked for.  A slot of the
-      // ring is free once piece k + 1 - kSeenRing has been worked off, whose pages
-      // have been loaded.
-      auto publish = [&](int k) {
-        if (k >= kSeenRing && !wait(piece_free(k), k / kSeenRing - 1)) return false;
-        if (lane == 0) {
-          PromptPiece& p = s_piece[k % kSeenRing];
-          if (!seen_next(kv, a, s_walk, p)) p.row_hi = 0;
-          mbar_arrive(piece_full(k));
-        }
-        __syncwarp();
-        return true;
-      };
-      bool ok = publish(0);
-      for (int k = 0, before = 0; ok; ++k) {
-        const PromptPiece pc = s_piece[k % kSeenRing];
-        if (pc.row_hi == 0) break;
-        ok = publish(k + 1) && load(pc, before);
-        before += pc.j1 - pc.j0;
-      }
     }
     // a copy in flight when a wait gave up ends before the CTA does
     for (int p = max(0, unfinished - R); p < unfinished; ++p) local_drain(rawf(p % R), (uint32_t)(p / R) & 1u);
@@ -487,12 +270,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       const uint32_t id_s = id | ((uint32_t)(128 >> 3) << 17), id_o = id | ((uint32_t)(D >> 3) << 17);
       uint32_t rg0 = 0, rg1 = 0;  // of even and odd steps
       bool ok = true;
-      int had[2] = {0, 0}, qs[2] = {0, 0};  // by row tile: steps and tiles of Q so far
-      pieces(false, [&](const PromptPiece& pc, int before) {
-      const int steps = pc.j1 - pc.j0, nt = pc.row_hi - pc.row_lo > 128 ? 2 : 1;
-      if (SEEN && steps == 0) return true;
-      auto scores = [&](int g, int jj) {
-        const int j = before + jj;
+      auto scores = [&](int g, int j) {
         ok = ok && wait(two(kFull, j & 1), j >> 1);
         if (!ok) return;
         tc_fence_after();
@@ -511,12 +289,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         if (g == nt - 1) tc_commit(two(kFree, j & 1));
         (j & 1 ? rg1 : rg0) = range(j);
       };
-      for (int g = 0; g < nt; ++g) ok = ok && wait(two(qFull, g), qs[g]);
+      for (int g = 0; g < nt; ++g) ok = ok && wait(two(qFull, g), 0);
       for (int g = 0; g < nt; ++g) scores(g, 0);
-      for (int jj = 0; jj < steps && ok; ++jj)
+      for (int j = 0; j < steps && ok; ++j)
         for (int g = 0; g < nt && ok; ++g) {
-          const int j = before + jj;
-          ok = wait(two(pFull, g), had[g] + jj) && wait(two(vFull, j & 1), j >> 1);
+          ok = wait(two(pFull, g), j) && wait(two(vFull, j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
           const uint32_t bf = (1u << 7) | (1u << 10);
@@ -528,19 +305,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
             asm volatile(
                 "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem + 256u + (uint32_t)g * 128u),
-                "r"(tmem + (uint32_t)g * 128u + (uint32_t)kk * 8u), "l"(bd), "r"(ids[kk / 4]), "r"(jj > 0 || kk > 0 ? 1u : 0u)
+                "r"(tmem + (uint32_t)g * 128u + (uint32_t)kk * 8u), "l"(bd), "r"(ids[kk / 4]), "r"(j > 0 || kk > 0 ? 1u : 0u)
                 : "memory");
           }
           if (g == nt - 1) tc_commit(two(vFree, j & 1));
           tc_commit(two(pvDone, g));
-          if (jj + 1 < steps) scores(g, jj + 1);
+          if (j + 1 < steps) scores(g, j + 1);
         }
-      for (int g = 0; g < nt; ++g) {
-        had[g] += steps;
-        ++qs[g];
-      }
-      return ok;
-      });
       if (!ok) {
         tc_commit(last);
         local_drain(last, 0);
@@ -555,11 +326,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
       __syncwarp();
       if (lane == 0) mbar_arrive(rawe(p % R));
     };
-    pieces(true, [&](const PromptPiece& pc, int before) {
-    const int len = pc.len, ahead = before - pc.j0;
-    for (int j = before; j < before + (pc.j1 - pc.j0) && ok; ++j) {
+    for (int j = 0; j < steps && ok; ++j) {
       const int buf = j & 1;
-      auto key_at = [&](int p) { return slot_at(pc, p - 2 * ahead) * kKv4Page; };  // of a page of the ring
       const uint32_t kt = sk + (uint32_t)(buf * Shape::kv_tile), vt = sv + (uint32_t)(buf * Shape::kv_tile);
       if (j >= 2) ok = wait(two(kFree, buf), (j >> 1) - 1);
       uint32_t absent = 0;
@@ -666,7 +434,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
                                                                        kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
               const uint32_t pw = par[key * NG + gr];
               const float2 f = Half16<T>::widen2(pw);
-              const bool none = (param_bad<T>(pw) & kBad) || !there || key_at(p) + key >= len;
+              const bool none = (param_bad<T>(pw) & kBad) || !there || (page0 + p) * kKv4Page + key >= len;
               v[x] = none ? 0.0f : fmaf((float)((word >> (4 * n)) & 15u), f.x, f.y);
             }
             const uint32_t pair = narrow_finite<T>(v[0], v[1]);
@@ -692,14 +460,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
             bad |= FP16 ? param_large(pr[k][x]) : param_bad<__half>(pr[k][x]);
           }
         }
-        if ((bad & kBad) || !there || key_at(p) + 8 * oct + 7 >= len) {  // some key must be zero
+        if ((bad & kBad) || !there || (page0 + p) * kKv4Page + 8 * oct + 7 >= len) {  // some key must be zero
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int key = 8 * oct + (k ^ swap);
             uint32_t any = 0;  // (another group of the key may be bad: its own unit sees to it)
 #pragma unroll
             for (int x = 0; x < GW; ++x) any |= param_bad<__half>(pr[k][x]);
-            if ((any & kBad) || !there || key_at(p) + key >= len)
+            if ((any & kBad) || !there || (page0 + p) * kKv4Page + key >= len)
 #pragma unroll
               for (int x = 0; x < GW; ++x) pr[k][x] = 0u;
 #pragma unroll
@@ -742,18 +510,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         mbar_arrive(rawe((2 * j + 1) % R));
       }
     }
-    return ok;
-    });
   } else if (warp >= 14) {  // ---- the bf16 cache's parameters, in place as fp16
     if constexpr (!FP16) {
       // a slot's pages are all one warp's: one that skipped a page of a slot could
       // take the barrier's state before that page for the next page's arrival
-      pieces(true, [&](const PromptPiece& pc, int before) {
-      const int ahead = 2 * (before - pc.j0), len = pc.len;
-      for (int p = 2 * pc.j0 + ahead; p < 2 * pc.j1 + ahead; ++p) {
+      for (int p = 0; p < 2 * steps; ++p) {
         const int slot = p % R, j = p >> 1, h = p & 1;
         if ((slot == 1) != (warp == 15)) continue;
-        if (!wait(rawf(slot), p / R)) return false;
+        if (!wait(rawf(slot), p / R)) break;
         uint32_t ranges = 0;
         if (!((s_absent[j & 7] >> h) & 1u)) {
           uint32_t* par = reinterpret_cast<uint32_t*>(raw_g_rw + slot * BLK + 2 * kv4_codes_bytes(D));
@@ -775,7 +539,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const int key = lane + 32 * x;
-              const bool counts = slot_at(pc, p - ahead) * kKv4Page + key < len;
+              const bool counts = (page0 + p) * kKv4Page + key < len;
               uint32_t bad = 0;
               float m = 0.0f;
               bool fits = true;
@@ -812,109 +576,66 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         __syncwarp();
         if (lane == 0) mbar_arrive(ready(slot));
       }
-      return true;
-      });
     }
   } else {  // ---- P, one row per thread
-    const int g = (warp - 6) >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t ts = tmem + lanes + (uint32_t)g * 128u, to = tmem + lanes + 256u + (uint32_t)g * 128u;
-    // Q into its tile, channels in the codes' order, with the scale's sign; returns
-    // what scores are multiplied with
-    auto load_q = [&](const PromptPiece& pc) {
-      // Straight into shared memory, all loads in flight, neighbouring lanes a row's
-      // 16-byte units (a few lines a load, not 32); then in place.  Loops stay loops:
-      // this runs once a piece, and its time is that of fetching its code.
-      constexpr int UPR = D / 8, RPI = 32 / UPR;
-      const int row = pc.row_lo + 128 * g + r, tok = row / a.share, gh = row - tok * a.share;
-      const long long own = row < pc.row_hi
-                                ? (long long)((size_t)(pc.begin + tok) * a.q_stride + (size_t)(pc.head * a.share + gh) * D)
-                                : -1;
-      const T* src = static_cast<const T*>(a.q[pc.rank]);
-      const int u = lane % UPR, sub = lane / UPR;
-      const uint32_t tile = sq + (uint32_t)(g * Shape::q_tile) + (uint32_t)(u / 8) * 16384u;
-      auto place = [&](int i) {
-        const int x = quad * 32 + i * RPI + sub;
-        return tile + (uint32_t)x * 128u + (uint32_t)(((u % 8) ^ (x & 7)) * 16);
-      };
-#pragma unroll 1
-      for (int i = 0; i < UPR; ++i) {
-        const long long at = __shfl_sync(0xffffffffu, own, i * RPI + sub);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place(i)), "l"(src + (at < 0 ? 0 : at + 8 * u)),
-                     "r"(at < 0 ? 0 : 16)  // (rows that are not there: zeros)
-                     : "memory");
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+    const int g = (warp - 6) >> 2, quad = warp & 3, r = quad * 32 + lane, row = row_lo + 128 * g + r;
+    if (g < nt) {
+      const bool in = row < row_hi;
+      const int tok = row / a.share, gh = row - tok * a.share;
+      const int hi = in ? q.pos0 + tok : -1, lo = a.window > 0 ? q.pos0 + tok - a.window + 1 : 0;
       float c = fabsf(a.scale) * 1.44269504088896341f;
-      const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-#pragma unroll 2
-      for (int i = 0; i < UPR; ++i) {
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place(i)) : "memory");
+      {  // Q into its tile, channels in the codes' order, with the scale's sign
+        const T* src = static_cast<const T*>(a.q[rank]) + (size_t)(q.begin + tok) * a.q_stride +
+                       (size_t)(head * a.share + gh) * D;
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        const uint32_t dst = sq + (uint32_t)(g * Shape::q_tile) + (uint32_t)r * 128u;
         float f = 1.0f;
         if constexpr (!FP16) {  // a bf16 row as fp16: its largest value goes to 2^8 .. 2^9, exactly
-          uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+          uint32_t top = 0;
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 v = in ? *reinterpret_cast<const uint4*>(src + 8 * u) : make_uint4(0, 0, 0, 0);
+            top = __vmaxu2(__vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu)),
+                           v.w & 0x7fff7fffu);
+          }
           top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-          for (int m = UPR / 2; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
           const int e = top ? max(-100, min(119, (int)(top >> 7) - 127 - 8)) : 0;
           f = power2(-e);
-          const int mine = __shfl_sync(0xffffffffu, e, lane % RPI * UPR);
-          if (lane / RPI == i) c *= power2(mine);
+          c *= power2(e);
         }
         auto half = [&](uint32_t w) {  // two values
           if constexpr (FP16) return w ^ flip;
           const float2 x = param_floats(w);
           return Half16<__half>::narrow2(x.x * f, x.y * f) ^ flip;
         };
-        sts128(place(i), make_uint4(half(__byte_perm(v.x, v.z, 0x5410)), half(__byte_perm(v.x, v.z, 0x7632)),
-                                    half(__byte_perm(v.y, v.w, 0x5410)), half(__byte_perm(v.y, v.w, 0x7632))));
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+          const uint4 v = in ? *reinterpret_cast<const uint4*>(src + 8 * u) : make_uint4(0, 0, 0, 0);
+          const uint4 o = make_uint4(half(__byte_perm(v.x, v.z, 0x5410)), half(__byte_perm(v.x, v.z, 0x7632)),
+                                     half(__byte_perm(v.y, v.w, 0x5410)), half(__byte_perm(v.y, v.w, 0x7632)));
+          sts128(dst + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (r & 7)) * 16), o);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(two(qFull, g));
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(two(qFull, g));
-      return c;
-    };
-    auto mine = [&](const PromptPiece& pc) { return pc.row_hi - pc.row_lo > 128 * g && (!SEEN || pc.j1 > pc.j0); };
-    // One piece.  before: steps of the CTA so far, had: of this row tile; next() comes
-    // between the last scores and the results.
-    auto piece = [&](const PromptPiece& pc, int before, int had, float c, auto&& next) {
-      const int row = pc.row_lo + 128 * g + r, steps = pc.j1 - pc.j0;
-      const bool in = row < pc.row_hi;
-      const int tok = row / a.share, gh = row - tok * a.share;
-      int hi = in ? pc.pos0 + tok : -1, lo = a.window > 0 ? pc.pos0 + tok - a.window + 1 : 0;
+      const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+      const uint32_t ts = tmem + lanes + (uint32_t)g * 128u, to = tmem + lanes + 256u + (uint32_t)g * 128u;
       // the keys that every row of this warp sees need no test
-      const int first = pc.row_lo + 128 * g + quad * 32, last = min(first + 31, pc.row_hi - 1);
-      int all_hi = first < pc.row_hi ? pc.pos0 + first / a.share : 0x7fffffff;
-      int all_lo = a.window > 0 && first < pc.row_hi ? pc.pos0 + last / a.share - a.window + 1 : 0;
-      if (SEEN && a.mask) {
-        const SeenRow x = seen_row(a, pc.pos0, in ? pc.news : 0, tok, in ? pc.begin + tok : 0);
-        hi = in ? x.hi : -1;
-        lo = x.lo;
-        all_hi = first < pc.row_hi ? pc.pos0 - 1 : 0x7fffffff;
-        all_lo = __reduce_max_sync(0xffffffffu, in ? lo : -(1 << 30));
-      }
-      if (SEEN && c == 0.0f) c = 0x1p-140f;  // 0 times the hidden scores' infinity would be NaN
+      const int first = row_lo + 128 * g + quad * 32, last = min(first + 31, row_hi - 1);
+      const int all_hi = first < row_hi ? q.pos0 + first / a.share : 0x7fffffff;
+      const int all_lo = a.window > 0 && first < row_hi ? q.pos0 + last / a.share - a.window + 1 : 0;
       float ref = 0.0f, l = 0.0f;
       bool any = false, ok = true;
-      for (int jj = 0; jj < steps; ++jj) {
-        if (!(ok = wait(two(sFull, g), had + jj))) break;
+      int j = 0;
+      for (; j < steps; ++j) {
+        if (!(ok = wait(two(sFull, g), j))) break;
         tc_fence_after();
-        const int j = before + jj;
-        const int key0 = slot_at(pc, 2 * (pc.j0 + jj)) * kKv4Page;
+        const int key0 = (page0 + 2 * j) * kKv4Page;
         const uint32_t absent = s_absent[j & 7];
         const uint32_t rg = range(j);
         // (a page's V in bf16, so P too: tested in the masked form only)
-        bool masked, hides = false;
-        int key1 = 0;
-        if constexpr (SEEN) {
-          key1 = slot_at(pc, 2 * (pc.j0 + jj) + 1) * kKv4Page;
-          auto whole = [&](int k) { return k + kKv4Page - 1 <= all_hi && (k >= all_lo || k + kKv4Page <= a.sinks); };
-          hides = absent || !whole(key0) || !whole(key1);
-          masked = (rg & 0x202u) != 0;
-        } else {
-          masked = absent || key0 + 127 > all_hi || key0 < all_lo || (rg & 0x202u);
-        }
+        const bool masked = absent || key0 + 127 > all_hi || key0 < all_lo || (rg & 0x202u);
         if (rg & 0x101u) {  // keys with scales of their own
 #pragma unroll 1
           for (int c0 = rg & 1u ? 0 : 64; c0 < (rg & 0x100u ? 128 : 64); c0 += 16) {
@@ -927,26 +648,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
           }
           tmem_st_wait();
         }
-        if (SEEN && hides) {
-          // Hidden scores become -infinity in tensor memory, so that one form of what
-          // follows serves all steps: two would not stay in the instruction cache.
-          const SeenRow x = {hi, lo, pc.pos0, pc.news, a.mask && in ? a.mask + (size_t)(pc.begin + tok) * a.words : nullptr};
-#pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            const uint32_t w = (absent >> (c0 >> 6)) & 1u ? 0u : seen_word(x, a, (c0 < 64 ? key0 : key1) + (c0 & 32));
-            uint32_t v[32];
-            tmem_ld32(ts + (uint32_t)c0, v);
-            tmem_ld_wait32(v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((w >> i) & 1u)) v[i] = 0xff800000u;
-            tmem_st16(ts + (uint32_t)c0, v);
-            tmem_st16(ts + (uint32_t)c0 + 16u, v + 16);
-          }
-          tmem_st_wait();
-        }
         auto seen = [&](int i) {
-          if (SEEN) return true;
           const int key = key0 + i;
           return key <= hi && key >= lo && !((absent >> (i >> 6)) & 1u);
         };
@@ -956,7 +658,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         float m0 = -INFINITY, m1 = -INFINITY;
         tmem_ld32(ts, s[0]);
         auto top = [&](const uint32_t* v, int c0) {
-          if (!SEEN && masked) {
+          if (masked) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (seen(c0 + i)) m0 = fmaxf(m0, __uint_as_float(v[i]));
@@ -982,7 +684,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         if (__any_sync(0xffffffffu, grows && any)) {  // rescale the sums so far
           const float fix = grows && any ? exp2_approx(ref - mc) : 1.0f;
           l *= fix;
-          if (!(ok = wait(two(pvDone, g), had + jj - 1))) break;
+          if (!(ok = wait(two(pvDone, g), j - 1))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 16) {
@@ -1041,189 +743,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(Kv4Dev kv, con
         __syncwarp();
         if (lane == 0) mbar_arrive(two(pFull, g));
       }
-      if (ok) next();
-      const bool some = !SEEN || steps > 0;
-      if (ok && some) ok = wait(two(pvDone, g), had + steps - 1);
+      if (ok) ok = wait(two(pvDone, g), steps - 1);
       tc_fence_after();
-      if (SEEN && pc.slot >= 0) {  // a part of the tile
-        float* part = seen_parts(a, D, (int)blockIdx.x, pc.slot);
-        const int at = 128 * g + r;
-        if (in) {
-          part[at] = any || l != 0.0f ? ref : -INFINITY;  // (NaN is seen)
-          part[kPromptRows + at] = l;
-        }
-        float* dst = part + 2 * kPromptRows + 4 * at;
-        if (some)
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t v[16];
-            tmem_ld16(to + (uint32_t)c0, v);
-            tmem_ld_wait16(v);
-            if (in && ok)
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<uint4*>(dst + (size_t)(c0 + i) * kPromptRows) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-          }
-        return ok;
-      }
       const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
-      const bool wide_out = (reinterpret_cast<uintptr_t>(a.out[pc.rank]) & 31u) == 0;
-      const size_t at = (size_t)(pc.begin + tok) * a.q_heads + pc.head * a.share + gh;
-#pragma unroll(SEEN ? 1 : D / 16)
-      for (int c0 = 0; c0 < D; c0 += 16) {
-        uint32_t v[16], w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (some) {
-          tmem_ld16(to + (uint32_t)c0, v);
-          tmem_ld_wait16(v);
+      const size_t at = (size_t)(q.begin + tok) * a.q_heads + head * a.share + gh;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            w[i] = Half16<T>::narrow2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
-        }
+      for (int c0 = 0; c0 < D; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(to + (uint32_t)c0, v);
+        tmem_ld_wait16(v);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          w[i] = Half16<T>::narrow2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
         if (in && ok) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out[pc.rank]) + at * D + c0);
-          if (SEEN && wide_out) {  // each store of a warp touches 32 lines: half as many
-            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                         "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                         : "memory");
-          } else {
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-          }
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out[rank]) + at * D + c0);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
-      if (in && ok && a.lse[pc.rank])
-        a.lse[pc.rank][at] = l == 0.0f ? -INFINITY : (ref - kShift + log2f(l)) * 0.69314718055994531f;
-      return ok;
-    };
-    if constexpr (!SEEN) {
-      if (mine(one)) piece(one, 0, 0, load_q(one), [] {});
-    } else {
-      // the next piece's Q is loaded before this one's results are written
-      SeenJoin join = {};
-      float c_next = 0.0f;
-      bool ok = true;
-      auto fetch = [&](int k) {
-        if (!(ok = wait(piece_full(k), k / kSeenRing))) return;
-        const PromptPiece& p = s_piece[k % kSeenRing];
-        if (p.row_hi > 0 && mine(p)) c_next = load_q(p);
-      };
-      fetch(0);
-      for (int k = 0, before = 0, had = 0; ok; ++k) {
-        const PromptPiece& pc = s_piece[k % kSeenRing];
-        if (pc.row_hi == 0) break;
-        if (pc.parts) join = SeenJoin{pc.parts, pc.rank, pc.head, pc.row_lo, pc.row_hi, pc.begin, {0, 0}};
-        const int steps = pc.j1 - pc.j0;
-        if (pc.row_hi - pc.row_lo > 128 * g) {
-          const bool done = piece(pc, before, had, c_next, [&] { fetch(k + 1); });
-          ok = ok && done;
-          had += steps;
-        } else {
-          fetch(k + 1);
-        }
-        before += steps;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(piece_free(k));
-      }
-      if (warp == 6 && lane == 0) seen_joins(a)[blockIdx.x] = join;
+      if (in && ok && a.lse[rank])
+        a.lse[rank][at] = l == 0.0f ? -INFINITY : (ref - kShift + log2f(l)) * 0.69314718055994531f;
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
-}
-
-// Joins the parts of the tiles that were cut.  A CTA takes 32 rows, a lane each, its
-// warps the channels; the results go through shared memory to whole lines.
-constexpr int kSeenJoinThreads = 256, kSeenJoinRows = 32;
-template <typename T, int D>
-__global__ void __launch_bounds__(kSeenJoinThreads, 3) k_kv4_seen_join(const __grid_constant__ AttnArgs a, int ctas) {
-  constexpr int W = kSeenJoinThreads / 32, PER = D / 4 / W, kBatch = 4;  // 16-byte units of a row a warp takes; parts in flight
-  constexpr float kShift = 6.0f;
-  __shared__ int s_list[kDecMaxCtas], s_warp[W];
-  __shared__ uint2 s_out[kSeenJoinRows][D / 4 + 1];
-  pdl_prologue();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const SeenJoin* joins = seen_joins(a);
-  // the tiles that were cut, in order: the same list in every CTA
-  static_assert(kDecMaxCtas <= kSeenJoinThreads, "a thread each");
-  const bool mine = (int)threadIdx.x < ctas && joins[threadIdx.x].parts > 0;
-  const uint32_t there = __ballot_sync(0xffffffffu, mine);
-  if (lane == 0) s_warp[warp] = __popc(there);
-  __syncthreads();
-  int count = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) before += s_warp[w];
-    count += s_warp[w];
-  }
-  if (mine) s_list[before + __popc(there & ((1u << lane) - 1u))] = (int)threadIdx.x;
-  __syncthreads();
-  constexpr int kChunks = kPromptRows / kSeenJoinRows;
-  for (int item = blockIdx.x; item < count * kChunks; item += gridDim.x) {
-    const int cta = s_list[item / kChunks], row0 = item % kChunks * kSeenJoinRows, row = row0 + lane;
-    const SeenJoin j = joins[cta];
-    if (j.row_lo + row0 >= j.row_hi) continue;
-    const bool in = j.row_lo + row < j.row_hi;
-    auto part = [&](int i) { return seen_parts(a, D, cta + i, i == 0 ? 1 : 0); };
-    float m = -INFINITY;  // the row's largest reference
-    for (int i0 = 0; i0 < j.parts; i0 += 8) {
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = in && i0 + i < j.parts ? part(i0 + i)[row] : -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, x[i]);
-    }
-    const float mu = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    float4 o[PER];
-#pragma unroll
-    for (int x = 0; x < PER; ++x) o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = 0; i0 < j.parts; i0 += kBatch) {
-      float f[kBatch], pl[kBatch];
-      float4 v[kBatch][PER];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const bool has = in && i0 + b < j.parts;
-        const float* p = part(has ? i0 + b : 0);
-        const float ref = has ? p[row] : -INFINITY;
-        const bool some = ref != -INFINITY;  // (nothing was written where no key was seen)
-        f[b] = some ? ref : -INFINITY;
-        pl[b] = some ? p[kPromptRows + row] : 0.0f;
-#pragma unroll
-        for (int x = 0; x < PER; ++x)
-          v[b][x] = some ? *reinterpret_cast<const float4*>(p + 2 * kPromptRows + 4 * ((size_t)(warp + W * x) * kPromptRows + row))
-                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const float w = exp2_approx(f[b] - mu);
-        l = fmaf(w, pl[b], l);
-#pragma unroll
-        for (int x = 0; x < PER; ++x) {
-          o[x].x = fmaf(w, v[b][x].x, o[x].x);
-          o[x].y = fmaf(w, v[b][x].y, o[x].y);
-          o[x].z = fmaf(w, v[b][x].z, o[x].z);
-          o[x].w = fmaf(w, v[b][x].w, o[x].w);
-        }
-      }
-    }
-    const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
-#pragma unroll
-    for (int x = 0; x < PER; ++x)
-      s_out[lane][warp + W * x] = make_uint2(Half16<T>::narrow2(o[x].x * inv, o[x].y * inv), Half16<T>::narrow2(o[x].z * inv, o[x].w * inv));
-    auto at = [&](int x) {
-      const int y = j.row_lo + row0 + x, tok = y / a.share;
-      return (size_t)(j.begin + tok) * a.q_heads + j.head * a.share + (y - tok * a.share);
-    };
-    if (warp == 0 && in && a.lse[j.rank]) a.lse[j.rank][at(lane)] = l == 0.0f ? -INFINITY : (mu - kShift + log2f(l)) * 0.69314718055994531f;
-    __syncthreads();
-    for (int e = threadIdx.x; e < kSeenJoinRows * (D / 4); e += kSeenJoinThreads) {
-      const int x = e / (D / 4), d4 = e % (D / 4);
-      if (j.row_lo + row0 + x < j.row_hi)
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.out[j.rank]) + at(x) * D + 4 * d4) = s_out[x][d4];
-    }
-    __syncthreads();
-  }
 }
 
 }  // namespace dcc
