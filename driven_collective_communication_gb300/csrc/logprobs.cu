@@ -13,24 +13,34 @@
 // the lowest number, keys are all different, and the k largest do not depend on the
 // order in which they were met.  A CTA holds a threshold (a key that k others are
 // known to reach) and a buffer of the keys above it.  The first threshold comes
-// from the first batch: of each warp's 32 largest (one a lane) the j-th, and of the
-// warps' the smallest, is reached by 8 j >= k tokens.  Where the buffer fills, it
-// is cut to its k largest (a key's place is the number of keys above it), and the
-// k-th becomes the threshold; so most batches only compare their maximum with it.
+// from the first batch: each thread's largest value, of these the largest few of
+// each warp, of those the k-th, which k tokens reach.  After the first batch, and
+// where the buffer has grown, it is cut to its k largest (a key's place is the
+// number of keys above it), and the k-th becomes the threshold: about k (1 + ln of
+// the batches) tokens a row pass it, and the others cost one comparison a batch.
 //
 // Work split.  A row is cut into batches that each lie in one rank's shard, and a
 // CTA takes a run of them (a whole row, where rows fill the GPU): nothing is
 // exchanged but 16 bytes and k keys a run, joined by the CTA that comes last.
-// Bound by reading the logits once.
+//
+// Bound by reading the logits once (6.8 TB/s) if the instructions per token stay
+// below some 8; measured on GB300, fp16, 2048 rows of 152,008 tokens: 119 us
+// without alternatives (5.2 TB/s), 149 with one, 181 with 20 (3.4 TB/s); bf16, 256
+// rows of 131,072: 20, 27 and 36 us; one row: 8 to 15 us.  What is left is the
+// instructions (60 % of the issue slots) and the threads' waits for one another,
+// one a batch.  CTAs of 128 threads, six to an SM: 256 threads with the same
+// registers took 213 us (more warps wait at a barrier), 64 threads 208, and 64
+// registers a thread, which spill, 243 (the first case with 20).
 #include "comm.h"
 #include "kv4.cuh"
+#include "tcgen05.cuh"
 
 namespace dcc {
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpThreads = 128, kLpWarps = kLpThreads / 32;
 constexpr int kLpCap = 1024;      // keys of the buffer
 constexpr int kLpCut = 192;       // keys after a batch from which the buffer is cut
-constexpr int kLpMaxRuns = 1216;  // CTAs of a call whose rows are cut (8 to an SM)
+constexpr int kLpMaxRuns = 912;   // CTAs of a call whose rows are cut: one wave of 6 to an SM
 
 struct LpArgs {
   const void* x[DCC_MAX_RANKS];
@@ -44,40 +54,116 @@ struct LpArgs {
   unsigned long long* keys;   // [row][run][top]
   unsigned long long* status;
   size_t stride;
-  int n, columns, vocab, top, runs, batches /* of a rank's shard */, span /* vectors of a batch */;
+  int n, columns, vocab, top, runs, batches /* of a rank's shard */;
   float scale;
 };
 
+// The numbers of 16 bytes: as pairs, their maximum, and one of them.
 template <typename T>
-struct LpVec;  // the numbers of 16 bytes
+struct LpVec;
 template <>
 struct LpVec<float> {
   static constexpr int N = 4;
-  __device__ static void widen(uint4 v, float* f) {
-    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  __device__ static float2 pair(uint4 v, int i) {
+    return i == 0 ? make_float2(__uint_as_float(v.x), __uint_as_float(v.y)) : make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
+  template <int VPT>
+  __device__ static float top(const uint4* v) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      m = max3(m, __uint_as_float(v[i].x), __uint_as_float(v[i].y));
+      m = max3(m, __uint_as_float(v[i].z), __uint_as_float(v[i].w));
+    }
+    return m;
+  }
+  // a bit for each number that is `least` or more; the numbers of the first n vectors
+  template <int VPT>
+  __device__ static uint32_t reach(const uint4* v, float least) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (__uint_as_float(v[i].x) >= least) r |= 1u << (4 * i);
+      if (__uint_as_float(v[i].y) >= least) r |= 2u << (4 * i);
+      if (__uint_as_float(v[i].z) >= least) r |= 4u << (4 * i);
+      if (__uint_as_float(v[i].w) >= least) r |= 8u << (4 * i);
+    }
+    return r;
+  }
+  __device__ static uint32_t lanes(int n) { return (1u << (4 * n)) - 1u; }
+  // the number of bit x, and its column after the thread's first one
+  template <int VPT>
+  __device__ static float at(const uint4* v, int x, int* col) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (x == 4 * i) w = v[i].x;
+      if (x == 4 * i + 1) w = v[i].y;
+      if (x == 4 * i + 2) w = v[i].z;
+      if (x == 4 * i + 3) w = v[i].w;
+    }
+    *col = x / 4 * (kLpThreads * N) + x % 4;
+    return __uint_as_float(w);
+  }
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  __device__ static float load(const float* p) { return __ldg(p); }
 };
 template <typename T16>
 struct LpVec16 {
   static constexpr int N = 8;
-  __device__ static void widen(uint4 v, float* f) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = Half16<T16>::widen2(u[i]);
-      f[2 * i] = p.x, f[2 * i + 1] = p.y;
+  static constexpr uint32_t kNegInf = std::is_same<T16, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+  __device__ static uint32_t word(uint4 v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+  __device__ static float2 pair(uint4 v, int i) { return Half16<T16>::widen2(word(v, i)); }
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {  // (a NaN loses: it shows in Z)
+    if constexpr (std::is_same<T16, __half>::value) {
+      const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    } else {
+      const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&m);
     }
   }
+  template <int VPT>
+  __device__ static float top(const uint4* v) {
+    uint32_t m = kNegInf;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) m = max2(m, max2(max2(v[i].x, v[i].y), max2(v[i].z, v[i].w)));
+    const float2 f = Half16<T16>::widen2(m);
+    return fmaxf(fmaxf(f.x, f.y), -INFINITY);
+  }
+  // As for 32 bits; bits w and w + 16 are the halves of word w.  `least` is one of
+  // the type's numbers.
+  template <int VPT>
+  __device__ static uint32_t reach(const uint4* v, float least) {
+    const uint32_t l = Half16<T16>::narrow2(least, least);
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * VPT; ++i) r |= reach2(word(v[i / 4], i % 4), l) & (0x00010001u << i);
+    return r;
+  }
+  __device__ static uint32_t reach2(uint32_t a, uint32_t l) {
+    if constexpr (std::is_same<T16, __half>::value)
+      return __hge2_mask(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&l));
+    else
+      return __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&l));
+  }
+  __device__ static uint32_t lanes(int n) { return 0x00010001u * ((1u << (4 * n)) - 1u); }
+  template <int VPT>
+  __device__ static float at(const uint4* v, int x, int* col) {
+    const int i = x & 15;
+    uint32_t w = 0;
+#pragma unroll
+    for (int y = 0; y < 4 * VPT; ++y)
+      if (y == i) w = word(v[y / 4], y % 4);
+    *col = i / 4 * (kLpThreads * N) + i % 4 * 2 + (x >> 4);
+    return Half16<T16>::widen((uint16_t)(x >> 4 ? w >> 16 : w));
+  }
+  __device__ static float load(const T16* p) { return Half16<T16>::widen(__ldg(reinterpret_cast<const uint16_t*>(p))); }
 };
 template <>
 struct LpVec<__half> : LpVec16<__half> {};
 template <>
 struct LpVec<__nv_bfloat16> : LpVec16<__nv_bfloat16> {};
-template <typename T>
-struct LpNegInf {
-  static constexpr uint32_t word = std::is_same<T, float>::value ? 0xff800000u
-                                   : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
-};
 
 __device__ __forceinline__ float lp_exp2(float x) {  // 2^x; -inf gives 0
   float y;
@@ -111,12 +197,28 @@ __device__ __forceinline__ LpSum lp_join(LpSum a, LpSum b, float c) {
   }
   return r;
 }
+// over the CTA's threads, in a fixed order; all get it
+__device__ __forceinline__ LpSum lp_join_cta(LpSum x, float c, LpSum* smem /* kLpWarps */) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    const LpSum other = {__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.z, o),
+                         __shfl_xor_sync(0xffffffffu, x.u, o)};
+    x = lane & o ? lp_join(other, x, c) : lp_join(x, other, c);
+  }
+  if (lane == 0) smem[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = smem[0];
+#pragma unroll 1
+  for (int w = 1; w < kLpWarps; ++w) x = lp_join(x, smem[w], c);
+  return x;
+}
 
 struct LpTop {
   unsigned long long keys[2][kLpCap];
-  unsigned long long thr;
-  uint32_t est[kLpWarps];
-  int count, now;  // keys in buffer `now`
+  unsigned long long thr;  // only keys above it count
+  uint32_t est[kLpWarps * 32];
+  int count, now;          // keys in buffer `now`
 };
 // Cuts the buffer to its k largest keys, in descending order, and raises the
 // threshold to the k-th.  All threads call; the buffer is theirs before and after.
@@ -127,8 +229,14 @@ __device__ __forceinline__ void lp_cut(LpTop& s, int k) {
   for (int i = threadIdx.x; i < n; i += kLpThreads) {
     const unsigned long long key = from[i];
     int above = 0;
+    int j = 0;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) above += from[j] > key;
+    for (; j + 1 < n; j += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(from + j);
+      above += two.x > key;
+      above += two.y > key;
+    }
+    if (j < n) above += from[j] > key;
     if (above < k) to[above] = key;
     if (above == k - 1) s.thr = key;
   }
@@ -144,14 +252,39 @@ __device__ __forceinline__ bool lp_add(LpTop& s, unsigned long long key) {
   if (at < kLpCap) s.keys[s.now][at] = key;
   return at < kLpCap;
 }
+// A first threshold: each warp's j largest of one value a thread (0: none), of all
+// warps' the k-th.  All threads call.
+__device__ __forceinline__ void lp_first(LpTop& s, uint32_t mine, int k) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = min(32, (k + kLpWarps - 1) / kLpWarps + (k > 1 ? 2 : 0)), n = kLpWarps * j;
+  uint32_t keep = 0;
+#pragma unroll 1
+  for (int i = 0; i < j; ++i) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, mine);
+    const unsigned who = __ballot_sync(0xffffffffu, mine == best);
+    if (lane == __ffs(who) - 1) mine = 0u;
+    if (lane == i) keep = best;
+  }
+  if (lane < j) s.est[warp * j + lane] = keep;
+  __syncthreads();
+  if ((int)threadIdx.x < n) {
+    const uint32_t x = s.est[threadIdx.x];
+    int above = 0;  // before it in descending order
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) above += s.est[i] > x || (s.est[i] == x && i < (int)threadIdx.x);
+    if (above == k - 1 && x) s.thr = ((unsigned long long)x << 32) - 1;
+  }
+  __syncthreads();
+}
 
 template <typename T, int VPT>
-__global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_constant__ LpArgs a) {
-  constexpr int E = LpVec<T>::N;
-  __shared__ LpTop s;
+__global__ void __launch_bounds__(kLpThreads, 6) k_token_logprobs(const __grid_constant__ LpArgs a) {
+  using Vec = LpVec<T>;
+  constexpr int E = Vec::N;
+  __shared__ __align__(16) LpTop s;
   __shared__ LpSum s_sum[kLpWarps];
   __shared__ int s_last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = a.top;
+  const int k = a.top;
   const int row = (int)(blockIdx.x / (unsigned)a.runs), run = (int)(blockIdx.x % (unsigned)a.runs);
   const float c = a.scale * 1.44269504088896341f;
   if (threadIdx.x == 0) {
@@ -164,53 +297,75 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
   const int all = a.n * a.batches;
   const int b0 = (int)((long long)all * run / a.runs), b1 = (int)((long long)all * (run + 1) / a.runs);
   LpSum sum = {-INFINITY, 0.0f, 0.0f};
+  // A rank's part of the row: `head` columns up to the first whole vector, nv vectors,
+  // and what is left.  Batch g holds the vectors from g * kGroup on; the one that is
+  // not full, also the columns outside the vectors, one a thread.
+  constexpr int kGroup = kLpThreads * VPT;
+  struct Part {
+    const T* p;
+    int rank, valid, head, nv;
+  };
+  auto part = [&](int rank) {
+    Part x;
+    x.rank = rank;
+    x.p = static_cast<const T*>(a.x[rank]) + (size_t)row * a.stride;
+    x.valid = max(0, min(a.columns, a.vocab - rank * a.columns));
+    x.head = min(x.valid, (int)((16u - (reinterpret_cast<uintptr_t>(x.p) & 15u)) % 16u / sizeof(T)));
+    x.nv = (x.valid - x.head) / E;
+    return x;
+  };
+  struct Batch {
+    int rank, first, mine;  // the thread's first column, and vectors
+    int extra;              // its column outside the vectors, or -1
+    float x;
+  };
   uint4 next[VPT];
-  // a batch's 16-byte vectors; what does not belong to the row is -infinity
-  auto fetch = [&](int b) {
-    const int rank = b / a.batches, v0 = (b - rank * a.batches) * a.span;
-    const T* p = static_cast<const T*>(a.x[rank]) + (size_t)row * a.stride;
-    const int before = (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));  // of the first vector, not the row's
-    const int valid = max(0, min(a.columns, a.vocab - rank * a.columns));
+  Batch then;
+  auto fetch = [&](const Part& x, int g) {
+    const int v0 = g * kGroup, left = x.nv - v0;
+    const uint4* q = reinterpret_cast<const uint4*>(x.p + x.head) + v0 + (int)threadIdx.x;
+    then.rank = x.rank;
+    then.first = x.head + (v0 + (int)threadIdx.x) * E;
+    then.extra = -1;
+    then.x = -INFINITY;
+    if (left >= kGroup) {
+      then.mine = VPT;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * kLpThreads + (int)threadIdx.x, e0 = (v0 + v) * E - before;
-      uint4 w = make_uint4(LpNegInf<T>::word, LpNegInf<T>::word, LpNegInf<T>::word, LpNegInf<T>::word);
-      if (v < a.span && e0 < valid && e0 + E > 0) {
-        if (e0 >= 0 && e0 + E <= valid) {
-          w = __ldcs(reinterpret_cast<const uint4*>(p + e0));
-        } else {
-          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      for (int i = 0; i < VPT; ++i) next[i] = __ldcs(q + i * kLpThreads);
+    } else {
+      then.mine = max(0, min(VPT, (left - (int)threadIdx.x + kLpThreads - 1) / kLpThreads));
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (e0 + e >= 0 && e0 + e < valid) {
-              if constexpr (sizeof(T) == 4) {
-                u[e] = __ldg(reinterpret_cast<const uint32_t*>(p) + e0 + e);
-              } else {
-                const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(p) + e0 + e);
-                u[e / 2] = e & 1 ? (u[e / 2] & 0xffffu) | h << 16 : (u[e / 2] & 0xffff0000u) | h;
-              }
-            }
-          w = make_uint4(u[0], u[1], u[2], u[3]);
-        }
+      for (int i = 0; i < VPT; ++i)
+        if (i < then.mine) next[i] = __ldcs(q + i * kLpThreads);
+      if (left >= 0 && (int)threadIdx.x < x.valid - x.nv * E) {
+        then.extra = (int)threadIdx.x < x.head ? (int)threadIdx.x : x.nv * E + (int)threadIdx.x;
+        then.x = Vec::load(x.p + then.extra);
       }
-      next[i] = w;
     }
   };
-  if (b0 < b1) fetch(b0);
+  int held = 0;  // keys of the buffer, at most
+  Part at = part(b0 / a.batches);
+  int g = b0 % a.batches;
+  fetch(at, g);  // (every run has a batch)
   for (int b = b0; b < b1; ++b) {
     uint4 v[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) v[i] = next[i];
-    if (b + 1 < b1) fetch(b + 1);
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      float f[E];
-      LpVec<T>::widen(v[i], f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) top = fmaxf(top, f[e]);
+    const Batch now = then;
+    if (b + 1 < b1) {
+      if (++g == a.batches) {
+        g = 0;
+        at = part(at.rank + 1);
+      }
+      fetch(at, g);
     }
-    // sums
+    if (now.mine < VPT) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (i >= now.mine) v[i] = make_uint4(Vec::kNegInf, Vec::kNegInf, Vec::kNegInf, Vec::kNegInf);
+    }
+    const float top = fmaxf(Vec::template top<VPT>(v), now.x);
+    // sums (the difference first: the values may be as large as the type holds)
     const float m = fmaxf(sum.m, top), ref = m == -INFINITY ? 0.0f : m;
     if (m > sum.m) {
       const float d = sum.m == -INFINITY ? 0.0f : (sum.m - m) * c, f = lp_exp2(d);
@@ -218,116 +373,84 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
       sum.z *= f;
       sum.m = m;
     }
-    float z0 = 0.0f, z1 = 0.0f, u0 = 0.0f, u1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      float f[E];
-      LpVec<T>::widen(v[i], f);
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float da = (f[e] - ref) * c, db = (f[e + 1] - ref) * c, pa = lp_exp2(da), pb = lp_exp2(db);
-        z0 += pa;
-        z1 += pb;
-        u0 = fmaf(pa, fmaxf(da, -1000.0f), u0);  // (0 times infinity)
-        u1 = fmaf(pb, fmaxf(db, -1000.0f), u1);
-      }
+    if (now.extra >= 0) {
+      const float d = (now.x - ref) * c, e = lp_exp2(d);
+      sum.z += e;
+      sum.u = fmaf(e, fmaxf(d, -1000.0f), sum.u);
     }
-    sum.z += z0 + z1;
-    sum.u += u0 + u1;
+    float2 z = make_float2(0.0f, 0.0f), u = z;
+    const float2 cc = make_float2(c, c), nr = make_float2(-ref, -ref);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (i < now.mine)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const float2 d = mul2(add2(Vec::pair(v[i], e), nr), cc);
+          const float2 w = make_float2(lp_exp2(d.x), lp_exp2(d.y));
+          z = add2(z, w);
+          u = fma2(w, d, u);
+        }
+    const float zb = z.x + z.y;
+    float ub = u.x + u.y;
+    if (!(ub - ub == 0.0f)) {  // 0 times a hidden token's infinity, or NaN: once more, with care
+      u = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (i < now.mine)
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            const float2 d = mul2(add2(Vec::pair(v[i], e), nr), cc);
+            u = fma2(make_float2(lp_exp2(d.x), lp_exp2(d.y)), make_float2(fmaxf(d.x, -1000.0f), fmaxf(d.y, -1000.0f)), u);
+          }
+      ub = u.x + u.y;
+    }
+    sum.z += zb;
+    sum.u += ub;
     if (k == 0) continue;
     // top alternatives
-    const int rank = b / a.batches, v0 = (b - rank * a.batches) * a.span;
-    const int before =
-        (int)((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x[rank]) + (size_t)row * a.stride) & 15u) / sizeof(T));
-    const int valid = max(0, min(a.columns, a.vocab - rank * a.columns));
-    if (b == b0) {
-      const int j = (k + kLpWarps - 1) / kLpWarps;
-      bool some = false;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int x = i * kLpThreads + (int)threadIdx.x, e0 = (v0 + x) * E - before;
-        some |= x < a.span && e0 < valid && e0 + E > 0;
-      }
-      uint32_t mine = some ? lp_order(top) : 0u, best = 0u;
-      for (int i = 0; i < j; ++i) {
-        best = __reduce_max_sync(0xffffffffu, mine);
-        const unsigned who = __ballot_sync(0xffffffffu, mine == best);
-        if (lane == __ffs(who) - 1) mine = 0u;
-      }
-      if (lane == 0) s.est[warp] = best;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        uint32_t least = 0xffffffffu;
-        int warps = 0;
-        for (int w = 0; w < kLpWarps; ++w)
-          if (s.est[w]) {
-            least = min(least, s.est[w]);
-            ++warps;
-          }
-        if (warps * j >= k) s.thr = ((unsigned long long)least << 32) - 1;  // least > 0
-      }
-      __syncthreads();
-    }
-    unsigned long long thr = s.thr;
+    if (s.thr == 0) lp_first(s, now.mine > 0 || now.extra >= 0 ? lp_order(top) : 0u, k);
     uint32_t pending = 0;
-    if (lp_order(top) >= (uint32_t)(thr >> 32)) {
-      const float least = lp_value((uint32_t)(thr >> 32));
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        float f[E];
-        LpVec<T>::widen(v[i], f);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (!(f[e] < least)) pending |= 1u << (i * E + e);
-      }
+    bool extra = false;
+    const uint32_t first = (uint32_t)((s.thr + 1) >> 32);  // the least value that may count
+    if (lp_order(top) >= first) {
+      const float least = first ? lp_value(first) : -INFINITY;
+      pending = Vec::template reach<VPT>(v, least);
+      if (now.mine < VPT) pending &= Vec::lanes(now.mine);
+      extra = now.extra >= 0 && now.x >= least;
     }
-    // the places of pending tokens go down as they are added; where the buffer is
-    // full it is cut, and those that are left try again
-    bool again;
-    do {
-      thr = s.thr;
-      __syncthreads();  // all have read it, and the count after the last batch
+    // The bits go as their tokens are added.  Only where the buffer might be too small
+    // the threads look together whether it was: then it is cut, and those that are
+    // left try again.
+    int adders = __syncthreads_count(pending != 0 || extra);
+    while (adders) {
+      const unsigned long long thr = s.thr;
+      const uint32_t id0 = (uint32_t)(now.rank * a.columns);
       while (pending) {
-        const int x = __ffs(pending) - 1, i = x / E, e = x % E;
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int y = 0; y < VPT; ++y)
-          if (y == i) w[0] = v[y].x, w[1] = v[y].y, w[2] = v[y].z, w[3] = v[y].w;
-        float f;
-        if constexpr (sizeof(T) == 4) {
-          f = __uint_as_float(e == 0 ? w[0] : e == 1 ? w[1] : e == 2 ? w[2] : w[3]);
-        } else {
-          const uint32_t p = e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3];
-          f = Half16<T>::widen((uint16_t)(e & 1 ? p >> 16 : p));
-        }
-        const int q = i * kLpThreads + (int)threadIdx.x, col = (v0 + q) * E - before + e;
-        if (q < a.span && col >= 0 && col < valid) {
-          const unsigned long long key = lp_key(f, (uint32_t)(rank * a.columns + col));
-          if (key > thr && !lp_add(s, key)) break;
-        }
+        const int x = __ffs(pending) - 1;
+        int col;
+        const float f = Vec::template at<VPT>(v, x, &col);
+        const unsigned long long key = lp_key(f, id0 + (uint32_t)(now.first + col));
+        if (key > thr && !lp_add(s, key)) break;
         pending &= pending - 1;
       }
-      again = __syncthreads_or(pending != 0);
-      if (again || s.count > kLpCut) lp_cut(s, k);
-    } while (again);
+      if (extra) {
+        const unsigned long long key = lp_key(now.x, id0 + (uint32_t)now.extra);
+        extra = key > thr && !lp_add(s, key);
+      }
+      held += adders * (VPT * E + 1);
+      if (held <= kLpCap) break;
+      adders = __syncthreads_count(pending != 0 || extra);
+      held = s.count;
+      if (adders || held > kLpCut || held > k + k) {
+        lp_cut(s, k);
+        held = s.count;
+      }
+    }
   }
 
   // ---- the CTA's sums
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const LpSum other = {__shfl_xor_sync(0xffffffffu, sum.m, o), __shfl_xor_sync(0xffffffffu, sum.z, o),
-                         __shfl_xor_sync(0xffffffffu, sum.u, o)};
-    sum = lane & o ? lp_join(other, sum, c) : lp_join(sum, other, c);
-  }
-  if (lane == 0) s_sum[warp] = sum;
-  if (k) {
-    __syncthreads();
-    lp_cut(s, k);
-  }
-  __syncthreads();
-  sum = s_sum[0];
-#pragma unroll
-  for (int w = 1; w < kLpWarps; ++w) sum = lp_join(sum, s_sum[w], c);
+  sum = lp_join_cta(sum, c, s_sum);  // (and everything is in the buffer)
+  if (k) lp_cut(s, k);
 
   if (a.runs > 1) {  // join the runs of the row
     const size_t at = (size_t)row * a.runs + run;
@@ -343,10 +466,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
     if (!s_last) return;
     __threadfence();
     sum = LpSum{-INFINITY, 0.0f, 0.0f};
-    for (int i = 0; i < a.runs; ++i) {
+    for (int i = threadIdx.x; i < a.runs; i += kLpThreads) {
       const float4 p = __ldcg(&a.sums[(size_t)row * a.runs + i]);
       sum = lp_join(sum, LpSum{p.x, p.y, p.z}, c);
     }
+    sum = lp_join_cta(sum, c, s_sum);
     if (k) {
       const unsigned long long* keys = a.keys + (size_t)row * a.runs * k;
       if (threadIdx.x == 0) {
@@ -354,11 +478,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
         s.thr = 0;
       }
       __syncthreads();
-      // k tokens reach the largest of the runs' k-th keys
-      for (int i = threadIdx.x; i < a.runs; i += kLpThreads) {
-        const unsigned long long last = __ldcg(keys + (size_t)i * k + k - 1);
-        if (last) atomicMax(&s.thr, last - 1);
+      // k tokens reach the k-th of the runs' first keys, and the largest of their k-th
+      uint32_t best = 0;
+      unsigned long long last = 0;
+      // (neighbouring runs in different warps)
+      for (int i = (threadIdx.x & 31) * kLpWarps + (threadIdx.x >> 5); i < a.runs; i += kLpThreads) {
+        best = max(best, (uint32_t)(__ldcg(keys + (size_t)i * k) >> 32));
+        last = max(last, __ldcg(keys + (size_t)i * k + k - 1));
       }
+      lp_first(s, best, k);
+      if (last) atomicMax(&s.thr, last - 1);
       __syncthreads();
       for (int i0 = 0; i0 < a.runs * k; i0 += kLpThreads) {
         const unsigned long long thr = s.thr;
@@ -387,10 +516,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
         lp = nan;
       } else if (t >= 0) {
         const int rank = t / a.columns;
-        const T* p = static_cast<const T*>(a.x[rank]) + (size_t)row * a.stride + (t - rank * a.columns);
-        float x;
-        if constexpr (sizeof(T) == 4) x = __ldg(reinterpret_cast<const float*>(p));
-        else x = Half16<T>::widen(__ldg(reinterpret_cast<const uint16_t*>(p)));
+        const float x = Vec::load(static_cast<const T*>(a.x[rank]) + (size_t)row * a.stride + (t - rank * a.columns));
         lp = none ? nan : fmaf(x - sum.m, a.scale, -lz);
       }
       a.logprob[row] = lp;
@@ -481,14 +607,12 @@ int dcc_token_logprobs(int n_ranks, const void* const* logits, size_t tokens, si
   a.vocab = (int)vocab;
   a.top = top;
   a.scale = scale;
-  // A shard's vectors, and one more where rows do not begin on one.  Batches are
-  // four vectors a thread, or one where the GPU would not be full otherwise.
-  const long long vectors = (long long)((columns * size + 15) / 16 + 1);
-  const long long runs_wanted = dcc::kLpMaxRuns / (long long)tokens;  // of a row
+  // A shard's vectors in batches of four a thread, or one where the GPU would not be
+  // full otherwise; the last one is not full.
+  const long long vectors = (long long)((columns * size + 15) / 16), runs_wanted = dcc::kLpMaxRuns / (long long)tokens;  // of a row
   const auto batches = [&](int per) { return (vectors + per * dcc::kLpThreads - 1) / (per * dcc::kLpThreads); };
   const int per = n_ranks * batches(4) < runs_wanted ? 1 : 4;
   a.batches = (int)batches(per);
-  a.span = (int)((vectors + a.batches - 1) / a.batches);
   const long long all = (long long)n_ranks * a.batches;
   a.runs = (int)(runs_wanted < 1 ? 1 : runs_wanted < all ? runs_wanted : all);
   const int type = t == DCC_FP32 ? 0 : t == DCC_FP16 ? 1 : 2;
