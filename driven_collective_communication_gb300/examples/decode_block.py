@@ -63,14 +63,20 @@ class Block:
             dcc.dcc_linear(self.w_qkv, [x] * n, b["qkv"], bias=self.b_qkv)
             heads = [t.view(T, Hq + 2 * Hkv, D) for t in b["qkv"]]
             self.cache.append([t[:, Hq:Hq + Hkv] for t in heads], [t[:, Hq + Hkv:] for t in heads], start)
-            self.cache.attention([t[:, :Hq] for t in heads], [t.view(T, Hq, D) for t in b["attn"]], start, max_new,
-                                 self.ws_attention)
+            self.attend([t[:, :Hq] for t in heads], [t.view(T, Hq, D) for t in b["attn"]], start, max_new)
             self._row_parallel(comm, self.w_out, b["attn"], b["h"], T)
             x = norm(b["h"][0])
             dcc.dcc_linear(self.w_up, [x] * n, b["up"], bias=self.b_up, act="silu")
             self._row_parallel(comm, self.w_down, b["up"], b["h"], T)
             assert comm.check() == dcc.DCC_OK and dcc.dcc_local_check() == dcc.DCC_OK
         return b["h"][0].clone()
+
+    def attend(self, q, out, start, max_new):
+        self.cache.attention(q, out, start, max_new, self.ws_attention)
+
+    def unseen(self, s, length, t):
+        """[t, length]: the positions that sequence s's t newest rows do not see."""
+        return torch.arange(length, device="cuda")[None, :] > torch.arange(length - t, length, device="cuda")[:, None]
 
     def _row_parallel(self, comm, weight, x, h, tokens):
         """h <- h + sum over ranks of x W^T, at most 256 tokens at a time."""
@@ -109,8 +115,7 @@ class Block:
             row = 0
             for s, t in enumerate(news):
                 keys, vals = k[r][whole[s]:whole[s + 1]].float(), v[r][whole[s]:whole[s + 1]].float()
-                pos = torch.arange(lens[s] - t, lens[s], device="cuda")[:, None]
-                hide = torch.arange(lens[s], device="cuda")[None, :] > pos
+                hide = self.unseen(s, lens[s], t)
                 for q in range(Hq):
                     g = q // (Hq // Hkv)
                     score = (qkv[row:row + t, q] @ keys[:, g].T * D ** -0.5).masked_fill(hide, float("-inf"))
