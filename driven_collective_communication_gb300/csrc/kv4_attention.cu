@@ -137,8 +137,10 @@ int attention_call(const dcc_kv4_t* kv, int layer, void* const* q, void* const* 
   cudaStream_t st = static_cast<cudaStream_t>(s);
   const long long heads = (long long)kv->n_ranks * kv->kv_heads;
   dcc::AttnPlan p = {};
-  if (seen) p = dcc::seen_plan(heads, kv->seqs, kv->max_pages, kv->head_dim, (long long)max_new * a.share, sms);
-  else p = dcc::attn_plan(heads, kv->seqs, kv->max_pages, kv->head_dim, a.share, (long long)tokens, max_new, sms);
+  if (seen)
+    p = dcc::seen_plan(heads, kv->seqs, kv->max_pages, kv->head_dim, a.share, (long long)tokens, max_new, a.window, a.sinks, sms);
+  else
+    p = dcc::attn_plan(heads, kv->seqs, kv->max_pages, kv->head_dim, a.share, (long long)tokens, max_new, sms);
   if (p.prompt) {
     const dcc::AttnKernel k = dcc::attn_kernel(fp16, seen, kv->head_dim, kv->group, dcc::kAttnPrompt);
     if (dcc_host::max_active_per_sm(k.fn, k.threads, k.smem) < 1) return DCC_ERR_LAUNCH;

@@ -215,6 +215,16 @@ struct DecSeq {
   // row, the others go on at page0 + kept; and the new tokens
   int kept, news;
 };
+// The next sequence after s that has rows, or kv.seqs; a whole warp looks.
+__device__ __forceinline__ int next_with_rows(const Kv4Dev& kv, const AttnArgs& a, int s) {
+  const int lane = threadIdx.x & 31;
+  for (int s0 = s + 1; s0 < kv.seqs; s0 += 32) {
+    const int x = s0 + lane;
+    const unsigned some = __ballot_sync(0xffffffffu, x < kv.seqs && min(a.tokens, a.start[x + 1]) > max(0, a.start[x]));
+    if (some) return s0 + __ffs(some) - 1;
+  }
+  return kv.seqs;
+}
 // the table's slot of a sequence's page, both counted from page0
 __device__ __forceinline__ int dec_slot_of(const DecSeq& q, int slot) { return slot - q.page0 < q.kept ? slot - q.page0 : slot; }
 template <bool SEEN>
@@ -431,10 +441,15 @@ __global__ void __launch_bounds__(DecShape<D, G, RT, SMALL>::warps * 32, DecShap
     DecSeq q = c.q;
     if (seg >= nh * q.tiles) {
       seg = 0;
-      do {
-        ++s;
+      if constexpr (SEEN) {
+        s = next_with_rows(kv, a, s);
         if (s < kv.seqs) q = dec_seq<SEEN>(kv, a, s, ROWS);
-      } while (s < kv.seqs && q.pages == 0);
+      } else {
+        do {
+          ++s;
+          if (s < kv.seqs) q = dec_seq<SEEN>(kv, a, s, ROWS);
+        } while (s < kv.seqs && q.pages == 0);
+      }
     }
     put(c, s, seg, q);
   };

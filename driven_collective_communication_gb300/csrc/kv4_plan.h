@@ -42,11 +42,23 @@ inline void stream_plan(AttnPlan* p, long long n_heads, long long seqs, long lon
   p->small = rows <= 8 && n_heads * seqs * max_pages <= sms * kDecSmallWarps;
 }
 
-// Rows with sets of seen keys of their own: the prompt kernel splits such calls
-// evenly, so it takes all that need more than one pass of the streaming kernel.
-inline AttnPlan seen_plan(long long n_heads, long long seqs, long long max_pages, int dim, long long rows, long long sms) {
+// Rows with sets of seen keys of their own (trees, windows with sinks).  Their
+// kernel of many rows splits any call evenly over the SMs, so what counts is how
+// often the streaming kernel goes over the keys: once, it is the faster one; twice,
+// it is where an SM has more than some 16 steps of 128 keys (the other's start
+// and joins no longer show); three times, never.  Measured, streaming / other, us, 8
+// heads per kv head: 128 channels, 32 rows, 8 x 700 keys (segments x keys) 20.7 /
+// 17.5, 8 x 8192 32.9 / 30.7, 128 x 2048 65 / 61, 512 x 4096 254 / 312, 8 x 65,536 75
+// / 84; 48 rows (three times) 23.0 / 17.8, 34.8 / 32.4, 87 / 62, 370 / 315, 102 / 87.
+// 64 channels, 48 rows, the same: 19.4 / 13.6, 29.3 / 22.7, 53 / 43, 194 / 218, 58 / 63.
+inline AttnPlan seen_plan(long long n_heads, long long seqs, long long max_pages, int dim, long long share, long long tokens,
+                          long long max_new, long long window, long long sinks, long long sms) {
   AttnPlan p = {};
-  p.prompt = rows > (dim == 64 ? 24 : 16);
+  const long long rows = max_new * share, tile = dim == 64 ? 24 : 16, passes = (rows + tile - 1) / tile;
+  long long full = (tokens + max_new - 1) / max_new, pages = max_pages;  // sequences, as below
+  if (full > seqs) full = seqs;
+  if (window > 0 && (window + sinks + max_new) / 64 + 1 < pages) pages = (window + sinks + max_new) / 64 + 1;
+  p.prompt = passes > 2 || (passes == 2 && n_heads * full * pages <= 32 * sms);
   if (!p.prompt) stream_plan(&p, n_heads, seqs, max_pages, dim, rows, sms);
   return p;
 }

@@ -38,16 +38,12 @@ struct SeenWalk {
   long long units;   // of the line
   int ctas;
   int s, seg, j;     // the sequence, its tile (rank and head slowest), the step within
+  bool over;         // that was the sequence's last tile
 };
-// The next piece of a run (one thread).
+// The next piece of a run, whose sequence has tiles from w.seg on (one thread).
 __device__ __forceinline__ bool seen_next(const Kv4Dev& kv, const AttnArgs& a, SeenWalk& w, PromptPiece& p) {
   if (w.u >= w.end) return false;
-  const int nh = kv.n * kv.heads;
-  DecSeq q = dec_seq<true>(kv, a, w.s, kPromptRows);
-  while (w.seg >= nh * q.tiles) {  // on to the next sequence that has rows
-    q = dec_seq<true>(kv, a, ++w.s, kPromptRows);
-    w.seg = 0;
-  }
+  const DecSeq q = dec_seq<true>(kv, a, w.s, kPromptRows);
   const int rh = w.seg / q.tiles, tile = w.seg - rh * q.tiles, steps = seen_tile_steps(a, q);
   p.seq = w.s;
   p.rank = rh / kv.heads;
@@ -80,6 +76,7 @@ __device__ __forceinline__ bool seen_next(const Kv4Dev& kv, const AttnArgs& a, S
   w.u += take;
   w.j = 0;
   ++w.seg;
+  w.over = w.seg >= kv.n * kv.heads * q.tiles;
   return true;
 }
 // what a call's workspace holds after the streaming kernel's counters
@@ -213,7 +210,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
       if (mine && first * nh <= c0 && c0 < (first + mine) * nh) {
         const int steps = seen_tile_steps(a, dec_seq<true>(kv, a, s, kPromptRows));
         const long long in = c0 - first * nh;
-        s_walk = SeenWalk{c0, c1, units, C, s, (int)(in / steps), (int)(in % steps)};
+        s_walk = SeenWalk{c0, c1, units, C, s, (int)(in / steps), (int)(in % steps), false};
       }
     }
   }
@@ -285,6 +282,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
       // have been loaded.
       auto publish = [&](int k) {
         if (k >= kSeenRing && !wait(piece_free(k), k / kSeenRing - 1)) return false;
+        if (s_walk.over) {  // on to the next sequence that has rows
+          const int s = next_with_rows(kv, a, s_walk.s);
+          __syncwarp();  // all have read the walk
+          if (lane == 0) s_walk.s = s, s_walk.seg = 0, s_walk.over = false;
+        }
+        __syncwarp();
         if (lane == 0) {
           PromptPiece& p = s_piece[k % kSeenRing];
           if (!seen_next(kv, a, s_walk, p)) p.row_hi = 0;

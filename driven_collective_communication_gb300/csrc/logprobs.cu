@@ -221,8 +221,10 @@ struct LpTop {
   int count, now;          // keys in buffer `now`
 };
 // Cuts the buffer to its k largest keys, in descending order, and raises the
-// threshold to the k-th.  All threads call; the buffer is theirs before and after.
-__device__ __forceinline__ void lp_cut(LpTop& s, int k) {
+// threshold to the k-th.  All threads call, between two barriers without additions;
+// returns the keys left (read from the buffer instead, another thread might have
+// added to it already).
+__device__ __forceinline__ int lp_cut(LpTop& s, int k) {
   const int n = min(s.count, kLpCap), now = s.now;
   const unsigned long long* from = s.keys[now];
   unsigned long long* to = s.keys[now ^ 1];
@@ -246,6 +248,7 @@ __device__ __forceinline__ void lp_cut(LpTop& s, int k) {
     s.now = now ^ 1;
   }
   __syncthreads();
+  return min(n, k);
 }
 __device__ __forceinline__ bool lp_add(LpTop& s, unsigned long long key) {
   const int at = atomicAdd(&s.count, 1);
@@ -441,10 +444,7 @@ __global__ void __launch_bounds__(kLpThreads, 6) k_token_logprobs(const __grid_c
       if (held <= kLpCap) break;
       adders = __syncthreads_count(pending != 0 || extra);
       held = s.count;
-      if (adders || held > kLpCut || held > k + k) {
-        lp_cut(s, k);
-        held = s.count;
-      }
+      if (adders || held > kLpCut || held > k + k) held = lp_cut(s, k);
     }
   }
 

@@ -281,3 +281,33 @@ def test_missing_pages_are_reported(dcc, news, share):  # noqa: F811
     cache.table[0, 1] = table[0, 1].item()
     cache.attention_tree([q], [out], batch(news), mask, max_new=news[0], workspace=ws)
     assert dcc.dcc_local_check() == dcc.DCC_OK
+
+
+@pytest.mark.parametrize("dtype,dim,group", SHAPES)
+@pytest.mark.parametrize("new,window", [(3, 0), (4, 0), (4, 700)])
+def test_two_passes_of_the_streaming_kernel(dcc, dtype, dim, group, new, window):  # noqa: F811
+    """Rows that it takes in two goes, over a row of the table long enough for the rule."""
+    g = torch.Generator().manual_seed(new + dim)
+    lens, news = [1500, 70], [new, 2]
+    share = 8 if dim == 128 else 10
+    need = [-(-m // R.PAGE) for m in lens]
+    cache, _, table = make_cache(dcc, g, 1, lens, 1, dim, group, dtype, max_pages=5000 if window == 0 else max(need))
+    masks = [S.tree(g, t) for t in news]
+    q, out, lse = attend(dcc, cache, g, 1, 1, dim, dtype, lens, news, share, window, 9 if window else 0, masks)
+    check(cache, table, 1, 1, dim, group, dtype, lens, news, share, window, 9 if window else 0, masks, q, out, lse, "prompt")
+
+
+@pytest.mark.parametrize("share", [1, 8])
+@pytest.mark.parametrize("tree", [True, False])
+def test_idle_slots(dcc, share, tree):  # noqa: F811
+    """Two sequences with rows among a thousand slots without any."""
+    g = torch.Generator().manual_seed(12)
+    lens, news = [0] * 1000, [0] * 1000
+    for s, (m, t) in {3: (300, 9), 977: (700, 5)}.items():
+        lens[s], news[s] = m, t
+    lens[500] = 200  # holds tokens, brings none
+    cache, _, table = make_cache(dcc, g, 2, lens, 1, 128, 64, "bf16")
+    masks = [S.tree(g, t) for t in news] if tree else None
+    window, sinks = (0, 0) if tree else (100, 70)
+    q, out, lse = attend(dcc, cache, g, 2, 1, 128, "bf16", lens, news, share, window, sinks, masks)
+    check(cache, table, 2, 1, 128, 64, "bf16", lens, news, share, window, sinks, masks, q, out, lse, "prompt")
