@@ -30,7 +30,7 @@ AttnKernel attn_kernel_of(int which) {
   using No = std::false_type;
   switch (which) {
     case kAttnPrompt:
-      if constexpr (SEEN) return {(const void*)&k_kv4_seen<T, D, G>, kPromptThreads, PromptShape<D, G>::smem};
+      if constexpr (SEEN) return {(const void*)&k_kv4_seen<T, D, G>, kPromptThreads, kSeenSmem<T, D, G>};
       else return {(const void*)&k_kv4_prompt<T, D, G>, kPromptThreads, PromptShape<D, G>::smem};
     case kAttnJoin:
       if constexpr (SEEN) return {(const void*)&k_kv4_seen_join<T, D>, kSeenJoinThreads, 0};

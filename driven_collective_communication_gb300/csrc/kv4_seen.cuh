@@ -96,6 +96,25 @@ __device__ __forceinline__ float* seen_parts(const AttnArgs& a, int dim, int cta
   return reinterpret_cast<float*>(a.ws + 1024 + kSeenJoinBytes) + (2 * (size_t)cta + slot) * seen_part(dim);
 }
 
+// fp16 output of 64-wide heads: K in two numbers.  Rounded to fp16, K, V and P
+// together put an output that sees a few hundred keys 3.5e-4 off where its own
+// rounding is 2.1e-4, and K is the largest of the three; the second number has room
+// in shared memory at 64 channels only.
+template <typename T, int D>
+constexpr bool kSeenExactK = std::is_same<T, __half>::value && D == 64;
+template <typename T, int D, int G>
+constexpr size_t kSeenSmem = PromptShape<D, G>::smem + (kSeenExactK<T, D> ? 2 * PromptShape<D, G>::kv_tile : 0);
+// lo + step * code, biased codes as Pair16, as a number and what its rounding left
+__device__ __forceinline__ void value_exact(uint32_t c, uint32_t step, uint32_t lo, uint32_t* big, uint32_t* small) {
+  const uint32_t bias = 0x54005400u;
+  auto h = [](const uint32_t& w) { return *reinterpret_cast<const __half2*>(&w); };
+  const __half2 n = __hsub2(h(c), h(bias)), p = __hmul2(n, h(step)), q = __hfma2(n, h(step), __hneg2(p));  // p + q, exactly
+  const __half2 s = __hadd2(p, h(lo)), b = __hsub2(s, p);
+  const __half2 r = __hadd2(q, __hadd2(__hsub2(p, __hsub2(s, b)), __hsub2(h(lo), b)));  // the sum's error, exactly, and q
+  *big = *reinterpret_cast<const uint32_t*>(&s);
+  *small = *reinterpret_cast<const uint32_t*>(&r);
+}
+
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const __grid_constant__ AttnArgs a, LocalDev dc) {
   using Shape = PromptShape<D, G>;
@@ -116,7 +135,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
   auto piece_full = [&](int k) { return smem_addr_u32(&s_piece_bars[k % kSeenRing]); };
   auto piece_free = [&](int k) { return smem_addr_u32(&s_piece_bars[kSeenRing + k % kSeenRing]); };
   const uint32_t base = (smem_addr_u32(prompt_raw) + 1023u) & ~1023u;
-  const uint32_t sq = base, sk = sq + 2 * Shape::q_tile, sv = sk + 2 * Shape::kv_tile, raw = sv + 2 * Shape::kv_tile;
+  const uint32_t sq = base, sk = sq + 2 * Shape::q_tile, sv = sk + 2 * Shape::kv_tile;
+  constexpr bool EXACT = kSeenExactK<T, D>;
+  const uint32_t sk2 = sv + 2 * Shape::kv_tile, raw = sk2 + (EXACT ? 2 * Shape::kv_tile : 0);  // (K's second numbers)
   unsigned char* raw_g_rw = prompt_raw + (raw - smem_addr_u32(prompt_raw));
   const unsigned char* raw_g = raw_g_rw;
   const uint32_t bars = raw + (uint32_t)(R * BLK);
@@ -331,6 +352,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + (uint32_t)g * 128u),
               "l"(ad), "l"(bd), "r"(id_s), "r"(kk > 0 ? 1u : 0u)
               : "memory");
+          if constexpr (EXACT)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + (uint32_t)g * 128u),
+                "l"(ad), "l"(mma_smem_desc(sk2 + (uint32_t)((j & 1) * Shape::kv_tile) + off)), "r"(id_s), "r"(1u)
+                : "memory");
         }
         tc_commit(two(sFull, g));
         if (g == nt - 1) tc_commit(two(kFree, j & 1));
@@ -434,6 +461,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
                                                            (uint32_t)(((u % 8) ^ (key & 7)) * 16 + 4 * (i & 3))),
                            "r"(pair)
                            : "memory");
+              if constexpr (EXACT)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (sk2 - sk) + (uint32_t)(u / 8) * 16384u +
+                                                             (uint32_t)(((u % 8) ^ (key & 7)) * 16 + 4 * (i & 3))),
+                             "r"(0u)
+                             : "memory");
             }
             continue;
           }
@@ -447,11 +479,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
 #pragma unroll
           for (int jj = 0; jj < JW; ++jj) {
             const int u = 4 * jj + t, gr = 32 * jj / G;  // channels 8 u ..
+            const uint32_t at = row + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (key & 7)) * 16);
+            if constexpr (EXACT) {
+              uint4 a, b;
+              value_exact(Pair16<__half>::code<0>(w[jj]), step[gr], lo[gr], &a.x, &b.x);
+              value_exact(Pair16<__half>::code<1>(w[jj]), step[gr], lo[gr], &a.y, &b.y);
+              value_exact(Pair16<__half>::code<2>(w[jj]), step[gr], lo[gr], &a.z, &b.z);
+              value_exact(Pair16<__half>::code<3>(w[jj]), step[gr], lo[gr], &a.w, &b.w);
+              sts128(at, a);
+              sts128(at + (sk2 - sk), b);
+              continue;
+            }
             const uint4 v = make_uint4(Pair16<__half>::value(Pair16<__half>::code<0>(w[jj]), step[gr], lo[gr]),
                                        Pair16<__half>::value(Pair16<__half>::code<1>(w[jj]), step[gr], lo[gr]),
                                        Pair16<__half>::value(Pair16<__half>::code<2>(w[jj]), step[gr], lo[gr]),
                                        Pair16<__half>::value(Pair16<__half>::code<3>(w[jj]), step[gr], lo[gr]));
-            sts128(row + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (key & 7)) * 16), v);
+            sts128(at, v);
           }
         }
       }

@@ -40,7 +40,7 @@ namespace dcc {
 constexpr int kLpThreads = 128, kLpWarps = kLpThreads / 32;
 constexpr int kLpCap = 1024;      // keys of the buffer
 constexpr int kLpCut = 192;       // keys after a batch from which the buffer is cut
-constexpr int kLpMaxRuns = 912;   // CTAs of a call whose rows are cut: one wave of 6 to an SM
+constexpr int kLpMaxRuns = 1064;  // CTAs of a call whose rows are cut: one wave of 7 to an SM
 
 struct LpArgs {
   const void* x[DCC_MAX_RANKS];
@@ -281,7 +281,7 @@ __device__ __forceinline__ void lp_first(LpTop& s, uint32_t mine, int k) {
 }
 
 template <typename T, int VPT>
-__global__ void __launch_bounds__(kLpThreads, 6) k_token_logprobs(const __grid_constant__ LpArgs a) {
+__global__ void __launch_bounds__(kLpThreads, 7) k_token_logprobs(const __grid_constant__ LpArgs a) {
   using Vec = LpVec<T>;
   constexpr int E = Vec::N;
   __shared__ __align__(16) LpTop s;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kLpThreads, 6) k_token_logprobs(const __grid_c
       if (held <= kLpCap) break;
       adders = __syncthreads_count(pending != 0 || extra);
       held = s.count;
-      if (adders || held > kLpCut || held > k + k) held = lp_cut(s, k);
+      if (adders || held > kLpCut || held > k + k / 2) held = lp_cut(s, k);
     }
   }
 
