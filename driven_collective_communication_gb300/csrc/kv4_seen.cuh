@@ -1,6 +1,44 @@
 // kv4_seen.cuh -- attention of many query rows over the 4-bit paged cache, for rows
 // with sets of seen keys of their own: trees of drafted tokens, and windows whose
 // first tokens stay visible.
+//
+// The steps and roles are the prompt kernel's (kv4_prompt.cuh: 256 rows of one
+// sequence, rank and kv head, 128 keys a step; S = Q K^T, P = 2^(c S - ref) and O +=
+// P V on tcgen05, one warp that loads, one that issues, four that unpack, eight
+// that make P).  What differs:
+//
+// Which keys a row sees.  A step whose keys some row of a warp does not see first
+// takes the rows' 128 bits -- a run of keys, the sinks, and of a tree the mask's
+// words shifted into place -- and puts -infinity over the hidden scores in tensor
+// memory.  What follows is one form for all steps.  A tree has a few such steps a
+// tile (the drafted tokens lie at the end), a window two or three.
+//
+// Work split.  Verifying a tree, a segment has one or a few row tiles and thousands
+// of keys, and there may be one sequence: tiles alone would leave the SMs idle.
+// So all steps of all tiles form one line, cut evenly over the SMs; a CTA goes from
+// piece to piece with its barriers' phases running on, the loading warp finds the
+// pieces ahead, and the next piece's Q comes before this one's results are
+// written.  A tile that is cut leaves its reference, sum and O in fp32, and a second
+// kernel joins them in order: results do not depend on timing.
+//
+// Bound by neither the tensor pipe (37 %) nor the issue slots (47 %): the chain of
+// hand-overs between the roles, as in the prompt kernel.  Measured on GB300, 128
+// channels, 8 heads per kv head: 152 segments of 4096 keys x 32 drafted tokens fp16
+// 91 us, bf16 109 (2.4 and 2.8 us a step, and 15 for start and end); 32 requests of
+// up to 4096 keys, 8 ranks, bf16 154 us (0.36 PFLOP/s: a third is start, the ends of
+// pieces and the join); one of 131,109 keys x 63 tokens, 16 kv heads of 4 heads, fp16
+// 275 us (1.0 PFLOP/s).
+//
+// Code size decided most: each role's code has to stay in the instruction cache.
+// A masked and an unmasked form of the steps, and Q and the results in unrolled
+// loops, had taken 120 us instead of 91 (182 instead of 127 with a window).  Tried
+// without gain: a warp for each row tile's MMAs (110 us: in one thread's order the
+// tiles' chains stay half a step apart), eight unpacking warps with the registers
+// split by roles (96 us), pages asked into L2 ahead (no change), the waits' loop as
+// a function (96 us), Q's loads a step earlier (no change).
+//
+// What it rounds: as the prompt kernel, each of K, V and P to fp16; with 64 channels
+// and fp16 output K is two numbers (kSeenExactK).
 #pragma once
 #include "kv4_prompt.cuh"
 
@@ -127,8 +165,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
   // bf16 cache, by step and page: 1 where a key of K has its own scale, 2 where V stays bf16
   __shared__ __align__(2) uint8_t s_range[8][2];
   __shared__ int8_t s_exp[4][128];  // by step: K's powers of two
-  // the pieces, found by the warp that loads, ahead of the others.  The last
-  // one is marked: row_hi 0.
+  // the pieces, found by the warp that loads, ahead of the others; what comes after the
+  // last one has row_hi 0
   __shared__ SeenWalk s_walk;
   __shared__ PromptPiece s_piece[kSeenRing];
   __shared__ __align__(8) uint64_t s_piece_bars[2 * kSeenRing];
@@ -254,16 +292,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
   // Calls `work` for every piece with the steps before it, until one returns false
   // (one thread, or a whole warp).
   auto pieces = [&](bool whole_warp, auto&& work) {
-    {
-      for (int k = 0, done = 0;; ++k) {
-        if (!wait(piece_full(k), k / kSeenRing)) return false;
-        const PromptPiece& p = s_piece[k % kSeenRing];
-        if (p.row_hi == 0) return true;
-        if (!work(p, done)) return false;
-        done += p.j1 - p.j0;
-        if (whole_warp) __syncwarp();
-        if (!whole_warp || lane == 0) mbar_arrive(piece_free(k));
-      }
+    for (int k = 0, done = 0;; ++k) {
+      if (!wait(piece_full(k), k / kSeenRing)) return false;
+      const PromptPiece& p = s_piece[k % kSeenRing];
+      if (p.row_hi == 0) return true;
+      if (!work(p, done)) return false;
+      done += p.j1 - p.j0;
+      if (whole_warp) __syncwarp();
+      if (!whole_warp || lane == 0) mbar_arrive(piece_free(k));
     }
   };
   // the table's slot of a tile's page
@@ -272,58 +308,56 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
   if (warp == 0) {  // ---- loads
     int unfinished = 0;
     auto load = [&](const PromptPiece& pc, int before) {
-    int ids = -1, ids_at = -(1 << 30);
-    const int ahead = 2 * (before - pc.j0);  // of the ring, against the tile's pages
-    for (int v = 2 * pc.j0; v < 2 * pc.j1; ++v) {
-      const int p = v + ahead;
-      if (v - ids_at >= 32) {
-        ids_at = v;
-        ids = v + lane < pc.pages ? kv4_page(kv, pc.seq, slot_at(pc, v + lane)) : -1;
-      }
-      const int page = __shfl_sync(0xffffffffu, ids, v - ids_at), slot = p % R;
-      if (p >= R && !wait(rawe(slot), p / R - 1)) return false;
-      if (lane == 0) {
-        uint32_t& absent = s_absent[(p / 2) & 7];
-        absent = (p & 1 ? absent : 0u) | (page < 0 ? 1u << (p & 1) : 0u);
-        mma_mbar_expect(rawf(slot), page < 0 ? 0u : (uint32_t)BLK);
-        if (page >= 0)
-          asm volatile(
-              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                  raw + (uint32_t)(slot * BLK)),
-              "l"(kv4_block(kv, pc.rank, a.layer, page, pc.head, BLK)), "r"((uint32_t)BLK), "r"(rawf(slot))
-              : "memory");
-      }
-      ++unfinished;
-    }
-    return true;
-    };
-    {
-      // Piece k + 1 is made known before piece k's pages are asked for.  A slot of the
-      // ring is free once piece k + 1 - kSeenRing has been worked off, whose pages
-      // have been loaded.
-      auto publish = [&](int k) {
-        if (k >= kSeenRing && !wait(piece_free(k), k / kSeenRing - 1)) return false;
-        if (s_walk.over) {  // on to the next sequence that has rows
-          const int s = next_with_rows(kv, a, s_walk.s);
-          __syncwarp();  // all have read the walk
-          if (lane == 0) s_walk.s = s, s_walk.seg = 0, s_walk.over = false;
+      int ids = -1, ids_at = -(1 << 30);
+      const int ahead = 2 * (before - pc.j0);  // of the ring, against the tile's pages
+      for (int v = 2 * pc.j0; v < 2 * pc.j1; ++v) {
+        const int p = v + ahead;
+        if (v - ids_at >= 32) {
+          ids_at = v;
+          ids = v + lane < pc.pages ? kv4_page(kv, pc.seq, slot_at(pc, v + lane)) : -1;
         }
-        __syncwarp();
+        const int page = __shfl_sync(0xffffffffu, ids, v - ids_at), slot = p % R;
+        if (p >= R && !wait(rawe(slot), p / R - 1)) return false;
         if (lane == 0) {
-          PromptPiece& p = s_piece[k % kSeenRing];
-          if (!seen_next(kv, a, s_walk, p)) p.row_hi = 0;
-          mbar_arrive(piece_full(k));
+          uint32_t& absent = s_absent[(p / 2) & 7];
+          absent = (p & 1 ? absent : 0u) | (page < 0 ? 1u << (p & 1) : 0u);
+          mma_mbar_expect(rawf(slot), page < 0 ? 0u : (uint32_t)BLK);
+          if (page >= 0)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    raw + (uint32_t)(slot * BLK)),
+                "l"(kv4_block(kv, pc.rank, a.layer, page, pc.head, BLK)), "r"((uint32_t)BLK), "r"(rawf(slot))
+                : "memory");
         }
-        __syncwarp();
-        return true;
-      };
-      bool ok = publish(0);
-      for (int k = 0, before = 0; ok; ++k) {
-        const PromptPiece pc = s_piece[k % kSeenRing];
-        if (pc.row_hi == 0) break;
-        ok = publish(k + 1) && load(pc, before);
-        before += pc.j1 - pc.j0;
+        ++unfinished;
       }
+      return true;
+    };
+    // Piece k + 1 is made known before piece k's pages are asked for.  A slot of the
+    // ring is free once piece k + 1 - kSeenRing has been worked off, whose pages
+    // have been loaded.
+    auto publish = [&](int k) {
+      if (k >= kSeenRing && !wait(piece_free(k), k / kSeenRing - 1)) return false;
+      if (s_walk.over) {  // on to the next sequence that has rows
+        const int s = next_with_rows(kv, a, s_walk.s);
+        __syncwarp();  // all have read the walk
+        if (lane == 0) s_walk.s = s, s_walk.seg = 0, s_walk.over = false;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        PromptPiece& p = s_piece[k % kSeenRing];
+        if (!seen_next(kv, a, s_walk, p)) p.row_hi = 0;
+        mbar_arrive(piece_full(k));
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = publish(0);
+    for (int k = 0, before = 0; ok; ++k) {
+      const PromptPiece pc = s_piece[k % kSeenRing];
+      if (pc.row_hi == 0) break;
+      ok = publish(k + 1) && load(pc, before);
+      before += pc.j1 - pc.j0;
     }
     // a copy in flight when a wait gave up ends before the CTA does
     for (int p = max(0, unfinished - R); p < unfinished; ++p) local_drain(rawf(p % R), (uint32_t)(p / R) & 1u);
@@ -335,63 +369,63 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
       bool ok = true;
       int had[2] = {0, 0}, qs[2] = {0, 0};  // by row tile: steps and tiles of Q so far
       pieces(false, [&](const PromptPiece& pc, int before) {
-      const int steps = pc.j1 - pc.j0, nt = pc.row_hi - pc.row_lo > 128 ? 2 : 1;
-      if (steps == 0) return true;
-      auto scores = [&](int g, int jj) {
-        const int j = before + jj;
-        ok = ok && wait(two(kFull, j & 1), j >> 1);
-        if (!ok) return;
-        tc_fence_after();
+        const int steps = pc.j1 - pc.j0, nt = pc.row_hi - pc.row_lo > 128 ? 2 : 1;
+        if (steps == 0) return true;
+        auto scores = [&](int g, int jj) {
+          const int j = before + jj;
+          ok = ok && wait(two(kFull, j & 1), j >> 1);
+          if (!ok) return;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (uint32_t)(kk / 4) * 16384u + (uint32_t)(kk % 4) * 32u;
-          const uint64_t ad = mma_smem_desc(sq + (uint32_t)(g * Shape::q_tile) + off);
-          const uint64_t bd = mma_smem_desc(sk + (uint32_t)((j & 1) * Shape::kv_tile) + off);
-          asm volatile(
-              "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-              "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + (uint32_t)g * 128u),
-              "l"(ad), "l"(bd), "r"(id_s), "r"(kk > 0 ? 1u : 0u)
-              : "memory");
-          if constexpr (EXACT)
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (uint32_t)(kk / 4) * 16384u + (uint32_t)(kk % 4) * 32u;
+            const uint64_t ad = mma_smem_desc(sq + (uint32_t)(g * Shape::q_tile) + off);
+            const uint64_t bd = mma_smem_desc(sk + (uint32_t)((j & 1) * Shape::kv_tile) + off);
             asm volatile(
                 "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + (uint32_t)g * 128u),
-                "l"(ad), "l"(mma_smem_desc(sk2 + (uint32_t)((j & 1) * Shape::kv_tile) + off)), "r"(id_s), "r"(1u)
+                "l"(ad), "l"(bd), "r"(id_s), "r"(kk > 0 ? 1u : 0u)
                 : "memory");
-        }
-        tc_commit(two(sFull, g));
-        if (g == nt - 1) tc_commit(two(kFree, j & 1));
-        (j & 1 ? rg1 : rg0) = range(j);
-      };
-      for (int g = 0; g < nt; ++g) ok = ok && wait(two(qFull, g), qs[g]);
-      for (int g = 0; g < nt; ++g) scores(g, 0);
-      for (int jj = 0; jj < steps && ok; ++jj)
-        for (int g = 0; g < nt && ok; ++g) {
-          const int j = before + jj;
-          ok = wait(two(pFull, g), had[g] + jj) && wait(two(vFull, j & 1), j >> 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t bf = (1u << 7) | (1u << 10);
-          const uint32_t ids[2] = {id_o | ((j & 1 ? rg1 : rg0) & 2u ? bf : 0u), id_o | ((j & 1 ? rg1 : rg0) & 0x200u ? bf : 0u)};
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (uint32_t)(kk / 4) * (D * 128u) + (uint32_t)(kk % 4) * 32u;
-            const uint64_t bd = mma_smem_desc(sv + (uint32_t)((j & 1) * Shape::kv_tile) + off);
-            asm volatile(
-                "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem + 256u + (uint32_t)g * 128u),
-                "r"(tmem + (uint32_t)g * 128u + (uint32_t)kk * 8u), "l"(bd), "r"(ids[kk / 4]), "r"(jj > 0 || kk > 0 ? 1u : 0u)
-                : "memory");
+            if constexpr (EXACT)
+              asm volatile(
+                  "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + (uint32_t)g * 128u),
+                  "l"(ad), "l"(mma_smem_desc(sk2 + (uint32_t)((j & 1) * Shape::kv_tile) + off)), "r"(id_s), "r"(1u)
+                  : "memory");
           }
-          if (g == nt - 1) tc_commit(two(vFree, j & 1));
-          tc_commit(two(pvDone, g));
-          if (jj + 1 < steps) scores(g, jj + 1);
+          tc_commit(two(sFull, g));
+          if (g == nt - 1) tc_commit(two(kFree, j & 1));
+          (j & 1 ? rg1 : rg0) = range(j);
+        };
+        for (int g = 0; g < nt; ++g) ok = ok && wait(two(qFull, g), qs[g]);
+        for (int g = 0; g < nt; ++g) scores(g, 0);
+        for (int jj = 0; jj < steps && ok; ++jj)
+          for (int g = 0; g < nt && ok; ++g) {
+            const int j = before + jj;
+            ok = wait(two(pFull, g), had[g] + jj) && wait(two(vFull, j & 1), j >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t bf = (1u << 7) | (1u << 10);
+            const uint32_t ids[2] = {id_o | ((j & 1 ? rg1 : rg0) & 2u ? bf : 0u), id_o | ((j & 1 ? rg1 : rg0) & 0x200u ? bf : 0u)};
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (uint32_t)(kk / 4) * (D * 128u) + (uint32_t)(kk % 4) * 32u;
+              const uint64_t bd = mma_smem_desc(sv + (uint32_t)((j & 1) * Shape::kv_tile) + off);
+              asm volatile(
+                  "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem + 256u + (uint32_t)g * 128u),
+                  "r"(tmem + (uint32_t)g * 128u + (uint32_t)kk * 8u), "l"(bd), "r"(ids[kk / 4]), "r"(jj > 0 || kk > 0 ? 1u : 0u)
+                  : "memory");
+            }
+            if (g == nt - 1) tc_commit(two(vFree, j & 1));
+            tc_commit(two(pvDone, g));
+            if (jj + 1 < steps) scores(g, jj + 1);
+          }
+        for (int g = 0; g < nt; ++g) {
+          had[g] += steps;
+          ++qs[g];
         }
-      for (int g = 0; g < nt; ++g) {
-        had[g] += steps;
-        ++qs[g];
-      }
-      return ok;
+        return ok;
       });
       if (!ok) {
         tc_commit(last);
@@ -408,279 +442,279 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
       if (lane == 0) mbar_arrive(rawe(p % R));
     };
     pieces(true, [&](const PromptPiece& pc, int before) {
-    const int len = pc.len, ahead = before - pc.j0;
-    for (int j = before; j < before + (pc.j1 - pc.j0) && ok; ++j) {
-      const int buf = j & 1;
-      auto key_at = [&](int p) { return slot_at(pc, p - 2 * ahead) * kKv4Page; };  // of a page of the ring
-      const uint32_t kt = sk + (uint32_t)(buf * Shape::kv_tile), vt = sv + (uint32_t)(buf * Shape::kv_tile);
-      if (j >= 2) ok = wait(two(kFree, buf), (j >> 1) - 1);
-      uint32_t absent = 0;
+      const int len = pc.len, ahead = before - pc.j0;
+      for (int j = before; j < before + (pc.j1 - pc.j0) && ok; ++j) {
+        const int buf = j & 1;
+        auto key_at = [&](int p) { return slot_at(pc, p - 2 * ahead) * kKv4Page; };  // of a page of the ring
+        const uint32_t kt = sk + (uint32_t)(buf * Shape::kv_tile), vt = sv + (uint32_t)(buf * Shape::kv_tile);
+        if (j >= 2) ok = wait(two(kFree, buf), (j >> 1) - 1);
+        uint32_t absent = 0;
 #pragma unroll 1
-      for (int h = 0; h < 2 && ok; ++h) {  // K of the two pages
-        const int p = 2 * j + h, slot = p % R;
-        ok = wait(rawf(slot), p / R) && (FP16 || wait(ready(slot), p / R));
-        if (!ok) break;
-        absent = s_absent[j & 7];
-        const bool there = !((absent >> h) & 1u);
-        const unsigned char* blk = raw_g + slot * BLK;
-        const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D));
-        if (!there) continue;
-        // eight neighbouring lanes take the four quarters of rows r and r ^ 5
-        // (other half of the banks, other half of the swizzled chunks): no
-        // bank conflicts on either side
-        const int t = tid & 3;
+        for (int h = 0; h < 2 && ok; ++h) {  // K of the two pages
+          const int p = 2 * j + h, slot = p % R;
+          ok = wait(rawf(slot), p / R) && (FP16 || wait(ready(slot), p / R));
+          if (!ok) break;
+          absent = s_absent[j & 7];
+          const bool there = !((absent >> h) & 1u);
+          const unsigned char* blk = raw_g + slot * BLK;
+          const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D));
+          if (!there) continue;
+          // eight neighbouring lanes take the four quarters of rows r and r ^ 5
+          // (other half of the banks, other half of the swizzled chunks): no
+          // bank conflicts on either side
+          const int t = tid & 3;
 #pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-          const int key = (2 * ((tid >> 3) + 16 * pass)) ^ ((tid & 4) ? 5 : 0);
-          const uint32_t row = kt + (uint32_t)(64 * h + key) * 128u;
-          const unsigned char* src = blk + key * (D / 2) + t * (JW * 4);
-          uint32_t step[NG], lo[NG], w[JW];
-          uint32_t odd = 0;  // fp16: large or not finite, K or V (the bf16 cache's parameters have been seen to)
+          for (int pass = 0; pass < 2; ++pass) {
+            const int key = (2 * ((tid >> 3) + 16 * pass)) ^ ((tid & 4) ? 5 : 0);
+            const uint32_t row = kt + (uint32_t)(64 * h + key) * 128u;
+            const unsigned char* src = blk + key * (D / 2) + t * (JW * 4);
+            uint32_t step[NG], lo[NG], w[JW];
+            uint32_t odd = 0;  // fp16: large or not finite, K or V (the bf16 cache's parameters have been seen to)
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            const uint32_t pw = par[key * NG + gr];
-            if (FP16) odd |= param_large(par[(kKv4Page + key) * NG + gr]) | param_large(pw);
-            step[gr] = __byte_perm(pw, pw, 0x1010);
-            lo[gr] = __byte_perm(pw, pw, 0x3232);
-          }
-          if (FP16 && (odd & kBad)) {  // rare, so little code: a pair at a time, in fp32
-            uint32_t bad = 0;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) bad |= param_bad<T>(par[(kKv4Page + key) * NG + gr]);
-#pragma unroll 1
-            for (int i = 0; i < 4 * JW; ++i) {
-              const int u = 4 * (i >> 2) + t;
-              const uint32_t c = reinterpret_cast<const uint32_t*>(src)[i >> 2] >> (4 * (i & 3));
-              const uint32_t pw = par[key * NG + 8 * u / G];
-              const float2 f = Half16<T>::widen2(pw);
-              const uint32_t pair = (bad | param_bad<T>(pw)) & kBad
-                                        ? 0xffffffffu  // NaN
-                                        : narrow_finite<T>(fmaf((float)(c & 15u), f.x, f.y),
-                                                           fmaf((float)((c >> 16) & 15u), f.x, f.y));
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (uint32_t)(u / 8) * 16384u +
-                                                           (uint32_t)(((u % 8) ^ (key & 7)) * 16 + 4 * (i & 3))),
-                           "r"(pair)
-                           : "memory");
-              if constexpr (EXACT)
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (sk2 - sk) + (uint32_t)(u / 8) * 16384u +
-                                                             (uint32_t)(((u % 8) ^ (key & 7)) * 16 + 4 * (i & 3))),
-                             "r"(0u)
-                             : "memory");
+            for (int gr = 0; gr < NG; ++gr) {
+              const uint32_t pw = par[key * NG + gr];
+              if (FP16) odd |= param_large(par[(kKv4Page + key) * NG + gr]) | param_large(pw);
+              step[gr] = __byte_perm(pw, pw, 0x1010);
+              lo[gr] = __byte_perm(pw, pw, 0x3232);
             }
-            continue;
-          }
-          if constexpr (JW == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(src);
-            w[0] = v.x, w[1] = v.y;
-          }
+            if (FP16 && (odd & kBad)) {  // rare, so little code: a pair at a time, in fp32
+              uint32_t bad = 0;
 #pragma unroll
-          for (int jj = 0; jj < JW; ++jj) {
-            const int u = 4 * jj + t, gr = 32 * jj / G;  // channels 8 u ..
-            const uint32_t at = row + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (key & 7)) * 16);
-            if constexpr (EXACT) {
-              uint4 a, b;
-              value_exact(Pair16<__half>::code<0>(w[jj]), step[gr], lo[gr], &a.x, &b.x);
-              value_exact(Pair16<__half>::code<1>(w[jj]), step[gr], lo[gr], &a.y, &b.y);
-              value_exact(Pair16<__half>::code<2>(w[jj]), step[gr], lo[gr], &a.z, &b.z);
-              value_exact(Pair16<__half>::code<3>(w[jj]), step[gr], lo[gr], &a.w, &b.w);
-              sts128(at, a);
-              sts128(at + (sk2 - sk), b);
+              for (int gr = 0; gr < NG; ++gr) bad |= param_bad<T>(par[(kKv4Page + key) * NG + gr]);
+#pragma unroll 1
+              for (int i = 0; i < 4 * JW; ++i) {
+                const int u = 4 * (i >> 2) + t;
+                const uint32_t c = reinterpret_cast<const uint32_t*>(src)[i >> 2] >> (4 * (i & 3));
+                const uint32_t pw = par[key * NG + 8 * u / G];
+                const float2 f = Half16<T>::widen2(pw);
+                const uint32_t pair = (bad | param_bad<T>(pw)) & kBad
+                                          ? 0xffffffffu  // NaN
+                                          : narrow_finite<T>(fmaf((float)(c & 15u), f.x, f.y),
+                                                             fmaf((float)((c >> 16) & 15u), f.x, f.y));
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (uint32_t)(u / 8) * 16384u +
+                                                             (uint32_t)(((u % 8) ^ (key & 7)) * 16 + 4 * (i & 3))),
+                             "r"(pair)
+                             : "memory");
+                if constexpr (EXACT)
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (sk2 - sk) + (uint32_t)(u / 8) * 16384u +
+                                                               (uint32_t)(((u % 8) ^ (key & 7)) * 16 + 4 * (i & 3))),
+                               "r"(0u)
+                               : "memory");
+              }
               continue;
             }
-            const uint4 v = make_uint4(Pair16<__half>::value(Pair16<__half>::code<0>(w[jj]), step[gr], lo[gr]),
-                                       Pair16<__half>::value(Pair16<__half>::code<1>(w[jj]), step[gr], lo[gr]),
-                                       Pair16<__half>::value(Pair16<__half>::code<2>(w[jj]), step[gr], lo[gr]),
-                                       Pair16<__half>::value(Pair16<__half>::code<3>(w[jj]), step[gr], lo[gr]));
-            sts128(at, v);
-          }
-        }
-      }
-      if (!ok) break;
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(two(kFull, buf));
-      if (j >= 2) ok = wait(two(vFree, buf), (j >> 1) - 1);
-      if (!ok) break;
-      // V: a thread takes a chunk's word of 8 neighbouring keys (at D = 128 every
-      // other run of keys in swapped order, so that the two runs a warp works
-      // on lie in different banks); D = 64 has one word a chunk, so each half
-      // of the threads takes a page
-#pragma unroll 1
-      for (int h = D == 128 ? 0 : tid >> 6; h < 2; h += D == 128 ? 1 : 2) {
-        const int p = 2 * j + h;
-        if (D == 128 && h) done_with(p - 1);
-        const unsigned char* blk = raw_g + (p % R) * BLK;
-        const int c = tid & 7, oct = D == 128 ? tid >> 4 : (tid >> 3) & 7, ws = D == 128 ? (tid >> 3) & 1 : 0;
-        const int swap = D == 128 ? oct & 1 : 0;
-        const uint32_t sel0 = swap ? 0x1054u : 0x5410u, sel1 = swap ? 0x3276u : 0x7632u;
-        const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D)) + kKv4Page * NG;
-        const bool there = !((absent >> h) & 1u);
-        bool wide = !FP16 && wide_v(j, h);
-        // the word's channels lie in one group (G = 64) or two (32)
-        const int g0 = 64 * ws / G;
-        constexpr int GW = G == 32 ? 2 : 1;
-        auto by_pairs = [&]() {  // rare, so little code rather than fast: two keys of a channel at a time, in fp32
-#pragma unroll 1
-          for (int i = 0; i < 32; ++i) {
-            const int n = i >> 2, gr = g0 + (GW > 1 ? n >> 2 : 0), d = 64 * ws + 16 * (n >> 1) + c + 8 * (n & 1);
-            float v[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int key = 8 * oct + 2 * (i & 3) + x;
-              const uint32_t word = *reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + key * (D / 2) +
-                                                                       kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
-              const uint32_t pw = par[key * NG + gr];
-              const float2 f = Half16<T>::widen2(pw);
-              const bool none = (param_bad<T>(pw) & kBad) || !there || key_at(p) + key >= len;
-              v[x] = none ? 0.0f : fmaf((float)((word >> (4 * n)) & 15u), f.x, f.y);
+            if constexpr (JW == 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src);
+              w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              w[0] = v.x, w[1] = v.y;
             }
-            const uint32_t pair = narrow_finite<T>(v[0], v[1]);
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(vt + (uint32_t)h * (D * 128u) + (uint32_t)d * 128u +
-                                                         (uint32_t)((oct ^ (d & 7)) * 16 + 4 * (i & 3))),
-                         "r"(pair)
-                         : "memory");
+#pragma unroll
+            for (int jj = 0; jj < JW; ++jj) {
+              const int u = 4 * jj + t, gr = 32 * jj / G;  // channels 8 u ..
+              const uint32_t at = row + (uint32_t)(u / 8) * 16384u + (uint32_t)(((u % 8) ^ (key & 7)) * 16);
+              if constexpr (EXACT) {
+                uint4 a, b;
+                value_exact(Pair16<__half>::code<0>(w[jj]), step[gr], lo[gr], &a.x, &b.x);
+                value_exact(Pair16<__half>::code<1>(w[jj]), step[gr], lo[gr], &a.y, &b.y);
+                value_exact(Pair16<__half>::code<2>(w[jj]), step[gr], lo[gr], &a.z, &b.z);
+                value_exact(Pair16<__half>::code<3>(w[jj]), step[gr], lo[gr], &a.w, &b.w);
+                sts128(at, a);
+                sts128(at + (sk2 - sk), b);
+                continue;
+              }
+              const uint4 v = make_uint4(Pair16<__half>::value(Pair16<__half>::code<0>(w[jj]), step[gr], lo[gr]),
+                                         Pair16<__half>::value(Pair16<__half>::code<1>(w[jj]), step[gr], lo[gr]),
+                                         Pair16<__half>::value(Pair16<__half>::code<2>(w[jj]), step[gr], lo[gr]),
+                                         Pair16<__half>::value(Pair16<__half>::code<3>(w[jj]), step[gr], lo[gr]));
+              sts128(at, v);
+            }
           }
-        };
-        if (!FP16 && wide) {
-          by_pairs();
-          continue;
         }
-        uint32_t w[8], pr[8][GW], bad = 0;
+        if (!ok) break;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(two(kFull, buf));
+        if (j >= 2) ok = wait(two(vFree, buf), (j >> 1) - 1);
+        if (!ok) break;
+        // V: a thread takes a chunk's word of 8 neighbouring keys (at D = 128 every
+        // other run of keys in swapped order, so that the two runs a warp works
+        // on lie in different banks); D = 64 has one word a chunk, so each half
+        // of the threads takes a page
+#pragma unroll 1
+        for (int h = D == 128 ? 0 : tid >> 6; h < 2; h += D == 128 ? 1 : 2) {
+          const int p = 2 * j + h;
+          if (D == 128 && h) done_with(p - 1);
+          const unsigned char* blk = raw_g + (p % R) * BLK;
+          const int c = tid & 7, oct = D == 128 ? tid >> 4 : (tid >> 3) & 7, ws = D == 128 ? (tid >> 3) & 1 : 0;
+          const int swap = D == 128 ? oct & 1 : 0;
+          const uint32_t sel0 = swap ? 0x1054u : 0x5410u, sel1 = swap ? 0x3276u : 0x7632u;
+          const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 2 * kv4_codes_bytes(D)) + kKv4Page * NG;
+          const bool there = !((absent >> h) & 1u);
+          bool wide = !FP16 && wide_v(j, h);
+          // the word's channels lie in one group (G = 64) or two (32)
+          const int g0 = 64 * ws / G;
+          constexpr int GW = G == 32 ? 2 : 1;
+          auto by_pairs = [&]() {  // rare, so little code rather than fast: two keys of a channel at a time, in fp32
+#pragma unroll 1
+            for (int i = 0; i < 32; ++i) {
+              const int n = i >> 2, gr = g0 + (GW > 1 ? n >> 2 : 0), d = 64 * ws + 16 * (n >> 1) + c + 8 * (n & 1);
+              float v[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int key = 8 * oct + (k ^ swap);
-          w[k] = *reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + key * (D / 2) +
-                                                    kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
-#pragma unroll
-          for (int x = 0; x < GW; ++x) {
-            pr[k][x] = par[key * NG + g0 + x];
-            bad |= FP16 ? param_large(pr[k][x]) : param_bad<__half>(pr[k][x]);
-          }
-        }
-        if ((bad & kBad) || !there || key_at(p) + 8 * oct + 7 >= len) {  // some key must be zero
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int key = 8 * oct + (k ^ swap);
-            uint32_t any = 0;  // (another group of the key may be bad: its own unit sees to it)
-#pragma unroll
-            for (int x = 0; x < GW; ++x) any |= param_bad<__half>(pr[k][x]);
-            if ((any & kBad) || !there || key_at(p) + key >= len)
-#pragma unroll
-              for (int x = 0; x < GW; ++x) pr[k][x] = 0u;
-#pragma unroll
-            for (int x = 0; x < GW; ++x) wide |= FP16 && (param_large(pr[k][x]) & kBad);  // or is large
-          }
-          if (FP16 && wide) {
+              for (int x = 0; x < 2; ++x) {
+                const int key = 8 * oct + 2 * (i & 3) + x;
+                const uint32_t word = *reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + key * (D / 2) +
+                                                                         kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
+                const uint32_t pw = par[key * NG + gr];
+                const float2 f = Half16<T>::widen2(pw);
+                const bool none = (param_bad<T>(pw) & kBad) || !there || key_at(p) + key >= len;
+                v[x] = none ? 0.0f : fmaf((float)((word >> (4 * n)) & 15u), f.x, f.y);
+              }
+              const uint32_t pair = narrow_finite<T>(v[0], v[1]);
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(vt + (uint32_t)h * (D * 128u) + (uint32_t)d * 128u +
+                                                           (uint32_t)((oct ^ (d & 7)) * 16 + 4 * (i & 3))),
+                           "r"(pair)
+                           : "memory");
+            }
+          };
+          if (!FP16 && wide) {
             by_pairs();
             continue;
           }
-        }
-        uint32_t out[8][4];
+          uint32_t w[8], pr[8][GW], bad = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // pairs of keys
-          const int k0 = 2 * e, k1 = 2 * e + 1;
-          const uint32_t step0 = __byte_perm(pr[k0][0], pr[k1][0], sel0), lo0 = __byte_perm(pr[k0][0], pr[k1][0], sel1);
-          const uint32_t step1 = GW > 1 ? __byte_perm(pr[k0][GW - 1], pr[k1][GW - 1], sel0) : step0;
-          const uint32_t lo1 = GW > 1 ? __byte_perm(pr[k0][GW - 1], pr[k1][GW - 1], sel1) : lo0;
-          const uint32_t x0 = __byte_perm(w[k0], w[k1], sel0), x1 = __byte_perm(w[k0], w[k1], sel1);
-          out[0][e] = Pair16<__half>::value(Pair16<__half>::template code<0>(x0), step0, lo0);
-          out[1][e] = Pair16<__half>::value(Pair16<__half>::template code<1>(x0), step0, lo0);
-          out[2][e] = Pair16<__half>::value(Pair16<__half>::template code<2>(x0), step0, lo0);
-          out[3][e] = Pair16<__half>::value(Pair16<__half>::template code<3>(x0), step0, lo0);
-          out[4][e] = Pair16<__half>::value(Pair16<__half>::template code<0>(x1), step1, lo1);
-          out[5][e] = Pair16<__half>::value(Pair16<__half>::template code<1>(x1), step1, lo1);
-          out[6][e] = Pair16<__half>::value(Pair16<__half>::template code<2>(x1), step1, lo1);
-          out[7][e] = Pair16<__half>::value(Pair16<__half>::template code<3>(x1), step1, lo1);
-        }
+          for (int k = 0; k < 8; ++k) {
+            const int key = 8 * oct + (k ^ swap);
+            w[k] = *reinterpret_cast<const uint32_t*>(blk + kv4_codes_bytes(D) + key * (D / 2) +
+                                                      kv4_v_chunk(D, c, key) * (D / 16) + ws * 4);
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const int d = 64 * ws + 16 * (n >> 1) + c + 8 * (n & 1);
-          sts128(vt + (uint32_t)h * (D * 128u) + (uint32_t)d * 128u + (uint32_t)((oct ^ (d & 7)) * 16),
-                 make_uint4(out[n][0], out[n][1], out[n][2], out[n][3]));
+            for (int x = 0; x < GW; ++x) {
+              pr[k][x] = par[key * NG + g0 + x];
+              bad |= FP16 ? param_large(pr[k][x]) : param_bad<__half>(pr[k][x]);
+            }
+          }
+          if ((bad & kBad) || !there || key_at(p) + 8 * oct + 7 >= len) {  // some key must be zero
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int key = 8 * oct + (k ^ swap);
+              uint32_t any = 0;  // (another group of the key may be bad: its own unit sees to it)
+#pragma unroll
+              for (int x = 0; x < GW; ++x) any |= param_bad<__half>(pr[k][x]);
+              if ((any & kBad) || !there || key_at(p) + key >= len)
+#pragma unroll
+                for (int x = 0; x < GW; ++x) pr[k][x] = 0u;
+#pragma unroll
+              for (int x = 0; x < GW; ++x) wide |= FP16 && (param_large(pr[k][x]) & kBad);  // or is large
+            }
+            if (FP16 && wide) {
+              by_pairs();
+              continue;
+            }
+          }
+          uint32_t out[8][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // pairs of keys
+            const int k0 = 2 * e, k1 = 2 * e + 1;
+            const uint32_t step0 = __byte_perm(pr[k0][0], pr[k1][0], sel0), lo0 = __byte_perm(pr[k0][0], pr[k1][0], sel1);
+            const uint32_t step1 = GW > 1 ? __byte_perm(pr[k0][GW - 1], pr[k1][GW - 1], sel0) : step0;
+            const uint32_t lo1 = GW > 1 ? __byte_perm(pr[k0][GW - 1], pr[k1][GW - 1], sel1) : lo0;
+            const uint32_t x0 = __byte_perm(w[k0], w[k1], sel0), x1 = __byte_perm(w[k0], w[k1], sel1);
+            out[0][e] = Pair16<__half>::value(Pair16<__half>::template code<0>(x0), step0, lo0);
+            out[1][e] = Pair16<__half>::value(Pair16<__half>::template code<1>(x0), step0, lo0);
+            out[2][e] = Pair16<__half>::value(Pair16<__half>::template code<2>(x0), step0, lo0);
+            out[3][e] = Pair16<__half>::value(Pair16<__half>::template code<3>(x0), step0, lo0);
+            out[4][e] = Pair16<__half>::value(Pair16<__half>::template code<0>(x1), step1, lo1);
+            out[5][e] = Pair16<__half>::value(Pair16<__half>::template code<1>(x1), step1, lo1);
+            out[6][e] = Pair16<__half>::value(Pair16<__half>::template code<2>(x1), step1, lo1);
+            out[7][e] = Pair16<__half>::value(Pair16<__half>::template code<3>(x1), step1, lo1);
+          }
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const int d = 64 * ws + 16 * (n >> 1) + c + 8 * (n & 1);
+            sts128(vt + (uint32_t)h * (D * 128u) + (uint32_t)d * 128u + (uint32_t)((oct ^ (d & 7)) * 16),
+                   make_uint4(out[n][0], out[n][1], out[n][2], out[n][3]));
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(two(vFull, buf));
+          if (D == 64) mbar_arrive(rawe((2 * j) % R));
+          mbar_arrive(rawe((2 * j + 1) % R));
         }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(two(vFull, buf));
-        if (D == 64) mbar_arrive(rawe((2 * j) % R));
-        mbar_arrive(rawe((2 * j + 1) % R));
-      }
-    }
-    return ok;
+      return ok;
     });
   } else if (warp >= 14) {  // ---- the bf16 cache's parameters, in place as fp16
     if constexpr (!FP16) {
       // a slot's pages are all one warp's: one that skipped a page of a slot could
       // take the barrier's state before that page for the next page's arrival
       pieces(true, [&](const PromptPiece& pc, int before) {
-      const int ahead = 2 * (before - pc.j0), len = pc.len;
-      for (int p = 2 * pc.j0 + ahead; p < 2 * pc.j1 + ahead; ++p) {
-        const int slot = p % R, j = p >> 1, h = p & 1;
-        if ((slot == 1) != (warp == 15)) continue;
-        if (!wait(rawf(slot), p / R)) return false;
-        uint32_t ranges = 0;
-        if (!((s_absent[j & 7] >> h) & 1u)) {
-          uint32_t* par = reinterpret_cast<uint32_t*>(raw_g_rw + slot * BLK + 2 * kv4_codes_bytes(D));
-          uint32_t k[2][NG], v[2][NG], most = 0, least = 0xffffffffu;
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              k[x][gr] = par[(lane + 32 * x) * NG + gr];
-              v[x][gr] = par[(kKv4Page + lane + 32 * x) * NG + gr];
-              const uint32_t a = k[x][gr] & 0x7fff7fffu, b = v[x][gr] & 0x7fff7fffu;
-              most = __vmaxu2(most, __vmaxu2(a, b));
-              least = __vminu2(least, __vminu2(a, b));
-            }
-          // Mostly all are far inside: steps of 2^-10 .. 2^6 and lo up to 2^10
-          // make groups of 2^-8 .. 2^11.
-          const bool inside = (least & 0xffffu) >= 0x3a80u && (most & 0xffffu) <= 0x4280u && (most >> 16) <= 0x4480u;
-          if (!__all_sync(0xffffffffu, inside)) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int key = lane + 32 * x;
-              const bool counts = slot_at(pc, p - ahead) * kKv4Page + key < len;
-              uint32_t bad = 0;
-              float m = 0.0f;
-              bool fits = true;
-#pragma unroll
-              for (int gr = 0; gr < NG; ++gr) {
-                m = fmaxf(m, param_top(k[x][gr]));
-                fits = fits && fp16_fits(param_top(v[x][gr]), kTopV);
-                bad |= param_bad<T>(v[x][gr]);
-              }
-              const int e = fp16_fits(m, kTopK) ? 0 : max(-120, min(126, (int)(__float_as_uint(m) >> 23) - 127));
-              s_exp[j & 3][64 * h + key] = (int8_t)e;
-              ranges |= counts ? (e ? 1u : 0u) | (fits ? 0u : 2u) : 0u;
-#pragma unroll
-              for (int gr = 0; gr < NG; ++gr) {
-                const float2 f = param_floats(k[x][gr]);
-                par[key * NG + gr] = (bad & kBad) ? 0xffffffffu : Half16<__half>::narrow2(f.x * power2(-e), f.y * power2(-e));
-              }
-            }
-            ranges = __reduce_or_sync(0xffffffffu, ranges);
-          } else {
+        const int ahead = 2 * (before - pc.j0), len = pc.len;
+        for (int p = 2 * pc.j0 + ahead; p < 2 * pc.j1 + ahead; ++p) {
+          const int slot = p % R, j = p >> 1, h = p & 1;
+          if ((slot == 1) != (warp == 15)) continue;
+          if (!wait(rawf(slot), p / R)) return false;
+          uint32_t ranges = 0;
+          if (!((s_absent[j & 7] >> h) & 1u)) {
+            uint32_t* par = reinterpret_cast<uint32_t*>(raw_g_rw + slot * BLK + 2 * kv4_codes_bytes(D));
+            uint32_t k[2][NG], v[2][NG], most = 0, least = 0xffffffffu;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int gr = 0; gr < NG; ++gr) par[(lane + 32 * x) * NG + gr] = param_half(k[x][gr]);
+              for (int gr = 0; gr < NG; ++gr) {
+                k[x][gr] = par[(lane + 32 * x) * NG + gr];
+                v[x][gr] = par[(kKv4Page + lane + 32 * x) * NG + gr];
+                const uint32_t a = k[x][gr] & 0x7fff7fffu, b = v[x][gr] & 0x7fff7fffu;
+                most = __vmaxu2(most, __vmaxu2(a, b));
+                least = __vminu2(least, __vminu2(a, b));
+              }
+            // Mostly all are far inside: steps of 2^-10 .. 2^6 and lo up to 2^10
+            // make groups of 2^-8 .. 2^11.
+            const bool inside = (least & 0xffffu) >= 0x3a80u && (most & 0xffffu) <= 0x4280u && (most >> 16) <= 0x4480u;
+            if (!__all_sync(0xffffffffu, inside)) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int key = lane + 32 * x;
+                const bool counts = slot_at(pc, p - ahead) * kKv4Page + key < len;
+                uint32_t bad = 0;
+                float m = 0.0f;
+                bool fits = true;
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                  m = fmaxf(m, param_top(k[x][gr]));
+                  fits = fits && fp16_fits(param_top(v[x][gr]), kTopV);
+                  bad |= param_bad<T>(v[x][gr]);
+                }
+                const int e = fp16_fits(m, kTopK) ? 0 : max(-120, min(126, (int)(__float_as_uint(m) >> 23) - 127));
+                s_exp[j & 3][64 * h + key] = (int8_t)e;
+                ranges |= counts ? (e ? 1u : 0u) | (fits ? 0u : 2u) : 0u;
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                  const float2 f = param_floats(k[x][gr]);
+                  par[key * NG + gr] = (bad & kBad) ? 0xffffffffu : Half16<__half>::narrow2(f.x * power2(-e), f.y * power2(-e));
+                }
+              }
+              ranges = __reduce_or_sync(0xffffffffu, ranges);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) par[(lane + 32 * x) * NG + gr] = param_half(k[x][gr]);
+            }
+            if (!(ranges & 2u))
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) par[(kKv4Page + lane + 32 * x) * NG + gr] = param_half(v[x][gr]);
           }
-          if (!(ranges & 2u))
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int gr = 0; gr < NG; ++gr) par[(kKv4Page + lane + 32 * x) * NG + gr] = param_half(v[x][gr]);
+          if (lane == 0) s_range[j & 7][h] = (uint8_t)ranges;
+          // (the fence before a new page comes over these is the readers')
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready(slot));
         }
-        if (lane == 0) s_range[j & 7][h] = (uint8_t)ranges;
-        // (the fence before a new page comes over these is the readers')
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ready(slot));
-      }
-      return true;
+        return true;
       });
     }
   } else {  // ---- P, one row per thread

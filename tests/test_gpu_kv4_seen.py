@@ -311,3 +311,33 @@ def test_idle_slots(dcc, share, tree):  # noqa: F811
     window, sinks = (0, 0) if tree else (100, 70)
     q, out, lse = attend(dcc, cache, g, 2, 1, 128, "bf16", lens, news, share, window, sinks, masks)
     check(cache, table, 2, 1, 128, 64, "bf16", lens, news, share, window, sinks, masks, q, out, lse, "prompt")
+
+
+def test_two_calls_at_once(dcc):  # noqa: F811
+    """On two streams, with a workspace each, over and over: as one after the other."""
+    g = torch.Generator().manual_seed(13)
+    lens, news = [3000, 700], [40, 9]
+    cache, _, _ = make_cache(dcc, g, 2, lens, 1, 128, 64, "bf16")
+    q = [torch.randn(sum(news), 8, 128, generator=g).bfloat16().cuda() for _ in range(2)]
+    mask, start = S.pack([m for t in news for m in S.tree(g, t)], 2).cuda(), batch(news)
+    streams, ws = [torch.cuda.Stream() for _ in range(2)], [cache.attention_workspace(8) for _ in range(2)]
+
+    def call(i, out):
+        with torch.cuda.stream(streams[i]):
+            if i == 0:
+                cache.attention_tree(q, out, start, mask, max_new=40, workspace=ws[0])
+            else:
+                cache.attention_sinks(q, out, start, max_new=40, workspace=ws[1], window=300, sinks=70)
+    want = [[torch.empty_like(x) for x in q] for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        call(i, want[i])
+        torch.cuda.synchronize()
+    got = [[[torch.empty_like(x) for x in q] for _ in range(2)] for _ in range(6)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for i in range(2):
+            call(i, pair[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for pair in got for i in range(2) for a, b in zip(pair[i], want[i]))
+    assert dcc.dcc_local_check() == dcc.DCC_OK

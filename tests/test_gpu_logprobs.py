@@ -234,3 +234,19 @@ def test_after_the_column_parallel_layer(dcc):  # noqa: F811
     y = [torch.empty(T, R, dtype=torch.bfloat16, device="cuda") for _ in range(n)]
     dcc.dcc_linear(w, [x] * n, y)
     check(dcc, y, torch.randint(0, 3990, (T,), generator=g).to(torch.int32).cuda(), 8, vocab=3990)
+
+
+def test_rows_past_four_gigabytes(dcc):  # noqa: F811
+    x = torch.empty(2, 17000, 65600, dtype=torch.float16, device="cuda")  # 2.2 GB a rank, and rows 131,200 apart below
+    for r in range(2):
+        for a in range(0, 17000, 1000):
+            x[r, a:a + 1000] = torch.randn(1000, 65600, device="cuda")
+    wide = x.view(17000, 131200)
+    rows = torch.cat([torch.arange(3), torch.arange(8400, 8403), torch.arange(16990, 17000)]).cuda()
+    target = torch.arange(17000, dtype=torch.int32, device="cuda")
+    for xs in ([x[0], x[1]], [wide]):
+        lp, en, ids, tl = call(dcc, xs, target, 3)
+        want, entropy, order, log, tol, tol_entropy = plain([t[rows] for t in xs], target[rows], 3, None, 1.0)
+        assert torch.equal(ids[rows].long(), order)
+        assert ((lp[rows].double() - want).abs() <= tol.gather(1, target[rows].long()[:, None])[:, 0]).all()
+        assert ((en[rows].double() - entropy).abs() <= tol_entropy).all()
