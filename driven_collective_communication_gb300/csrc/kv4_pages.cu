@@ -430,7 +430,9 @@ __global__ void __launch_bounds__(kCopyThreads) k_kv4_copy(Kv4Dev kv, CopyArgs a
 // each, several rows at a time.  The path ascends, so a row's place is never
 // past it: a batch of rows is read before any of it is written, and what later
 // batches read lies behind all that was written.  The books follow in a second
-// kernel, which reads what the first one decided.
+// kernel, which reads what the first one decided.  Bound by latency (GB300: 64
+// sequences x 16 layers x 8 ranks, up to 7 of 32 drafted tokens kept, 9.3 MB moved: 5
+// to 9 us and 6 for the books).
 struct KeepArgs {
   const int32_t* start;
   const int32_t* path;

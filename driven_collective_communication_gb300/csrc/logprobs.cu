@@ -24,13 +24,13 @@
 // exchanged but 16 bytes and k keys a run, joined by the CTA that comes last.
 //
 // Bound by reading the logits once (6.8 TB/s) if the instructions per token stay
-// below some 8; measured on GB300, fp16, 2048 rows of 152,008 tokens: 119 us
-// without alternatives (5.2 TB/s), 149 with one, 181 with 20 (3.4 TB/s); bf16, 256
-// rows of 131,072: 20, 27 and 36 us; one row: 8 to 15 us.  What is left is the
-// instructions (60 % of the issue slots) and the threads' waits for one another,
-// one a batch.  CTAs of 128 threads, six to an SM: 256 threads with the same
-// registers took 213 us (more warps wait at a barrier), 64 threads 208, and 64
-// registers a thread, which spill, 243 (the first case with 20).
+// below some 8; measured on GB300, fp16, 2048 rows of 152,008 tokens: 122 us
+// without alternatives (5.1 TB/s), 146 with one, 178 with 20 (3.5 TB/s); bf16, 256
+// rows of 131,072: 20, 26 and 36 us; one row: 8 to 15 us.  What is left is the
+// instructions (63 % of the issue slots) and the threads' waits for one another,
+// one a batch.  CTAs of 128 threads, seven to an SM: 256 threads with about the
+// same registers took 213 us (more warps wait at a barrier), 64 threads 208, and
+// 64 registers a thread, which spill, 243 (the first case with 20).
 #include "comm.h"
 #include "kv4.cuh"
 #include "tcgen05.cuh"

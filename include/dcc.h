@@ -635,7 +635,8 @@ int dcc_kv4_attention_sinks(const dcc_kv4_t* kv, int layer, void* const* q, void
  * drafted tokens sees the last max(0, window - c) positions of the context and
  * its first `sinks`: what a sequential pass over its branch sees, for branches
  * up to the window's length.  A row that sees nothing gives zeros and lse
- * -infinity. */
+ * -infinity.  (In these two calls the keys of fp16 caches of 64 channels enter the
+ * scores exactly.) */
 #define DCC_TREE_MAX 1024
 int dcc_kv4_attention_tree(const dcc_kv4_t* kv, int layer, void* const* q, void* const* out, float* const* lse,
                            int q_heads, size_t tokens, size_t q_stride, const int32_t* start, int max_new,
