@@ -725,8 +725,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
     // what scores are multiplied with
     auto load_q = [&](const PromptPiece& pc) {
       // Straight into shared memory, all loads in flight, neighbouring lanes a row's
-      // 16-byte units (a few lines a load, not 32); then in place.  Loops stay loops:
-      // this runs once a piece, and its time is that of fetching its code.
+      // 16-byte units (a few lines a load, not 32); then in place, a lane a row.  Loops
+      // stay loops: this runs once a piece, and much of its time is fetching its code.
       constexpr int UPR = D / 8, RPI = 32 / UPR;
       const int row = pc.row_lo + 128 * g + r, tok = row / a.share, gh = row - tok * a.share;
       const long long own = row < pc.row_hi
@@ -747,30 +747,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
                      : "memory");
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      float c = fabsf(a.scale) * 1.44269504088896341f;
-      const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-#pragma unroll 2
-      for (int i = 0; i < UPR; ++i) {
+      __syncwarp();  // (a lane's row has come through all of them)
+      const uint32_t own_row = sq + (uint32_t)(g * Shape::q_tile) + (uint32_t)r * 128u;
+      auto unit = [&](int x) { return own_row + (uint32_t)(x / 8) * 16384u + (uint32_t)(((x % 8) ^ (r & 7)) * 16); };
+      auto get = [&](int x) {
         uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place(i)) : "memory");
-        float f = 1.0f;
-        if constexpr (!FP16) {  // a bf16 row as fp16: its largest value goes to 2^8 .. 2^9, exactly
-          uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-          top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-          for (int m = UPR / 2; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-          const int e = top ? max(-100, min(119, (int)(top >> 7) - 127 - 8)) : 0;
-          f = power2(-e);
-          const int mine = __shfl_sync(0xffffffffu, e, lane % RPI * UPR);
-          if (lane / RPI == i) c *= power2(mine);
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(unit(x)) : "memory");
+        return v;
+      };
+      float c = fabsf(a.scale) * 1.44269504088896341f, f = 1.0f;
+      const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+      if constexpr (!FP16) {  // a bf16 row as fp16: its largest value goes to 2^8 .. 2^9, exactly
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int x = 0; x < UPR; ++x) {
+          const uint4 v = get(x);
+          top = __vmaxu2(__vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu)),
+                         v.w & 0x7fff7fffu);
         }
-        auto half = [&](uint32_t w) {  // two values
-          if constexpr (FP16) return w ^ flip;
-          const float2 x = param_floats(w);
-          return Half16<__half>::narrow2(x.x * f, x.y * f) ^ flip;
-        };
-        sts128(place(i), make_uint4(half(__byte_perm(v.x, v.z, 0x5410)), half(__byte_perm(v.x, v.z, 0x7632)),
-                                    half(__byte_perm(v.y, v.w, 0x5410)), half(__byte_perm(v.y, v.w, 0x7632))));
+        top = max(top & 0xffffu, top >> 16);
+        const int e = top ? max(-100, min(119, (int)(top >> 7) - 127 - 8)) : 0;
+        f = power2(-e);
+        c *= power2(e);
+      }
+      auto half = [&](uint32_t w) {  // two values
+        if constexpr (FP16) return w ^ flip;
+        const float2 x = param_floats(w);
+        return Half16<__half>::narrow2(x.x * f, x.y * f) ^ flip;
+      };
+#pragma unroll 4
+      for (int x = 0; x < UPR; ++x) {
+        const uint4 v = get(x);
+        sts128(unit(x), make_uint4(half(__byte_perm(v.x, v.z, 0x5410)), half(__byte_perm(v.x, v.z, 0x7632)),
+                                   half(__byte_perm(v.y, v.w, 0x5410)), half(__byte_perm(v.y, v.w, 0x7632))));
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
