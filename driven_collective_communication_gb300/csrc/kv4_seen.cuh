@@ -25,9 +25,9 @@
 // hand-overs between the roles, as in the prompt kernel.  Measured on GB300, 128
 // channels, 8 heads per kv head: 152 segments of 4096 keys x 32 drafted tokens fp16
 // 91 us, bf16 109 (2.4 and 2.8 us a step, and 15 for start and end); 32 requests of
-// up to 4096 keys, 8 ranks, bf16 154 us (0.36 PFLOP/s: a third is start, the ends of
+// up to 4096 keys, 8 ranks, bf16 149 us (0.37 PFLOP/s: a third is start, the ends of
 // pieces and the join); one of 131,109 keys x 63 tokens, 16 kv heads of 4 heads, fp16
-// 275 us (1.0 PFLOP/s).
+// 276 us (1.0 PFLOP/s).
 //
 // Code size decided most: each role's code has to stay in the instruction cache.
 // A masked and an unmasked form of the steps, and Q and the results in unrolled
@@ -36,6 +36,9 @@
 // tiles' chains stay half a step apart), eight unpacking warps with the registers
 // split by roles (96 us), pages asked into L2 ahead (no change), the waits' loop as
 // a function (96 us), Q's loads a step earlier (no change).
+//
+// The code stands apart from the prompt kernel's: as one template, that one's time
+// moved by up to 7 % either way.
 //
 // What it rounds: as the prompt kernel, each of K, V and P to fp16; with 64 channels
 // and fp16 output K is two numbers (kSeenExactK).

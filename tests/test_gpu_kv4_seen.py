@@ -341,3 +341,25 @@ def test_two_calls_at_once(dcc):  # noqa: F811
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for pair in got for i in range(2) for a, b in zip(pair[i], want[i]))
     assert dcc.dcc_local_check() == dcc.DCC_OK
+
+
+@pytest.mark.parametrize("news,share", [([5, 2], 2), ([40, 33], 8)])
+def test_layers(dcc, news, share):  # noqa: F811
+    """Each layer's own pages."""
+    g = torch.Generator().manual_seed(14)
+    lens = [300, 90]
+    cache, _, table = make_cache(dcc, g, 2, lens, 2, 64, 32, "fp16", layers=3)
+    start, mask = batch(news), S.pack([m for t in news for m in S.tree(g, t)], 2).cuda()
+    q = [torch.randn(sum(news), 2 * share, 64, generator=g).half().cuda() for _ in range(2)]
+    ws = cache.attention_workspace(2 * share)
+    for layer in range(3):
+        alone = dcc.Kv4Cache([p[layer:layer + 1] for p in cache.pools], cache.table, cache.lengths, None, 2, 64, 32, "fp16")
+        for tree in (True, False):
+            got, want = ([torch.empty_like(x) for x in q] for _ in range(2))
+            for c, out, at in ((cache, got, layer), (alone, want, 0)):
+                if tree:
+                    c.attention_tree(q, out, start, mask, max_new=max(news), workspace=ws, layer=at)
+                else:
+                    c.attention_sinks(q, out, start, max_new=max(news), workspace=ws, window=60, sinks=5, layer=at)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert dcc.dcc_local_check() == dcc.DCC_OK
