@@ -14,7 +14,7 @@
 // It is bound by latency, and a cluster's barrier with its fence costs more
 // than a CTA's: a fork of 64 beams out of 128 with its copies takes 19 us on
 // GB300 with one CTA (a host that issues slowly: up to 25), 27 with the cluster.  It writes the list of page copies to
-// the workspace.  The second kernel copies:
+// the workspace (a reservation's few copies it makes itself, book_copy).  The second kernel copies:
 // the number of copies is only known on the device, so its CTAs (as many as
 // the GPU holds) stride over (copy, rank, layer, chunk), 16 bytes a thread and
 // several loads in flight; it is bound by memory (GB300: 0.98 GB read and
@@ -36,13 +36,13 @@ constexpr int kCopyUnroll = 4;     // 16-byte vectors a thread has in flight
 
 // Workspace, int32 words: totals, then the copies and the lists.
 constexpr int kWsWords = 64;
-enum { kWsCopies = 0, kWsTotal = 8 /* + 8 j + CTA, j = 0..2 */, kWsFails = 40, kWsFreed = 41 };
+enum { kWsCopies = 0, kWsTotal = 8 /* + 8 j + CTA, j = 0..2 */, kWsFails = 40, kWsFreed = 41, kWsBack = 42 };
 struct PagesWs {
   int32_t* w;     // kWsWords
   int32_t* from;  // [pages]: page copied / moved
   int32_t* to;    // [pages]: page it goes to; also the list of free pages given out
-  int32_t* mark;  // [seqs]: which request named the sequence first
-  int32_t* pre;   // [seqs + 1]: pages wanted before request i
+  int32_t* mark;  // [seqs]: which request named the sequence first; of a reservation, what its copies go to
+  int32_t* pre;   // [seqs + 1]: pages wanted before request i, kOwnPage where one is for a copy
 };
 
 enum BookMode { kBookFree = 0, kBookFork = 1, kBookReserve = 2 };
@@ -52,6 +52,7 @@ struct BookArgs {
   int count;
   int32_t* info;
   PagesWs ws;
+  unsigned vecs;  // reserve: 16-byte vectors of one page in one layer
 };
 
 template <int CTAS>
@@ -125,8 +126,53 @@ __device__ __forceinline__ void list_free(const Kv4Dev& kv, Span my, int base, i
   }
 }
 
+// The partial last page of a sequence that is to grow, and how many own it.  Where others
+// do (the page was full when a fork shared it, and a part of the sequence's tokens has been
+// given up since, k_kv4_keep_book), the rest of it is not this sequence's to write: it
+// leaves the page for a copy.  In three steps of one load each, so that the kernel's other work comes between them
+// (GB300: a reservation of 64 sequences 6.1 us, 5.8 before it asked; one after the other 6.7).
+constexpr int kOwnPage = (int)0x80000000u;
+struct LastPage {
+  int len, p, owners;
+  __device__ __forceinline__ void lengths(const Kv4Dev& kv, const BookArgs& a, int i) {
+    const int add = i < kv.seqs ? a.dst[i] : 0, held = i < kv.seqs ? kv.len[i] : 0;
+    len = add > 0 ? held : 0;
+  }
+  __device__ __forceinline__ void page(const Kv4Dev& kv, int i) {  // (-1: whole, or no page of the pool's)
+    p = len > 0 && len % kKv4Page && len / kKv4Page < kv.max_pages ? kv.table[(size_t)i * kv.max_pages + len / kKv4Page] : -1;
+  }
+  __device__ __forceinline__ void count(const Kv4Dev& kv) { owners = p >= 0 && p < kv.pages ? ld_count(kv.refs + p) : 0; }
+};
+
+// The pages that reservations have left, copied for those that left them, by all of the
+// grid's warps: page by page, layer by layer.  Rare (see LastPage), so it has no
+// launch of its own, which every reservation would pay for (GB300: 2 pages of 128 blocks
+// of 9216 bytes take 68 us by one CTA, 64 1.5 ms; by the cluster of large pools 218 us).
+template <int CTAS>
+__device__ __noinline__ void book_copy(const Kv4Dev& kv, const BookArgs& a, int copies) {
+  constexpr int kUnroll = 8;  // vectors a lane has in flight
+  const int lane = threadIdx.x & 31, parts = kv.n * kv.layers;
+  const long long units = (long long)copies * parts;
+  for (long long u = ((long long)blockIdx.x * kBookThreads + threadIdx.x) >> 5; u < units; u += CTAS * kBookThreads / 32) {
+    const int i = (int)(u / parts), part = (int)(u % parts), rank = part / kv.layers, layer = part % kv.layers;
+    const int p = __ldcg(a.ws.from + i), q = __ldcg(a.ws.mark + i);
+    const uint4* src = reinterpret_cast<const uint4*>(kv.pool[rank]) + ((size_t)layer * kv.pages + p) * a.vecs;
+    uint4* dst = reinterpret_cast<uint4*>(kv.pool[rank]) + ((size_t)layer * kv.pages + q) * a.vecs;
+    for (unsigned v0 = lane; v0 < a.vecs; v0 += 32 * kUnroll) {
+      uint4 r[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (v0 + 32 * j < a.vecs) r[j] = __ldcs(src + v0 + 32 * j);
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (v0 + 32 * j < a.vecs) __stcs(dst + v0 + 32 * j, r[j]);
+    }
+  }
+}
+
 // Pages request i asks for: of a fork, one if src holds a partial page; of a
-// reservation, those its sequence lacks.  ok: the request can be served at all.
+// reservation, those its sequence lacks (without one for a copy).  ok: the request can
+// be served at all.
 __device__ __forceinline__ int book_want(const Kv4Dev& kv, const BookArgs& a, int mode, int i, bool* ok) {
   if (mode == kBookFork) {
     const int d = a.dst[i], s = a.src[i];
@@ -144,7 +190,7 @@ __device__ __forceinline__ int book_want(const Kv4Dev& kv, const BookArgs& a, in
 }
 
 template <int CTAS>
-__global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a, int mode) {
+__global__ void __launch_bounds__(kBookThreads) k_kv4_book(const __grid_constant__ Kv4Dev kv, const __grid_constant__ BookArgs a, int mode) {
   __shared__ int smem[32];
   pdl_prologue();
   const int cta = (int)blockIdx.x, tid = cta * kBookThreads + (int)threadIdx.x;
@@ -155,6 +201,8 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
   const int mp = kv.max_pages;
 
   for (int i = tid; i < kWsWords; i += kAll) ws.w[i] = 0;
+  LastPage last = {0, -1, 0};  // of the request that this thread looks at first
+  if (mode == kBookReserve) last.lengths(kv, a, (int)threadIdx.x);
   if (mode != kBookReserve) {
     for (int i = tid; i < kv.seqs; i += kAll) ws.mark[i] = 0x7fffffff;
     book_sync<CTAS>();
@@ -189,9 +237,18 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
 
   // free pages, by CTA
   const Span my = my_pages<CTAS>(kv.pages, cta);
-  int mine = 0;
-  for (int p = my.b + (int)threadIdx.x; p < my.e; p += kBookThreads) mine += ld_count(kv.refs + p) == 0;
+  int mine = 0, c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int p = my.b + (int)threadIdx.x + j * kBookThreads;
+    c[j] = p < my.e ? ld_count(kv.refs + p) : 1;
+  }
+  if (mode == kBookReserve) last.page(kv, (int)threadIdx.x);  // (under the counts' loads)
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mine += c[j] == 0;
+  for (int p = my.b + (int)threadIdx.x + 4 * kBookThreads; p < my.e; p += kBookThreads) mine += ld_count(kv.refs + p) == 0;
   mine = cta_sum(mine, smem);
+  if (mode == kBookReserve) last.count(kv);
   if (threadIdx.x == 0) ws.w[kWsTotal + cta] = mine;
   // pages wanted before each request: CTA 0, in 64 bits, capped (a request
   // past the cap is past any pool's end and fails)
@@ -200,11 +257,18 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
     long long base = 0;
     for (int i0 = 0; i0 < n_req; i0 += kBookThreads) {
       const int i = i0 + (int)threadIdx.x;
-      bool ok;
-      const long long want = i < n_req ? book_want(kv, a, mode, i, &ok) : 0;
+      bool ok = false;
+      long long want = i < n_req ? book_want(kv, a, mode, i, &ok) : 0;
+      if (mode == kBookReserve && i0 > 0) {
+        last.lengths(kv, a, i);
+        last.page(kv, i);
+        last.count(kv);
+      }
+      const bool leaves = ok && last.owners > 1;
+      want += leaves;
       long long total;
       const long long at = base + cta_scan(want, &total, smem64);
-      if (i < n_req) ws.pre[i] = (int)(at < kCap ? at : kCap);
+      if (i < n_req) ws.pre[i] = (int)(at < kCap ? at : kCap) | (leaves ? kOwnPage : 0);
       base += total;
     }
     if (threadIdx.x == 0) ws.pre[n_req] = (int)(base < kCap ? base : kCap);
@@ -229,11 +293,12 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
   book_sync<CTAS>();
 
   // serve the requests: one warp each
-  int fails = 0, given = 0;
+  int fails = 0, given = 0, back = 0;
   for (int i = tid >> 5; i < n_req; i += kAll / 32) {
     const int lane = threadIdx.x & 31;
     bool ok;
-    const int want = book_want(kv, a, mode, i, &ok), at = __ldcg(ws.pre + i);
+    const int word = __ldcg(ws.pre + i), at = word & ~kOwnPage, leaves = word < 0;
+    const int want = book_want(kv, a, mode, i, &ok) + leaves;
     __syncwarp();  // every lane has read the length that lane 0 changes below
     if (mode == kBookFork && (a.src[i] < 0 || a.src[i] >= kv.seqs)) book_bad(kv, a.src[i]);
     if (!ok || (want && at + want > nfree)) {
@@ -264,33 +329,44 @@ __global__ void __launch_bounds__(kBookThreads) k_kv4_book(Kv4Dev kv, BookArgs a
         kv.len[d] = len;
       }
     } else if (a.dst[i] > 0) {
-      const int len = kv.len[i], held = (len + kKv4Page - 1) / kKv4Page;
+      const int len = kv.len[i], first = (len + kKv4Page - 1) / kKv4Page - leaves;
       int32_t* row = kv.table + (size_t)i * mp;
+      const int p = leaves ? row[first] : 0;
+      __syncwarp();
       for (int j = lane; j < want; j += 32) {
         const int q = __ldcg(ws.to + at + j);
-        row[held + j] = q;
+        row[first + j] = q;
         kv.refs[q] = 1;
       }
       __syncwarp();
       if (lane == 0) {
         kv.len[i] = len + a.dst[i];
         given += want;
+        if (leaves) {
+          back += atomicSub(kv.refs + p, 1) == 1;  // (given out again by later calls only)
+          const int c = atomicAdd(&ws.w[kWsCopies], 1);
+          ws.from[c] = p;
+          ws.mark[c] = __ldcg(ws.to + at);
+        }
       }
     }
   }
   if (fails) atomicAdd(&ws.w[kWsFails], fails);
   if (given) atomicAdd(&ws.w[kWsFreed], given);
+  if (back) atomicAdd(&ws.w[kWsBack], back);
   // forks are served in order of their place in the list, so the copies are its first entries
   book_sync<CTAS>();
+  const int copies = __ldcg(ws.w + kWsCopies);
   if (tid == 0) {
-    const int g = __ldcg(ws.w + kWsFreed);
-    ws.w[kWsCopies] = mode == kBookFork ? g : 0;
+    const int g = __ldcg(ws.w + kWsFreed), b = __ldcg(ws.w + kWsBack), f = __ldcg(ws.w + kWsFails);
+    if (mode == kBookFork) ws.w[kWsCopies] = g;
     if (a.info) {
-      a.info[0] = nfree - g;
-      a.info[1] = __ldcg(ws.w + kWsFails);
+      a.info[0] = nfree - g + b;
+      a.info[1] = f;
       a.info[2] = g;
     }
   }
+  if (mode == kBookReserve && copies) book_copy<CTAS>(kv, a, copies);
 }
 
 struct CompactArgs {
@@ -689,6 +765,7 @@ int book_call(const dcc_kv4_t* kv, int mode, const int32_t* src, const int32_t* 
   a.dst = dst;
   a.count = (int)count;
   a.info = info;
+  a.vecs = (unsigned)((size_t)kv->kv_heads * dcc::kv4_block_bytes(kv->head_dim, kv->group) / 16);
   if ((rc = dcc_host::kv4_ready(&d)) != DCC_OK) return rc;
   void* args[] = {&d, &a, &mode};
   const long long rows = mode == dcc::kBookReserve ? 0 : (long long)count * kv->max_pages;

@@ -652,10 +652,13 @@ int dcc_kv4_attention_tree(const dcc_kv4_t* kv, int layer, void* const* q, void*
 int dcc_kv4_pages_workspace(const dcc_kv4_t* kv, size_t* bytes);
 
 /* Let sequence s hold add[s] more tokens (device, seqs; add[s] <= 0: none):
- * len[s] grows and new pages join its row.  A sequence whose pages are no
+ * len[s] grows and new pages join its row.  Where its last page is partial and
+ * others own it too (shared by a fork while it was full, a part of its tokens given
+ * up by dcc_kv4_keep since), the sequence leaves it for a copy of its own (all
+ * layers, all ranks), as a fork's.  A sequence whose pages are no
  * longer there, or whose row is too short, keeps its length, and so does
  * every later one that needs a page once the pool has run out.  info: free
- * pages left, sequences not served, pages given. */
+ * pages left, sequences not served, pages given (copies among them). */
 int dcc_kv4_reserve(const dcc_kv4_t* kv, const int32_t* add, int32_t* info, void* workspace, size_t workspace_bytes,
                     dcc_stream_t s);
 
@@ -684,7 +687,8 @@ int dcc_kv4_fork(const dcc_kv4_t* kv, const int32_t* src, const int32_t* dst, si
  * sequence is left as it is where count[s] is not in 0 .. its drafted tokens, the
  * path does not ascend within them, it has more drafted tokens than tokens, or a
  * row would move into a page that another sequence shares (a path that begins 0,
- * 1, 2 .. moves nothing up to there).  info: free pages left, sequences left as
+ * 1, 2 .. moves nothing up to there; a length that ends in such a page grows on in
+ * one of its own, see dcc_kv4_reserve).  info: free pages left, sequences left as
  * they are, tokens moved. */
 int dcc_kv4_keep(const dcc_kv4_t* kv, const int32_t* start, const int32_t* path, size_t tokens, const int32_t* count,
                  int32_t* info, void* workspace, size_t workspace_bytes, dcc_stream_t s);
