@@ -66,9 +66,13 @@ int attention_call(const dcc_kv4_t* kv, int layer, void* const* q, void* const* 
       window < 0 || sinks < 0 || !(scale - scale == 0.0f))
     return DCC_ERR_INVALID_ARG;
   if (q_heads % kv->kv_heads || q_heads / kv->kv_heads > 128) return DCC_ERR_INVALID_ARG;
-  size_t need = 0;
-  rc = dcc_kv4_attention_workspace(kv, q_heads, &need);
-  if (rc != DCC_OK) return rc;
+  // positions stay below 2^30 (kv4_view), so a window that long hides nothing;
+  // kept, position - window + 1 would leave 32 bits for rows before position zero
+  if (window >= 1 << 30) window = 0;
+  if (window == 0) sinks = 0;
+  const bool seen = tree || sinks > 0;  // else causal rows, one run of keys each
+  size_t need = dcc::dec_ws_bytes();
+  if (seen && (rc = dcc_kv4_attention_workspace(kv, q_heads, &need)) != DCC_OK) return rc;
   if (workspace_bytes < need) return DCC_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(start) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 15u) || q_stride % 8)
     return DCC_ERR_MISALIGNED;
@@ -115,13 +119,10 @@ int attention_call(const dcc_kv4_t* kv, int layer, void* const* q, void* const* 
   a.layer = layer;
   a.q_heads = q_heads;
   a.max_new = max_new;
-  // positions stay below 2^30 (kv4_view), so a window that long hides nothing;
-  // kept, position - window + 1 would leave 32 bits for rows before position zero
-  a.window = window < (1 << 30) ? window : 0;
-  a.sinks = a.window ? (sinks < (1 << 30) ? sinks : 1 << 30) : 0;
+  a.window = window;
+  a.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
   a.mask = mask;
   a.words = words;
-  const bool seen = tree || a.sinks > 0;  // else causal rows, one run of keys each
   a.scale = scale;
   a.share = q_heads / kv->kv_heads;
   a.ws = static_cast<char*>(workspace);

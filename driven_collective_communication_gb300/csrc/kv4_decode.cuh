@@ -108,6 +108,7 @@ constexpr int kDecMaxSlot = dec_slot(16, 128) > dec_slot(24, 64) ? dec_slot(16, 
 __host__ __device__ constexpr size_t dec_ws_bytes() {
   return 1024 + (size_t)kDecMaxCtas * (2 + kDecMaxWarps) * kDecMaxSlot * 4;
 }
+static_assert(dec_ws_bytes() == DCC_KV4_ATTENTION_BYTES, "what dcc.h says");
 
 // Warps and stages: as many bytes in flight as shared memory holds, three
 // warps to a scheduler where a tile's registers allow (8 rows), two otherwise.

@@ -56,6 +56,7 @@ ALGO_CODES = {"auto": DCC_ALGO_AUTO, "one_shot": DCC_ALGO_ONE_SHOT, "two_shot": 
               "two_shot_scratch": DCC_ALGO_TWO_SHOT_SCRATCH, "two_shot_bulk": DCC_ALGO_TWO_SHOT_BULK,
               "one_shot_ll": DCC_ALGO_ONE_SHOT_LL}
 DCC_KV4_PAGE = 64
+DCC_KV4_ATTENTION_BYTES = 19211264  # what dcc_kv4_attention alone needs of a workspace
 DCC_TREE_MAX = 1024
 DCC_TOP_MAX = 64
 ACT_CODES = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}

@@ -610,7 +610,9 @@ int dcc_kv4_read(const dcc_kv4_t* kv, int layer, void* const* k, void* const* v,
  * K or V of a bf16 cache beyond 2^96 may overflow the fp32 sums.
  * workspace: dcc_kv4_attention_workspace bytes, 16-byte aligned, filled with
  * zeros once before its first use (calls leave its counters at zero); calls
- * that may run at the same time need one each. */
+ * that may run at the same time need one each.  One size serves the three attention
+ * calls; a program that calls this one only needs DCC_KV4_ATTENTION_BYTES. */
+#define DCC_KV4_ATTENTION_BYTES 19211264
 int dcc_kv4_attention(const dcc_kv4_t* kv, int layer, void* const* q, void* const* out, float* const* lse, int q_heads,
                       size_t tokens, size_t q_stride, const int32_t* start, int max_new, float scale, int window,
                       void* workspace, size_t workspace_bytes, dcc_stream_t s);
