@@ -145,13 +145,14 @@ template <typename T, int D>
 constexpr bool kSeenExactK = std::is_same<T, __half>::value && D == 64;
 template <typename T, int D, int G>
 constexpr size_t kSeenSmem = PromptShape<D, G>::smem + (kSeenExactK<T, D> ? 2 * PromptShape<D, G>::kv_tile : 0);
-// lo + step * code, biased codes as Pair16, as a number and what its rounding left
+// lo + step * code, biased codes as Pair16, as a number and what its rounding left: both
+// parts of that are exact, their sum is rounded, 2^-22 of |step code| + |value|
 __device__ __forceinline__ void value_exact(uint32_t c, uint32_t step, uint32_t lo, uint32_t* big, uint32_t* small) {
   const uint32_t bias = 0x54005400u;
   auto h = [](const uint32_t& w) { return *reinterpret_cast<const __half2*>(&w); };
   const __half2 n = __hsub2(h(c), h(bias)), p = __hmul2(n, h(step)), q = __hfma2(n, h(step), __hneg2(p));  // p + q, exactly
   const __half2 s = __hadd2(p, h(lo)), b = __hsub2(s, p);
-  const __half2 r = __hadd2(q, __hadd2(__hsub2(p, __hsub2(s, b)), __hsub2(h(lo), b)));  // the sum's error, exactly, and q
+  const __half2 r = __hadd2(q, __hadd2(__hsub2(p, __hsub2(s, b)), __hsub2(h(lo), b)));  // the product's error, and the sum's
   *big = *reinterpret_cast<const uint32_t*>(&s);
   *small = *reinterpret_cast<const uint32_t*>(&r);
 }
@@ -490,19 +491,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_seen(Kv4Dev kv, const
                 const uint32_t c = reinterpret_cast<const uint32_t*>(src)[i >> 2] >> (4 * (i & 3));
                 const uint32_t pw = par[key * NG + 8 * u / G];
                 const float2 f = Half16<T>::widen2(pw);
-                const uint32_t pair = (bad | param_bad<T>(pw)) & kBad
-                                          ? 0xffffffffu  // NaN
-                                          : narrow_finite<T>(fmaf((float)(c & 15u), f.x, f.y),
-                                                             fmaf((float)((c >> 16) & 15u), f.x, f.y));
+                const float2 v = make_float2(fmaf((float)(c & 15u), f.x, f.y), fmaf((float)((c >> 16) & 15u), f.x, f.y));
+                const uint32_t pair = (bad | param_bad<T>(pw)) & kBad ? 0xffffffffu /* NaN */ : narrow_finite<T>(v.x, v.y);
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (uint32_t)(u / 8) * 16384u +
                                                              (uint32_t)(((u % 8) ^ (key & 7)) * 16 + 4 * (i & 3))),
                              "r"(pair)
                              : "memory");
-                if constexpr (EXACT)
+                if constexpr (EXACT) {
+                  // what the first number left: at most 16, or 32 of a last code an ulp past
+                  // the type's largest number; nothing of a NaN, or of a value further out
+                  const float2 b = Half16<T>::widen2(pair), r = make_float2(v.x - b.x, v.y - b.y);
                   asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (sk2 - sk) + (uint32_t)(u / 8) * 16384u +
                                                                (uint32_t)(((u % 8) ^ (key & 7)) * 16 + 4 * (i & 3))),
-                               "r"(0u)
+                               "r"(Half16<T>::narrow2(fabsf(r.x) <= 32.0f ? r.x : 0.0f, fabsf(r.y) <= 32.0f ? r.y : 0.0f))
                                : "memory");
+                }
               }
               continue;
             }

@@ -637,8 +637,14 @@ int dcc_kv4_attention_sinks(const dcc_kv4_t* kv, int layer, void* const* q, void
  * drafted tokens sees the last max(0, window - c) positions of the context and
  * its first `sinks`: what a sequential pass over its branch sees, for branches
  * up to the window's length.  A row that sees nothing gives zeros and lse
- * -infinity.  (In these two calls the keys of fp16 caches of 64 channels enter the
- * scores exactly.) */
+ * -infinity.
+ * What these two calls round is as above, but they go over to K, V and p in 16 bits
+ * earlier: rows of one kv head (max_new * q_heads / kv_heads) up to 16 (24 with 64
+ * channels) keep exact codes, from there to 32 (48) it depends on the work, above that
+ * they never do.  Then the keys of fp16 caches of 64 channels enter the scores as two
+ * fp16 numbers, less than 2^-20 of their group's largest magnitude off (or 2^-24 where
+ * that is more).  dcc_kv4_attention_sinks with window 0 or sinks 0 is
+ * dcc_kv4_attention in all of this. */
 #define DCC_TREE_MAX 1024
 int dcc_kv4_attention_tree(const dcc_kv4_t* kv, int layer, void* const* q, void* const* out, float* const* lse,
                            int q_heads, size_t tokens, size_t q_stride, const int32_t* start, int max_new,
