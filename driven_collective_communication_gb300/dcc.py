@@ -696,6 +696,8 @@ def dcc_token_logprobs(logits, target, logprob, workspace, entropy=None, top_ids
         raise ValueError("logits: (tokens, columns) a rank")
     tokens, columns = logits.shape
     top = 0 if top_ids is None else top_ids.shape[-1]
+    if (0 if top_logprobs is None else top_logprobs.shape[-1]) != top:
+        raise ValueError("top_ids and top_logprobs: both, of one shape, or neither")
     ids, lps = (_vector(top_ids, torch.int32, (tokens, top), "top_ids"),
                 _vector(top_logprobs, torch.float32, (tokens, top), "top_logprobs")) if top else (None, None)
     return _check(_lib.dcc_token_logprobs(len(logits), logits.ptrs, tokens, columns, logits.stride,
