@@ -82,7 +82,7 @@ int attention_call(const dcc_kv4_t* kv, int layer, void* const* q, void* const* 
   if (tokens * (size_t)(q_heads / kv->kv_heads) > (size_t)1 << 30) return DCC_ERR_INVALID_ARG;  // rows are 32-bit
   if (tree) {
     // a row's words hold all of its sequence's drafted tokens that rows of this call stand for
-    if (!mask || words < 1 || words > dcc::kTreeWords) return DCC_ERR_INVALID_ARG;
+    if ((!mask && tokens) || words < 1 || words > dcc::kTreeWords) return DCC_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(mask) & 3u) return DCC_ERR_MISALIGNED;
     if (((size_t)max_new < tokens ? (size_t)max_new : tokens) > (size_t)words * 32) return DCC_ERR_INVALID_ARG;
   }

@@ -568,8 +568,9 @@ int dcc_token_logprobs(int n_ranks, const void* const* logits, size_t tokens, si
   if (t != DCC_FP32 && t != DCC_FP16 && t != DCC_BF16) return DCC_ERR_UNSUPPORTED;
   if (!logits || !workspace || workspace_bytes < need || !(scale > 0.0f) || !(scale - scale == 0.0f))
     return DCC_ERR_INVALID_ARG;
-  if ((logprob != nullptr) != (target != nullptr) || (top > 0 && (!top_ids || !top_logprob)) ||
-      (top == 0 && (top_ids || top_logprob)) || (!logprob && !entropy && top == 0))
+  if (tokens &&  // (empty buffers have no address)
+      ((logprob != nullptr) != (target != nullptr) || (top > 0 && (!top_ids || !top_logprob)) ||
+       (top == 0 && (top_ids || top_logprob)) || (!logprob && !entropy && top == 0)))
     return DCC_ERR_INVALID_ARG;
   if (tokens > (size_t)1 << 24 || columns > (size_t)1 << 27 || stride > (size_t)1 << 32 || (tokens > 1 && stride < columns) ||
       columns * n_ranks > (size_t)1 << 30 || vocab < 1 || vocab > columns * n_ranks || (size_t)top > vocab)

@@ -3,8 +3,9 @@ given: what returns before anything is launched (no GPU needed)."""
 import pytest
 import torch
 
-from test_ops_arguments import dcc  # noqa: F401  (dcc: the fixture)
+from test_ops_arguments import dcc, desc  # noqa: F401  (dcc: the fixture)
 from test_ops_binding import bf16, dev  # noqa: F401
+from test_seen_arguments import lp, tree
 
 
 def f32(*shape):
@@ -22,3 +23,22 @@ def test_half_of_the_alternatives(dcc):  # noqa: F811
                  dict(top_ids=i32(4, 2), top_logprobs=f32(4, 0))):
         with pytest.raises(ValueError):
             dcc.dcc_token_logprobs(**a, **half)
+
+
+def test_trees_of_no_tokens(dcc):  # noqa: F811
+    """An empty batch has an empty mask, which has no address."""
+    assert tree(dcc, desc(dcc), tokens=0, mask=None) == dcc.DCC_OK
+    assert tree(dcc, desc(dcc), tokens=0, mask=None, words=0) == dcc.DCC_ERR_INVALID_ARG
+    assert tree(dcc, desc(dcc), tokens=1, max_new=1, mask=None) == dcc.DCC_ERR_INVALID_ARG
+
+
+def test_log_probabilities_of_no_tokens(dcc):  # noqa: F811
+    none = dict(target=None, logprob=None, entropy=None, ids=None, tops=None)
+    assert lp(dcc, tokens=0, **none) == dcc.DCC_OK
+    assert lp(dcc, tokens=0, top=0, **none) == dcc.DCC_OK
+    assert lp(dcc, tokens=0, top=65, **none) == dcc.DCC_ERR_INVALID_ARG
+    assert lp(dcc, tokens=0, ws=None, **none) == dcc.DCC_ERR_INVALID_ARG
+    ws = torch.zeros((1 << 20) + 16, dtype=torch.uint8)
+    ws = dev(ws[-ws.data_ptr() % 16:])  # (as the GPU's allocations are)
+    dcc.dcc_token_logprobs([bf16(0, 8)] * 2, i32(0), f32(0), ws)
+    dcc.dcc_token_logprobs([bf16(0, 8)] * 2, i32(0), f32(0), ws, entropy=f32(0), top_ids=i32(0, 3), top_logprobs=f32(0, 3))
