@@ -1,5 +1,5 @@
-"""Calls for drafted tokens and log probabilities whose buffers are empty or half
-given: what returns before anything is launched (no GPU needed)."""
+"""Calls for drafted tokens and log probabilities whose buffers are empty, half
+given or out of range: what returns before anything is launched (no GPU needed)."""
 import pytest
 import torch
 
@@ -40,5 +40,6 @@ def test_log_probabilities_of_no_tokens(dcc):  # noqa: F811
     assert lp(dcc, tokens=0, ws=None, **none) == dcc.DCC_ERR_INVALID_ARG
     ws = torch.zeros((1 << 20) + 16, dtype=torch.uint8)
     ws = dev(ws[-ws.data_ptr() % 16:])  # (as the GPU's allocations are)
-    dcc.dcc_token_logprobs([bf16(0, 8)] * 2, i32(0), f32(0), ws)
-    dcc.dcc_token_logprobs([bf16(0, 8)] * 2, i32(0), f32(0), ws, entropy=f32(0), top_ids=i32(0, 3), top_logprobs=f32(0, 3))
+    dcc.dcc_token_logprobs([bf16(0, 8)] * 2, i32(0), f32(0), ws, stream=0)
+    dcc.dcc_token_logprobs([bf16(0, 8)] * 2, i32(0), f32(0), ws, entropy=f32(0), top_ids=i32(0, 3), top_logprobs=f32(0, 3),
+                           stream=0)
