@@ -31,6 +31,8 @@
 // one a batch.  CTAs of 128 threads, seven to an SM: 256 threads with about the
 // same registers took 213 us (more warps wait at a barrier), 64 threads 208, and
 // 64 registers a thread, which spill, 243 (the first case with 20).
+#include <cfloat>
+
 #include "comm.h"
 #include "kv4.cuh"
 #include "tcgen05.cuh"
@@ -566,7 +568,8 @@ int dcc_token_logprobs(int n_ranks, const void* const* logits, size_t tokens, si
   int rc = dcc_token_logprobs_workspace(n_ranks, tokens, columns, top, &need);
   if (rc != DCC_OK) return rc;
   if (t != DCC_FP32 && t != DCC_FP16 && t != DCC_BF16) return DCC_ERR_UNSUPPORTED;
-  if (!logits || !workspace || workspace_bytes < need || !(scale > 0.0f) || !(scale - scale == 0.0f))
+  // the kernel's exponentials take scale log2 e, in fp32
+  if (!logits || !workspace || workspace_bytes < need || !(scale > 0.0f) || !(scale * 1.44269504088896341f <= FLT_MAX))
     return DCC_ERR_INVALID_ARG;
   if (tokens &&  // (empty buffers have no address)
       ((logprob != nullptr) != (target != nullptr) || (top > 0 && (!top_ids || !top_logprob)) ||

@@ -742,7 +742,7 @@ int dcc_linear(int n_ranks, void* const* weight, void* const* x, void* const* bi
  *                                  likely first, equal logits by token number; tokens * top each
  * in fp32, the same on every run.  A logit of -infinity is a token that cannot
  * come.  A row that holds a NaN or +infinity, or nothing but -infinity, gives NaN
- * and ids -1.  scale above 0.  fp32 / fp16 / bf16.  workspace:
+ * and ids -1.  scale above 0, and its product with log2 e in fp32's range.  fp32 / fp16 / bf16.  workspace:
  * dcc_token_logprobs_workspace bytes, 16-byte aligned, filled with zeros once
  * before its first use (calls leave its counters at zero, whatever their sizes);
  * calls that may run at the same time need one each. */

@@ -43,3 +43,8 @@ def test_log_probabilities_of_no_tokens(dcc):  # noqa: F811
     dcc.dcc_token_logprobs([bf16(0, 8)] * 2, i32(0), f32(0), ws, stream=0)
     dcc.dcc_token_logprobs([bf16(0, 8)] * 2, i32(0), f32(0), ws, entropy=f32(0), top_ids=i32(0, 3), top_logprobs=f32(0, 3),
                            stream=0)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3e38, 3.4028234e38])
+def test_scales_whose_product_with_log2_e_is_infinite(dcc, scale):  # noqa: F811
+    assert lp(dcc, scale=scale) == dcc.DCC_ERR_INVALID_ARG
