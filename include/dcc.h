@@ -740,7 +740,8 @@ int dcc_linear(int n_ranks, void* const* weight, void* const* x, void* const* bi
  *   entropy = -sum p ln p          NULL: not wanted
  *   top_ids, top_logprob           the `top` most likely tokens (0 .. DCC_TOP_MAX, at most vocab; 0: NULL), most
  *                                  likely first, equal logits by token number; tokens * top each
- * in fp32, the same on every run.  A logit of -infinity is a token that cannot
+ * in fp32, the same on every run (of a row scored in batches of other sizes, the
+ * ids; the sums may differ in their last bits).  A logit of -infinity is a token that cannot
  * come.  A row that holds a NaN or +infinity, or nothing but -infinity, gives NaN
  * and ids -1.  scale above 0, and its product with log2 e in fp32's range.  fp32 / fp16 / bf16.  workspace:
  * dcc_token_logprobs_workspace bytes, 16-byte aligned, filled with zeros once
